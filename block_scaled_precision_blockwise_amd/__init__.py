@@ -34,10 +34,15 @@ __all__ = [
     "bsq_mxfp8_backward_workspace_bytes", "bsq_mxfp8_backward",
     "mxfp8_backward_operand_shapes", "bsq_mxfp8_backward_quantize", "bsq_mxfp8_backward_gemms",
     "bsq_nvfp4_workspace_bytes", "bsq_scaled_matmul_nvfp4",
+    "BSQ_SOFTMAX", "BSQ_SIGMOID", "bsq_moe_route", "bsq_moe_route_backward",
+    "bsq_moe_capacity", "bsq_moe_plan_workspace_bytes", "bsq_moe_plan", "bsq_moe_gather_mx",
+    "bsq_moe_combine", "bsq_moe_combine_backward", "bsq_moe_matmul", "bsq_moe_wgrad",
+    "bsq_swiglu_mx", "bsq_swiglu_mx_backward",
     "BsqError",
 ]
 
 BSQ_F32, BSQ_BF16, BSQ_E4M3, BSQ_E5M2, BSQ_E8M0, BSQ_I8, BSQ_I32 = range(7)
+BSQ_SOFTMAX, BSQ_SIGMOID = range(2)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbsq.so")
@@ -48,6 +53,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 _SIGNATURES = {
     "bsq_version": (ctypes.c_char_p, []),
     "bsq_status_string": (ctypes.c_char_p, [_INT]),
@@ -75,6 +81,20 @@ _SIGNATURES = {
                                         _P, _P]),
     "bsq_nvfp4_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "bsq_scaled_matmul_nvfp4": (_INT, [_I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
+    "bsq_moe_route": (_INT, [_I64, _I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _INT, _INT, _F32, _P, _P, _P,
+                             _P]),
+    "bsq_moe_route_backward": (_INT, [_I64, _I64, _I64, _P, _INT, _INT, _INT, _F32, _P, _P, _P, _P, _P]),
+    "bsq_moe_capacity": (_I64, [_I64, _I64, _I64]),
+    "bsq_moe_plan_workspace_bytes": (_SZ, [_I64, _I64]),
+    "bsq_moe_plan": (_INT, [_I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bsq_moe_gather_mx": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _P, _P]),
+    "bsq_moe_combine": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P]),
+    "bsq_moe_combine_backward": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P]),
+    "bsq_moe_matmul": (_INT, [_I64, _I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _P, _INT,
+                              _P]),
+    "bsq_moe_wgrad": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _INT, _P]),
+    "bsq_swiglu_mx": (_INT, [_I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _P, _P, _P]),
+    "bsq_swiglu_mx_backward": (_INT, [_I64, _I64, _P, _INT, _P, _P, _INT, _P, _P]),
 }
 
 
@@ -529,3 +549,248 @@ def bsq_scaled_matmul_nvfp4(lhs, rhs, lhs_scales, rhs_scales, out, workspace, st
     _raise(lib().bsq_scaled_matmul_nvfp4(B, M, N, K, _ptr(lhs), _ptr(rhs), _ptr(lhs_scales), _ptr(rhs_scales),
                                          _ptr(out), od, _ptr(workspace), nbytes, _stream(stream)),
            "bsq_scaled_matmul_nvfp4")
+
+
+# ------------------------------------------------------ expert layers ----
+
+def _wide(t, name):
+    torch = _torch()
+    code = {torch.float32: BSQ_F32, torch.bfloat16: BSQ_BF16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _rank(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+
+
+def _blocks(codes, scales, shape, name, optional=False):
+    """Checks codes of `shape` and their scales, one per 32 along the last axis."""
+    if codes is None and scales is None and optional:
+        return
+    if codes is None or scales is None:
+        raise ValueError(f"{name} needs both codes and scales")
+    _bytes1(codes, name)
+    _bytes1(scales, name + " scales")
+    _expect(codes, codes.dtype, shape, name)
+    _expect(scales, scales.dtype, (*shape[:-1], shape[-1] // 32), name + " scales")
+
+
+def _one_code(code_dtype, *codes):
+    """The format of all the codes given: `code_dtype`, or what their dtypes say."""
+    if code_dtype is not None:
+        return code_dtype
+    kinds = {_fp8_code(c) for c in codes if c is not None}
+    if len(kinds) > 1:
+        raise TypeError("all codes of a call must have one format")
+    return kinds.pop() if kinds else BSQ_E4M3
+
+
+def bsq_moe_route(logits, ids, weights, bias=None, scores=None, groups: int = 1, top_groups: int = 1,
+                  group_top: int = 1, score: int = BSQ_SOFTMAX, renorm: bool = True, scale: float = 1.0,
+                  stream=None):
+    """Routing: logits [T, E] f32 or bf16 -> ids i32 [T, k], weights f32
+    [T, k], and, where given, all scores f32 [T, E]; bias f32 [E] steers the
+    choice only."""
+    torch = _torch()
+    _dev(logits, ids, weights, bias, scores)
+    _rank(logits, 2, "logits")
+    _rank(ids, 2, "ids")
+    T, E = logits.shape
+    k = ids.shape[1]
+    ld = _wide(logits, "logits")
+    _expect(ids, torch.int32, (T, k), "ids")
+    _expect(weights, torch.float32, (T, k), "weights")
+    if bias is not None:
+        _expect(bias, torch.float32, (E,), "bias")
+    if scores is not None:
+        _expect(scores, torch.float32, (T, E), "scores")
+    _raise(lib().bsq_moe_route(T, E, k, groups, top_groups, group_top, _ptr(logits), ld, _ptr(bias), score,
+                               int(renorm), scale, _ptr(ids), _ptr(weights), _ptr(scores), _stream(stream)),
+           "bsq_moe_route")
+
+
+def bsq_moe_route_backward(logits, ids, dweights, dlogits, dscores=None, score: int = BSQ_SOFTMAX,
+                           renorm: bool = True, scale: float = 1.0, stream=None):
+    """dlogits [T, E] (logits' dtype) from dweights f32 [T, k] and, where
+    given, dscores f32 [T, E]; ids are bsq_moe_route's."""
+    torch = _torch()
+    _dev(logits, ids, dweights, dlogits, dscores)
+    _rank(logits, 2, "logits")
+    _rank(ids, 2, "ids")
+    T, E = logits.shape
+    k = ids.shape[1]
+    ld = _wide(logits, "logits")
+    _expect(ids, torch.int32, (T, k), "ids")
+    _expect(dweights, torch.float32, (T, k), "dweights")
+    _expect(dlogits, logits.dtype, (T, E), "dlogits")
+    if dscores is not None:
+        _expect(dscores, torch.float32, (T, E), "dscores")
+    _raise(lib().bsq_moe_route_backward(T, E, k, _ptr(logits), ld, score, int(renorm), scale, _ptr(ids),
+                                        _ptr(dweights), _ptr(dscores), _ptr(dlogits), _stream(stream)),
+           "bsq_moe_route_backward")
+
+
+def bsq_moe_capacity(n: int, E: int, align: int = 1) -> int:
+    """Rows that n choices over E experts take at most."""
+    return int(lib().bsq_moe_capacity(n, E, align))
+
+
+def bsq_moe_plan_workspace_bytes(n: int, E: int) -> int:
+    return int(lib().bsq_moe_plan_workspace_bytes(n, E))
+
+
+def bsq_moe_plan(ids, offsets, counts, rows, pos, workspace, align: int = 1, stream=None):
+    """The order of rows: ids i32 (any shape, n choices) -> offsets i32
+    [E + 1], counts i32 [E], rows i32 [cap], pos i32 shaped as ids."""
+    torch = _torch()
+    _dev(ids, offsets, counts, rows, pos, workspace)
+    _rank(counts, 1, "counts")
+    _rank(rows, 1, "rows")
+    E, cap = counts.shape[0], rows.shape[0]
+    _expect(ids, torch.int32, ids.shape, "ids")
+    _expect(offsets, torch.int32, (E + 1,), "offsets")
+    _expect(counts, torch.int32, (E,), "counts")
+    _expect(rows, torch.int32, (cap,), "rows")
+    _expect(pos, torch.int32, ids.shape, "pos")
+    nbytes = workspace.numel() * workspace.element_size()
+    _raise(lib().bsq_moe_plan(ids.numel(), E, align, cap, _ptr(ids), _ptr(offsets), _ptr(counts), _ptr(rows),
+                              _ptr(pos), _ptr(workspace), nbytes, _stream(stream)), "bsq_moe_plan")
+
+
+def bsq_moe_gather_mx(x, rows, k: int, codes=None, scales=None, codes_t=None, scales_t=None, weights=None,
+                      code_dtype: Optional[int] = None, stream=None):
+    """x [T, H] f32 or bf16 in the order of rows (i32 [cap]) as 8-bit
+    operands: codes [cap, H] + scales [cap, H/32] and / or codes_t [H, cap] +
+    scales_t [H, cap/32]; weights f32 [T, k] multiplies each row."""
+    torch = _torch()
+    _dev(x, rows, codes, scales, codes_t, scales_t, weights)
+    _rank(x, 2, "x")
+    _rank(rows, 1, "rows")
+    T, H = x.shape
+    cap = rows.shape[0]
+    xd = _wide(x, "x")
+    _expect(rows, torch.int32, (cap,), "rows")
+    _blocks(codes, scales, (cap, H), "codes", optional=True)
+    _blocks(codes_t, scales_t, (H, cap), "codes_t", optional=True)
+    if weights is not None:
+        _expect(weights, torch.float32, (T, k), "weights")
+    _raise(lib().bsq_moe_gather_mx(T, H, cap, k, _ptr(x), xd, _ptr(rows), _ptr(weights),
+                                   _one_code(code_dtype, codes, codes_t), _ptr(codes), _ptr(scales), _ptr(codes_t),
+                                   _ptr(scales_t), _stream(stream)), "bsq_moe_gather_mx")
+
+
+def bsq_moe_combine(y, pos, out, weights=None, stream=None):
+    """out [T, H] = sum over j of weights[t, j] y[pos[t, j]]; y [cap, H] and
+    out f32 or bf16, pos i32 [T, k], weights f32 [T, k] or None (ones)."""
+    torch = _torch()
+    _dev(y, pos, out, weights)
+    _rank(y, 2, "y")
+    _rank(pos, 2, "pos")
+    cap, H = y.shape
+    T, k = pos.shape
+    yd = _wide(y, "y")
+    _expect(pos, torch.int32, (T, k), "pos")
+    _expect(out, y.dtype, (T, H), "out")
+    if weights is not None:
+        _expect(weights, torch.float32, (T, k), "weights")
+    _raise(lib().bsq_moe_combine(T, H, cap, k, _ptr(y), yd, _ptr(pos), _ptr(weights), _ptr(out), _stream(stream)),
+           "bsq_moe_combine")
+
+
+def bsq_moe_combine_backward(y, pos, dout, dweights, stream=None):
+    """dweights f32 [T, k] = y[pos[t, j]] . dout[t]; y [cap, H] and dout
+    [T, H] of one dtype (f32 or bf16)."""
+    torch = _torch()
+    _dev(y, pos, dout, dweights)
+    _rank(y, 2, "y")
+    _rank(pos, 2, "pos")
+    cap, H = y.shape
+    T, k = pos.shape
+    yd = _wide(y, "y")
+    _expect(pos, torch.int32, (T, k), "pos")
+    _expect(dout, y.dtype, (T, H), "dout")
+    _expect(dweights, torch.float32, (T, k), "dweights")
+    _raise(lib().bsq_moe_combine_backward(T, H, cap, k, _ptr(y), yd, _ptr(pos), _ptr(dout), _ptr(dweights),
+                                          _stream(stream)), "bsq_moe_combine_backward")
+
+
+def bsq_moe_matmul(a, a_scales, b, b_scales, offsets, out, rows=None, k: int = 1, a_dtype: Optional[int] = None,
+                   b_dtype: Optional[int] = None, stream=None):
+    """The experts' products: out [cap, N] (f32 or bf16), row r of expert e's
+    segment = a[rows[r] // k] (or a[r]) times b[e]^T; a [T, K], b [E, N, K]
+    fp8 codes with E8M0 scales [.., K/32], offsets i32 [E + 1]."""
+    torch = _torch()
+    _dev(a, a_scales, b, b_scales, offsets, out, rows)
+    _rank(a, 2, "a")
+    _rank(b, 3, "b")
+    _rank(out, 2, "out")
+    T, K = a.shape
+    E, N = b.shape[:2]
+    cap = out.shape[0]
+    _blocks(a, a_scales, (T, K), "a")
+    _blocks(b, b_scales, (E, N, K), "b")
+    _expect(offsets, torch.int32, (E + 1,), "offsets")
+    _expect(out, out.dtype, (cap, N), "out")
+    if rows is not None:
+        _expect(rows, torch.int32, (cap,), "rows")
+    _raise(lib().bsq_moe_matmul(T, cap, E, N, K, k, _ptr(a), _fp8_code(a) if a_dtype is None else a_dtype,
+                                _ptr(a_scales), _ptr(b), _fp8_code(b) if b_dtype is None else b_dtype,
+                                _ptr(b_scales), _ptr(offsets), _ptr(rows), _ptr(out), _wide(out, "out"),
+                                _stream(stream)), "bsq_moe_matmul")
+
+
+def bsq_moe_wgrad(dyt, dyt_scales, xt, xt_scales, offsets, dW, dyt_dtype: Optional[int] = None,
+                  xt_dtype: Optional[int] = None, stream=None):
+    """The experts' weight gradients dW [E, N, K] (f32 or bf16) from the
+    transposed operands dyt [N, cap] and xt [K, cap] (fp8 codes, E8M0 scales
+    [.., cap/32]); offsets i32 [E + 1], multiples of 128."""
+    torch = _torch()
+    _dev(dyt, dyt_scales, xt, xt_scales, offsets, dW)
+    _rank(dyt, 2, "dyt")
+    _rank(xt, 2, "xt")
+    _rank(dW, 3, "dW")
+    N, cap = dyt.shape
+    K = xt.shape[0]
+    E = dW.shape[0]
+    _blocks(dyt, dyt_scales, (N, cap), "dyt")
+    _blocks(xt, xt_scales, (K, cap), "xt")
+    _expect(offsets, torch.int32, (E + 1,), "offsets")
+    _expect(dW, dW.dtype, (E, N, K), "dW")
+    _raise(lib().bsq_moe_wgrad(cap, E, N, K, _ptr(dyt), _fp8_code(dyt) if dyt_dtype is None else dyt_dtype,
+                               _ptr(dyt_scales), _ptr(xt), _fp8_code(xt) if xt_dtype is None else xt_dtype,
+                               _ptr(xt_scales), _ptr(offsets), _ptr(dW), _wide(dW, "dW"), _stream(stream)),
+           "bsq_moe_wgrad")
+
+
+def bsq_swiglu_mx(gu, h, h_scales, ht=None, ht_scales=None, kept=None, kept_scales=None,
+                  code_dtype: Optional[int] = None, stream=None):
+    """Gated activation h = silu(g) u of gu [R, 2F] = [g | u] (f32 or bf16)
+    as 8-bit codes h [R, F], transposed ht [F, R] (or None), and gu itself
+    in 8 bits as kept [R, 2F] (or None), each with E8M0 scales."""
+    _dev(gu, h, h_scales, ht, ht_scales, kept, kept_scales)
+    _rank(gu, 2, "gu")
+    R, F = gu.shape[0], gu.shape[1] // 2
+    gd = _wide(gu, "gu")
+    _expect(gu, gu.dtype, (R, 2 * F), "gu")
+    _blocks(h, h_scales, (R, F), "h")
+    _blocks(ht, ht_scales, (F, R), "ht", optional=True)
+    _blocks(kept, kept_scales, (R, 2 * F), "kept", optional=True)
+    _raise(lib().bsq_swiglu_mx(R, F, _ptr(gu), gd, _one_code(code_dtype, h, ht, kept), _ptr(h), _ptr(h_scales),
+                               _ptr(ht), _ptr(ht_scales), _ptr(kept), _ptr(kept_scales), _stream(stream)),
+           "bsq_swiglu_mx")
+
+
+def bsq_swiglu_mx_backward(kept, kept_scales, dh, dgu, code_dtype: Optional[int] = None, stream=None):
+    """dgu [R, 2F] = [dg | du] from the 8-bit checkpoint kept [R, 2F] of gu
+    and dh [R, F] (dh and dgu of one dtype, f32 or bf16)."""
+    _dev(kept, kept_scales, dh, dgu)
+    _rank(dh, 2, "dh")
+    R, F = dh.shape
+    dd = _wide(dh, "dh")
+    _blocks(kept, kept_scales, (R, 2 * F), "kept")
+    _expect(dgu, dh.dtype, (R, 2 * F), "dgu")
+    _raise(lib().bsq_swiglu_mx_backward(R, F, _ptr(kept), _one_code(code_dtype, kept), _ptr(kept_scales), _ptr(dh),
+                                        dd, _ptr(dgu), _stream(stream)), "bsq_swiglu_mx_backward")

@@ -97,4 +97,19 @@ __device__ __forceinline__ void load8(const void* base, int64_t elem, float (&x)
   }
 }
 
+// Stores 8 consecutive values (as f32, or as bf16 rounded to nearest even).
+template <int BF16>
+__device__ __forceinline__ void store8(void* p, int64_t elem, const float (&v)[8]) {
+  if (BF16) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = encode_bf16(v[2 * i]) | (encode_bf16(v[2 * i + 1]) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + elem) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + elem);
+    f[0] = make_float4(v[0], v[1], v[2], v[3]);
+    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 }  // namespace bsq

@@ -321,6 +321,151 @@ bsq_status bsq_scaled_matmul_nvfp4(int64_t B, int64_t M, int64_t N, int64_t K, c
                                    const uint8_t* rhs_scales, void* out, int out_dtype, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* --------------------------------------------------------- expert layers -- */
+
+/* The parts of a mixture-of-experts layer around and inside its 8-bit
+ * products: routing tokens to experts, the order of their rows, the ragged
+ * products of all experts, and the gated activation between them.
+ *
+ * Conventions: T tokens, E experts (1 .. 1024), k choices per token.  A
+ * "choice" is an index t k + j (token t's j-th expert); n = T k of them.
+ * Expert e's rows are the segment [offsets[e], offsets[e + 1]) of the `cap`
+ * rows that the layer's arrays have; rows[r] is the choice at row r, -1 where
+ * there is none.  What these index arrays hold is read on the device only:
+ * numbers out of range are taken as "none" or cut to the arrays, and never
+ * make an access out of range.  Codes are blocked by 32 with E8M0 scales, as
+ * bsq_quant_mx writes them.  Every call gives the same bytes on every run. */
+
+typedef enum bsq_score {
+  BSQ_SOFTMAX = 0, /* p = softmax of a token's logits */
+  BSQ_SIGMOID = 1  /* p = 1 / (1 + e^-x) of each logit */
+} bsq_score;
+
+/* Routing.  With scores p of each token's E logits and c = p + bias: a group
+ * of E / groups neighbouring experts is worth the sum of its group_top (1 or
+ * 2) largest c; among the experts of the top_groups best groups the k with
+ * the largest c are chosen, largest first, the lowest index of equals.
+ * Their weights are p (without the bias), divided by their sum if renorm is
+ * not 0, times scale.
+ * The choice is the one that scores in 64 bits give.
+ *   logits  [T, E] of logits_dtype (BSQ_F32 or BSQ_BF16)
+ *   bias    float32 [E] or NULL
+ *   ids     int32 [T, k] (out);  weights float32 [T, k] (out)
+ *   scores  float32 [T, E], all p (out), or NULL
+ * A logit of -inf has score 0; a row of them has scores and weights 0.  NaN
+ * and +inf give unspecified values, but ids are k different experts always.
+ * Rules: E % groups == 0, 1 <= top_groups <= groups, k <= the experts of
+ * top_groups groups, group_top <= E / groups (else SHAPE); E <= 1024,
+ * k <= 64, groups <= 64, group_top <= 2, T <= 2^31 - 1 (else UNSUPPORTED). */
+bsq_status bsq_moe_route(int64_t T, int64_t E, int64_t k, int64_t groups, int64_t top_groups,
+                         int64_t group_top, const void* logits, int logits_dtype, const float* bias,
+                         int score, int renorm, float scale, int32_t* ids, float* weights,
+                         float* scores, void* stream);
+
+/* Gradient of bsq_moe_route with respect to the logits, the choice held
+ * fixed (the bias only steers the choice and has no gradient).
+ *   ids      int32 [T, k] as chosen (one outside 0 .. E - 1 adds nothing)
+ *   dweights float32 [T, k];  dscores float32 [T, E] or NULL
+ *   dlogits  [T, E] of logits_dtype (out) */
+bsq_status bsq_moe_route_backward(int64_t T, int64_t E, int64_t k, const void* logits,
+                                  int logits_dtype, int score, int renorm, float scale,
+                                  const int32_t* ids, const float* dweights, const float* dscores,
+                                  void* dlogits, void* stream);
+
+/* The order of rows: a stable sort of n choices by expert, each expert's
+ * segment starting at a multiple of `align` rows.
+ *   ids     int32 [n]; one outside 0 .. E - 1 has no row (pos -1)
+ *   offsets int32 [E + 1], first row of each segment and the end of the last
+ *   counts  int32 [E], choices in each segment
+ *   rows    int32 [cap], the choice at each row, -1 for none
+ *   pos     int32 [n], the row of each choice             (all out)
+ * cap: at least n + min(E, n) (align - 1); bsq_moe_capacity gives that,
+ * rounded up to a multiple of align (0 for invalid, INT64_MAX for too large
+ * arguments).  workspace: bsq_moe_plan_workspace_bytes(n, E) bytes.
+ * Rules: n and cap at most 2^31 - 1, E <= 1024 (else UNSUPPORTED). */
+int64_t bsq_moe_capacity(int64_t n, int64_t E, int64_t align);
+size_t bsq_moe_plan_workspace_bytes(int64_t n, int64_t E);
+bsq_status bsq_moe_plan(int64_t n, int64_t E, int64_t align, int64_t cap, const int32_t* ids,
+                        int32_t* offsets, int32_t* counts, int32_t* rows, int32_t* pos,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Tokens as 8-bit operands in the order of rows: row r is x[rows[r] / k]
+ * (times weights[rows[r]] where weights is not NULL: the gradient's rows),
+ * zeros where rows[r] is none, quantized as bsq_quant_mx does.
+ *   x        [T, H] of x_dtype (BSQ_F32 or BSQ_BF16)
+ *   weights  float32 [T, k] or NULL
+ *   codes    [cap, H], scales [cap, H / 32]: blocks along rows, or both NULL
+ *   codes_t  [H, cap], scales_t [H, cap / 32]: blocks of 32 rows, written
+ *            transposed (for bsq_moe_wgrad), or both NULL
+ * Rules: H % 32 == 0; with codes_t also cap % 32 == 0. */
+bsq_status bsq_moe_gather_mx(int64_t T, int64_t H, int64_t cap, int64_t k, const void* x, int x_dtype,
+                             const int32_t* rows, const float* weights, int code_dtype, uint8_t* codes,
+                             uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, void* stream);
+
+/* Rows summed back to their tokens: out[t] = sum over j of weights[t, j]
+ * y[pos[t, j]] (weights NULL: 1), float32 sums in the order of j; a pos
+ * outside 0 .. cap - 1 adds nothing.  With weights NULL this is also the
+ * gradient of the gather.
+ *   y [cap, H] and out [T, H] of y_dtype (BSQ_F32 or BSQ_BF16)
+ *   pos int32 [T, k], weights float32 [T, k]
+ * bsq_moe_combine_backward: dweights[t, j] = y[pos[t, j]] . dout[t], dout
+ * [T, H] of y_dtype, dweights float32 [T, k] (0 for a choice without a row).
+ * Rules: H % 8 == 0. */
+bsq_status bsq_moe_combine(int64_t T, int64_t H, int64_t cap, int64_t k, const void* y, int y_dtype,
+                           const int32_t* pos, const float* weights, void* out, void* stream);
+bsq_status bsq_moe_combine_backward(int64_t T, int64_t H, int64_t cap, int64_t k, const void* y,
+                                    int y_dtype, const int32_t* pos, const void* dout, float* dweights,
+                                    void* stream);
+
+/* The experts' products: out[r] = a[src(r)] B_e^T for the rows r of expert
+ * e's segment, src(r) = rows[r] / k, or r where rows is NULL.  Rows without
+ * a choice, and rows from offsets[E] on, are written as zeros.
+ *   a [T, K] codes (a_dtype E4M3 or E5M2), a_scales [T, K / 32]
+ *   b [E, N, K] codes (E4M3), b_scales [E, N, K / 32]
+ *   offsets int32 [E + 1] (any row numbers, also unaligned), rows int32 [cap]
+ *   out [cap, N] of out_dtype (BSQ_F32 or BSQ_BF16)
+ * The input's gradient is the same call with the transposed weights.
+ * Rules: K % 128 == 0, N % 16 == 0, T K / 32 and N K / 32 below 2^32 (else
+ * UNSUPPORTED). */
+bsq_status bsq_moe_matmul(int64_t T, int64_t cap, int64_t E, int64_t N, int64_t K, int64_t k,
+                          const uint8_t* a, int a_dtype, const uint8_t* a_scales, const uint8_t* b,
+                          int b_dtype, const uint8_t* b_scales, const int32_t* offsets,
+                          const int32_t* rows, void* out, int out_dtype, void* stream);
+
+/* The experts' weight gradients: dW[e] = sum over the rows r of expert e's
+ * segment of dyt[:, r] xt[:, r]^T (zeros for an empty segment).
+ *   dyt [N, cap] codes (E4M3 or E5M2), dyt_scales [N, cap / 32]
+ *   xt  [K, cap] codes (E4M3), xt_scales [K, cap / 32]; rows without a choice
+ *       hold zero codes in one of the two (bsq_moe_gather_mx writes both so)
+ *   offsets int32 [E + 1], multiples of 128 (align = 128 in bsq_moe_plan;
+ *       others are cut down to one)
+ *   dW [E, N, K] of out_dtype (BSQ_F32 or BSQ_BF16)
+ * Rules: cap % 128 == 0 (else SHAPE); N % 16 == 0, K % 16 == 0, N cap / 32
+ * and K cap / 32 below 2^32 (else UNSUPPORTED). */
+bsq_status bsq_moe_wgrad(int64_t cap, int64_t E, int64_t N, int64_t K, const uint8_t* dyt, int dyt_dtype,
+                         const uint8_t* dyt_scales, const uint8_t* xt, int xt_dtype,
+                         const uint8_t* xt_scales, const int32_t* offsets, void* dW, int out_dtype,
+                         void* stream);
+
+/* Gated activation in 8 bits: h = g / (1 + e^-g) u of gu = [g | u].
+ *   gu   [R, 2 F] of gu_dtype (BSQ_F32 or BSQ_BF16)
+ *   h    [R, F] codes, h_scales [R, F / 32]: the next product's operand
+ *   ht   [F, R] codes, ht_scales [F, R / 32]: blocks of 32 rows, written
+ *        transposed (for bsq_moe_wgrad), or both NULL
+ *   kept [R, 2 F] codes, kept_scales [R, 2 F / 32]: gu itself in 8 bits, the
+ *        checkpoint that the backward pass reads, or both NULL
+ * code_dtype (E4M3 or E5M2) is that of all codes.
+ * bsq_swiglu_mx_backward, from the checkpoint's values of g and u, with
+ * s = 1 / (1 + e^-g): dgu = [dh u s (1 + g (1 - s)) | dh g s], dh [R, F] and
+ * dgu [R, 2 F] of dh_dtype.
+ * Rules: F % 32 == 0; with ht also R % 32 == 0. */
+bsq_status bsq_swiglu_mx(int64_t R, int64_t F, const void* gu, int gu_dtype, int code_dtype, uint8_t* h,
+                         uint8_t* h_scales, uint8_t* ht, uint8_t* ht_scales, uint8_t* kept,
+                         uint8_t* kept_scales, void* stream);
+bsq_status bsq_swiglu_mx_backward(int64_t R, int64_t F, const uint8_t* kept, int code_dtype,
+                                  const uint8_t* kept_scales, const void* dh, int dh_dtype, void* dgu,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif
