@@ -11,13 +11,14 @@
 // their true order.
 #include <math.h>
 
+#include <type_traits>
+
+#include "fp8.h"
 #include "moe.h"
 
 namespace bsq {
 
 namespace {
-
-constexpr int kRouteMaxE = 1024;
 
 struct RouteArgs {
   int64_t T;
@@ -34,6 +35,47 @@ struct RouteArgs {
 template <int BF16>
 __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
   return BF16 ? decode_bf16(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// Values o .. o + 3 of a row of n; `none` past its end.  `whole`: rows are
+// whole fours, aligned.
+template <int BF16>
+__device__ __forceinline__ void load4(const void* base, int64_t row, int o, int n, bool whole, float none, float* x) {
+  if (whole) {
+    if (o >= n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = none;
+    } else if (BF16) {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + row + o);
+      x[0] = decode_bf16(v.x & 0xFFFFu);
+      x[1] = decode_bf16(v.x >> 16);
+      x[2] = decode_bf16(v.y & 0xFFFFu);
+      x[3] = decode_bf16(v.y >> 16);
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + row + o);
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = o + i < n ? logit_at<BF16>(base, row + o + i) : none;
+  }
+}
+
+// Over a row of 16 lanes, left in each.
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __uint_as_float(dpp_mov<0xB1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_mov<0x4E>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_mov<0x141>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(dpp_mov<0x140>(__float_as_uint(v))));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __uint_as_float(dpp_mov<0xB1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<0x4E>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<0x141>(__float_as_uint(v)));
+  return v + __uint_as_float(dpp_mov<0x140>(__float_as_uint(v)));
 }
 
 __device__ __forceinline__ double wave_max(double v) {
@@ -178,6 +220,323 @@ __global__ void __launch_bounds__(256) k_route(RouteArgs a) {
     route_token<BF16, EPL>(a, t, lane, cs[w]);
 }
 
+// ------------------------------------------------- few choices, fast path --
+// A token by L lanes (16: four tokens to a wave; 64), each with S scores.
+// The choice is a sort instead of rounds of argmax: a score's low 10 bits
+// make room for its expert's number, so that one 64-bit maximum orders scores
+// and breaks ties by the lowest index; every lane sorts its keys and keeps
+// 8, and log2(L) exchanges merge the lists (the larger of A[i] and B[7 - i]
+// are the 8 largest of two sorted lists).  Scores that are closer than the
+// lost bits and this path's own exponential (2^-42) allow are told apart by
+// the general path above, unless their logits and biases are the same.
+constexpr int kTop = 8;
+
+// e^x to a relative 2^-42 for x <= 0 or so: x = n ln 2 + r (ln 2 in two
+// pieces, the first of 36 bits, so that n times it is exact), the power series of
+// e^r to r^10 (|r| <= ln 2 / 2: the next term is below 2.3e-13).
+__device__ __forceinline__ double exp_near(double x) {
+  x = __builtin_fmax(x, -800.0);  // 2^-1154: zero either way
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = fma(n, -0x1.62e42fefa0000p-1, x);
+  r = fma(n, -0x1.cf79abc9e3b3ap-40, r);
+  double y = 1.0 / 3628800.0;
+  y = fma(y, r, 1.0 / 362880.0);
+  y = fma(y, r, 1.0 / 40320.0);
+  y = fma(y, r, 1.0 / 5040.0);
+  y = fma(y, r, 1.0 / 720.0);
+  y = fma(y, r, 1.0 / 120.0);
+  y = fma(y, r, 1.0 / 24.0);
+  y = fma(y, r, 1.0 / 6.0);
+  y = fma(y, r, 0.5);
+  y = fma(y, r, 1.0);
+  y = fma(y, r, 1.0);
+  return __builtin_ldexp(y, int(n));
+}
+
+// 1 / d for 1 <= d < 2^1000: the hardware's start and one Newton step.
+__device__ __forceinline__ double recip_near(double d) {
+  const double y = __builtin_amdgcn_rcp(d);
+  return fma(y, fma(-d, y, 1.0), y);
+}
+
+constexpr double kFar = 690.0;
+__device__ __forceinline__ double sigmoid_near(double x) {
+  // 0 from e^690 on (kFar), where the true score is below 2^-995
+  return x < -kFar ? 0.0 : recip_near(1.0 + exp_near(-x));
+}
+
+union Bits64 {
+  double d;
+  int64_t i;
+  uint32_t u[2];
+};
+
+// The value of the lane that step STEP pairs with this one (STEP 0 .. 3:
+// within rows of 16).
+template <int STEP>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+  return dpp_mov<STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140>(v);
+}
+// Both values of the pair, in an order that both lanes agree on or not (for
+// commutative use); steps 4 and 5 exchange rows and halves.
+template <int STEP>
+__device__ __forceinline__ void pair(double v, double& a, double& b) {
+  Bits64 x{v}, p, q;
+  if constexpr (STEP < 4) {
+    p.u[0] = partner<STEP>(x.u[0]);
+    p.u[1] = partner<STEP>(x.u[1]);
+    a = v;
+    b = p.d;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto s = STEP == 4 ? __builtin_amdgcn_permlane16_swap(x.u[h], x.u[h], false, false)
+                               : __builtin_amdgcn_permlane32_swap(x.u[h], x.u[h], false, false);
+      p.u[h] = uint32_t(s[0]);
+      q.u[h] = uint32_t(s[1]);
+    }
+    a = p.d;
+    b = q.d;
+  }
+}
+
+template <int N, typename F>
+__device__ __forceinline__ void steps(F&& f) {
+  if constexpr (N > 0) {
+    steps<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+template <int L>
+constexpr int kLog = L == 16 ? 4 : 6;
+
+template <int L>
+__device__ __forceinline__ double lanes_max(double v) {
+  steps<kLog<L>>([&](auto s) {
+    double a, b;
+    pair<decltype(s)::value>(v, a, b);
+    v = __builtin_fmax(a, b);
+  });
+  return v;
+}
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v) {
+  steps<kLog<L>>([&](auto s) {
+    double a, b;
+    pair<decltype(s)::value>(v, a, b);
+    v = a + b;
+  });
+  return v;
+}
+
+__device__ __forceinline__ void order2(double& a, double& b) {
+  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+  a = hi;
+  b = lo;
+}
+// Descending order of 8 (19 exchanges).
+__device__ __forceinline__ void sort8(double* v) {
+  order2(v[0], v[2]); order2(v[1], v[3]); order2(v[4], v[6]); order2(v[5], v[7]);
+  order2(v[0], v[4]); order2(v[1], v[5]); order2(v[2], v[6]); order2(v[3], v[7]);
+  order2(v[0], v[1]); order2(v[2], v[3]); order2(v[4], v[5]); order2(v[6], v[7]);
+  order2(v[2], v[4]); order2(v[3], v[5]);
+  order2(v[1], v[4]); order2(v[3], v[6]);
+  order2(v[1], v[2]); order2(v[3], v[4]); order2(v[5], v[6]);
+}
+// Descending order of 8 that rise and fall once.
+__device__ __forceinline__ void merge8(double* v) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) order2(v[i], v[i + d]);
+}
+
+constexpr double kNever = -1.7e308;  // key of an expert that has no score to be chosen by
+
+// The general path as a call, so that its registers are not this path's.
+template <int BF16, int EPL>
+__device__ __attribute__((noinline)) void route_token_apart(RouteArgs a, int64_t t, int lane, double* cs) {
+  route_token<BF16, EPL>(a, t, lane, cs);
+}
+
+template <int BF16, int L, int S>
+__global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
+  constexpr int kSlow = L * S / 64;  // scores per lane of the general path
+  __shared__ double cs[4][64 * kSlow];
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int E = a.E, G = a.groups, per = E / G;
+  const int LG = L / G, shift = 31 - __clz(LG);    // lanes per group
+  const int l = lane & (L - 1), g = l >> shift, lg = l & (LG - 1);
+  constexpr int V = 4;                            // neighbours in a lane
+  const bool whole = (per & (V - 1)) == 0;        // rows and groups start at whole fours
+  constexpr int TPW = 64 / L;
+  const int64_t t0 = (int64_t(blockIdx.x) * 4 + w) * TPW;
+  if (t0 >= a.T) return;
+  const int64_t t_mine = t0 + lane / L;
+  const bool live = t_mine < a.T;
+  const int64_t row = (live ? t_mine : a.T - 1) * E;
+
+  // slot i is expert (in its group) of chunk i / 4
+  auto at = [&](int i) { return (i / V * LG + lg) * V + (i & (V - 1)); };
+  float x[S];
+#pragma unroll
+  for (int q = 0; q < S / V; ++q)
+    load4<BF16>(a.logits, row + g * per, at(q * V), per, whole, -INFINITY, x + 4 * q);
+  // ---- scores
+  double c[S];
+  double top = 0.0, inv = 0.0;
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) c[i] = sigmoid_near(double(x[i]));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S; ++i) m = fmaxf(m, x[i]);
+    top = lanes_max<L>(double(m));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      // a row of -inf alone has scores of zero
+      c[i] = x[i] == -INFINITY ? 0.0 : exp_near(double(x[i]) - top);
+      sum += c[i];
+    }
+    sum = lanes_sum<L>(sum);
+    inv = sum == 0.0 ? 0.0 : recip_near(sum);
+#pragma unroll
+    for (int i = 0; i < S; ++i) c[i] *= inv;
+  }
+  if (a.scores != nullptr && live) {
+#pragma unroll
+    for (int q = 0; q < S / V; ++q) {
+      const int o = at(q * V);
+      float* p = a.scores + row + g * per + o;
+      if (whole) {
+        if (o < per)
+          *reinterpret_cast<float4*>(p) =
+              make_float4(float(c[4 * q]), float(c[4 * q + 1]), float(c[4 * q + 2]), float(c[4 * q + 3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (o + i < per) p[i] = float(c[4 * q + i]);
+      }
+    }
+  }
+  // ---- what the choice goes by
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int o = at(i);
+    if (a.bias != nullptr) c[i] += o < per ? double(a.bias[g * per + o]) : 0.0;
+    // infinities stay numbers beside the expert's number; NaN comes last
+    c[i] = __builtin_fmin(__builtin_fmax(c[i], kNever), -kNever);
+    if (o >= per) c[i] = -INFINITY;
+  }
+  bool in = true, close = false;  // close: for the general path to settle
+  if (G > 1) {
+    double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      b2 = __builtin_fmax(b2, __builtin_fmin(b1, c[i]));
+      b1 = __builtin_fmax(b1, c[i]);
+    }
+    steps<kLog<L>>([&](auto s) {
+      if ((1 << decltype(s)::value) < LG) {
+        double a1, o1, a2, o2;
+        pair<decltype(s)::value>(b1, a1, o1);
+        pair<decltype(s)::value>(b2, a2, o2);
+        b1 = __builtin_fmax(a1, o1);
+        b2 = __builtin_fmax(__builtin_fmin(a1, o1), __builtin_fmax(a2, o2));
+      }
+    });
+    const double worth = a.group_top == 2 ? b1 + b2 : b1;
+    int before = 0;  // groups that come before this lane's
+    for (int h = 1; h < G; ++h) {
+      const int og = (g + h) & (G - 1);
+      const double o = __shfl(worth, (lane & ~(L - 1)) + (og << shift));
+      before += (o > worth || (o == worth && og < g)) ? 1 : 0;
+      close |= o != worth && fabs(o - worth) <= (fabs(worth) + 2.0) * 0x1p-38;
+    }
+    in = before < a.top_groups;
+  }
+  double list[S > kTop ? S : kTop];
+  double key[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    Bits64 b{in || c[i] == -INFINITY ? c[i] : kNever};
+    const uint32_t e = uint32_t(g * per + at(i));
+    if (c[i] != -INFINITY) b.u[0] = (b.u[0] & ~1023u) | (b.i < 0 ? e : 1023u - e);
+    key[i] = list[i] = b.d;
+  }
+#pragma unroll
+  for (int i = S; i < kTop; ++i) list[i] = -INFINITY;
+  sort8(list);
+  if constexpr (S > kTop) {
+    sort8(list + kTop);
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) list[i] = __builtin_fmax(list[i], list[2 * kTop - 1 - i]);
+    merge8(list);
+  }
+  steps<kLog<L>>([&](auto s) {
+    double p[kTop], q[kTop];
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) pair<decltype(s)::value>(list[i], p[i], q[i]);
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) list[i] = __builtin_fmax(p[i], q[kTop - 1 - i]);
+    merge8(list);
+  });
+  // ---- lane j has the j-th choice
+  Bits64 mine{list[0]};
+  double last = list[0];
+#pragma unroll
+  for (int j = 1; j < kTop; ++j) {
+    if (l == j) mine.d = list[j];
+    if (a.k - 1 == j) last = list[j];
+  }
+  const bool on = l < a.k;
+  int id = int(mine.u[0] & 1023u);
+  if (mine.i >= 0) id = 1023 - id;
+  id = id < E ? id : E - 1;
+  const float xm = logit_at<BF16>(a.logits, row + id);
+  const double bm = a.bias != nullptr ? double(a.bias[id]) : 0.0;
+  double p = 0.0;
+  if (on) p = a.sigmoid ? sigmoid_near(double(xm)) : xm == -INFINITY ? 0.0 : exp_near(double(xm) - top) * inv;
+  const double total = lanes_sum<16>(p);
+
+  // ---- neighbours in the order, and the last against what was left out
+  const double next = __shfl_down(mine.d, 1), p_next = __shfl_down(p, 1), b_next = __shfl_down(bm, 1);
+  const float x_next = __shfl_down(xm, 1);
+  close |= l + 1 < a.k && next > kNever * 0.999 &&
+               fabs(mine.d - next) <= (fabs(mine.d) + p + p_next) * 0x1p-38 && !(xm == x_next && bm == b_next);
+  close |= a.sigmoid && on && xm < -kFar && xm > -760.f;  // a weight of what sigmoid_near leaves out
+  if (last > kNever * 0.999) {
+    const int from = (lane & ~(L - 1)) + a.k - 1;
+    const double lim = last - (fabs(last) + (a.bias != nullptr ? 1.0 : 0.0)) * 0x1p-38;
+    bool more = false;
+#pragma unroll
+    for (int i = 0; i < S; ++i) more |= key[i] >= lim && key[i] < last;
+    if (__ballot(more)) {
+      const float xk = __shfl(xm, from);
+      const double bk = __shfl(bm, from);
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        if (key[i] >= lim && key[i] < last) {
+          const int e = g * per + at(i);
+          close |= !(logit_at<BF16>(a.logits, row + e) == xk && (a.bias == nullptr || double(a.bias[e]) == bk));
+        }
+    }
+  }
+  const uint64_t again = __ballot(close && live);
+  const uint64_t whose = L == 64 ? ~0ull : 0xFFFFull;
+  if (on && live && !((again >> (lane & ~(L - 1))) & whose)) {
+    a.ids[t_mine * a.k + l] = id;
+    const double v = a.renorm ? (total == 0.0 ? 0.0 : p / total) : p;
+    a.weights[t_mine * a.k + l] = float(v * double(a.scale));
+  }
+  if (again)
+    for (int r = 0; r < TPW; ++r)
+      if ((again >> (L * r)) & whose) route_token_apart<BF16, kSlow>(a, t0 + r, lane, cs[w]);
+}
+
 // ------------------------------------------------------------- gradient --
 struct RouteBwdArgs {
   int64_t T;
@@ -279,6 +638,113 @@ __global__ void __launch_bounds__(256) k_route_backward(RouteBwdArgs a) {
     route_backward_token<BF16, EPL>(a, t, lane, dps[w]);
 }
 
+// Four tokens to a wave, 16 lanes and 16 S experts each; lane l holds the
+// choices l < k and the experts of chunks l, l + 16, ... of four.
+template <int BF16, int S>
+__global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
+  __shared__ __attribute__((aligned(16))) float dps[4][4][16 * S];
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15;
+  const int E = a.E;
+  const int64_t t0 = (int64_t(blockIdx.x) * 4 + w) * 4;
+  if (t0 >= a.T) return;
+  const bool live = t0 + lane / 16 < a.T, whole = (E & 3) == 0;
+  const int64_t t = live ? t0 + lane / 16 : a.T - 1, row = t * E;
+  float* const mine = dps[w][lane / 16];
+  // the chosen experts and their logits, while the row is on its way
+  const int id = l < a.k ? a.ids[t * a.k + l] : -1;
+  const bool on = id >= 0 && id < E;
+  float d = on ? a.dweights[t * a.k + l] * a.scale : 0.f;
+  const float xc = on ? logit_at<BF16>(a.logits, row + id) : -INFINITY;
+  float p[S], ds[S];
+#pragma unroll
+  for (int q = 0; q < S / 4; ++q) {
+    const int o = (q * 16 + l) * 4;
+    load4<BF16>(a.logits, row, o, E, whole, -INFINITY, p + 4 * q);
+    if (a.dscores != nullptr) load4<0>(a.dscores, row, o, E, whole, 0.f, ds + 4 * q);
+    *reinterpret_cast<float4*>(mine + o) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __builtin_amdgcn_wave_barrier();
+  float r = 0.f, top = 0.f, pc;
+  if (a.sigmoid) {
+    pc = 1.0f / (1.0f + expf(-xc));
+  } else {
+    top = p[0];
+#pragma unroll
+    for (int i = 1; i < S; ++i) top = fmaxf(top, p[i]);
+    top = row_max(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      p[i] = top == -INFINITY ? 0.f : expf(p[i] - top);
+      sum += p[i];
+    }
+    sum = row_sum(sum);
+    r = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < S; ++i) p[i] *= r;
+    pc = xc == -INFINITY ? 0.f : expf(xc - top) * r;
+  }
+  if (a.renorm) {
+    const float total = row_sum(on ? pc : 0.f);
+    const float rt = total == 0.f ? 0.f : 1.0f / total;
+    d = (d - row_sum(d * (pc * rt))) * rt;
+  }
+  if (on) mine[id] = d;
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+  float dp[S], dot = 0.f;
+#pragma unroll
+  for (int q = 0; q < S / 4; ++q) {
+    const float4 v = *reinterpret_cast<const float4*>(mine + (q * 16 + l) * 4);
+    dp[4 * q] = v.x;
+    dp[4 * q + 1] = v.y;
+    dp[4 * q + 2] = v.z;
+    dp[4 * q + 3] = v.w;
+  }
+  if (a.dscores != nullptr)
+#pragma unroll
+    for (int i = 0; i < S; ++i) dp[i] += ds[i];
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) dot = fmaf(p[i], dp[i], dot);
+    dot = row_sum(dot);
+  }
+#pragma unroll
+  for (int q = 0; q < S / 4; ++q) {
+    float dx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * q + i;
+      if (a.sigmoid) {
+        // p and 1 - p, without the cancellation
+        const float z = expf(-fabsf(p[j])), rz = 1.0f / (1.0f + z);
+        dx[i] = dp[j] * (z * rz) * rz;
+      } else {
+        dx[i] = p[j] * (dp[j] - dot);
+      }
+    }
+    const int o = (q * 16 + l) * 4;
+    if (!live) continue;
+    if (whole) {
+      if (o < E) {
+        if (BF16)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + row + o) =
+              make_uint2(encode_bf16(dx[0]) | (encode_bf16(dx[1]) << 16), encode_bf16(dx[2]) | (encode_bf16(dx[3]) << 16));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + row + o) =
+              make_float4(dx[0], dx[1], dx[2], dx[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (o + i < E) {
+          if (BF16) static_cast<uint16_t*>(a.dlogits)[row + o + i] = uint16_t(encode_bf16(dx[i]));
+          else static_cast<float*>(a.dlogits)[row + o + i] = dx[i];
+        }
+    }
+  }
+}
+
 template <typename F>
 void by_width(int E, F&& f) {
   const int epl = (E + 63) / 64;
@@ -288,6 +754,9 @@ void by_width(int E, F&& f) {
   else if (epl <= 8) f(std::integral_constant<int, 8>{});
   else f(std::integral_constant<int, 16>{});
 }
+
+// From this many tokens on, four share a wave.
+constexpr int64_t kRowTokens = 2048;
 
 unsigned token_grid(int64_t T) {
   const int64_t g = (T + 3) / 4;
@@ -299,6 +768,27 @@ unsigned token_grid(int64_t T) {
 bsq_status launch_route(const RouteLaunch& L, hipStream_t st) {
   const RouteArgs a{L.T, L.E, L.k, L.groups, L.top_groups, L.group_top, L.logits, L.sigmoid, L.renorm, L.scale,
                     L.bias, L.ids, L.weights, L.scores};
+  const bool even = (L.groups & (L.groups - 1)) == 0;
+  const int lanes = L.T >= kRowTokens && L.E <= 256 && L.groups <= 16 ? 16 : 64;
+  if (even && L.k <= kTop) {
+    const int slots = (L.E / L.groups + lanes / L.groups - 1) / (lanes / L.groups);
+    if (slots <= 16) {
+      const int64_t per = lanes == 16 ? 16 : 4, want = (L.T + per - 1) / per;
+      const unsigned grid = unsigned(want);
+      auto go = [&](auto l, auto s) {
+        if (L.bf16) hipLaunchKernelGGL((k_route_top<1, l.value, s.value>), grid, 256, 0, st, a);
+        else hipLaunchKernelGGL((k_route_top<0, l.value, s.value>), grid, 256, 0, st, a);
+      };
+      auto by_slots = [&](auto l) {
+        if (slots <= 4) go(l, std::integral_constant<int, 4>{});
+        else if (slots <= 8) go(l, std::integral_constant<int, 8>{});
+        else go(l, std::integral_constant<int, 16>{});
+      };
+      if (lanes == 16) by_slots(std::integral_constant<int, 16>{});
+      else by_slots(std::integral_constant<int, 64>{});
+      return launch_status("moe_route");
+    }
+  }
   by_width(L.E, [&](auto epl) {
     if (L.bf16) hipLaunchKernelGGL((k_route<1, epl.value>), token_grid(L.T), 256, 0, st, a);
     else hipLaunchKernelGGL((k_route<0, epl.value>), token_grid(L.T), 256, 0, st, a);
@@ -309,6 +799,17 @@ bsq_status launch_route(const RouteLaunch& L, hipStream_t st) {
 bsq_status launch_route_backward(const RouteBackwardLaunch& L, hipStream_t st) {
   const RouteBwdArgs a{L.T, L.E, L.k, L.logits, L.sigmoid, L.renorm, L.scale, L.ids, L.dweights, L.dscores,
                        L.dlogits};
+  if (L.E <= 256 && L.k <= 16 && L.T >= kRowTokens) {
+    const unsigned grid = unsigned((L.T + 15) / 16);
+    auto go = [&](auto s) {
+      if (L.bf16) hipLaunchKernelGGL((k_route_backward_rows<1, s.value>), grid, 256, 0, st, a);
+      else hipLaunchKernelGGL((k_route_backward_rows<0, s.value>), grid, 256, 0, st, a);
+    };
+    if (L.E <= 64) go(std::integral_constant<int, 4>{});
+    else if (L.E <= 128) go(std::integral_constant<int, 8>{});
+    else go(std::integral_constant<int, 16>{});
+    return launch_status("moe_route_backward");
+  }
   by_width(L.E, [&](auto epl) {
     if (L.bf16) hipLaunchKernelGGL((k_route_backward<1, epl.value>), token_grid(L.T), 256, 0, st, a);
     else hipLaunchKernelGGL((k_route_backward<0, epl.value>), token_grid(L.T), 256, 0, st, a);

@@ -199,6 +199,122 @@ def test_route_backward_passes_over_ids_that_are_none():
         _within(_values(dl), want, 6 * _span(x) * size + TINY, "dlogits")
 
 
+MANY = 2051  # tokens enough for the kernels that put four in a wave, and three left over
+
+
+@pytest.mark.parametrize("E,k,bf16,opts", [
+    (256, 8, True, dict(sigmoid=True, groups=8, top_groups=4, group_top=2, scale=2.5)),
+    (256, 8, False, dict(groups=8, top_groups=3, group_top=1)), (256, 1, True, {}), (255, 8, False, dict(sigmoid=True)),
+    (250, 7, True, dict(groups=2, top_groups=1, renorm=False)), (128, 8, True, {}), (129, 5, False, {}),
+    (64, 6, True, dict(sigmoid=True, groups=16, top_groups=5, group_top=2)), (65, 2, True, dict(sigmoid=True)),
+    (96, 8, False, dict(groups=4, top_groups=2, group_top=2)), (8, 8, True, {}), (3, 2, False, dict(sigmoid=True)),
+    (1, 1, True, {}), (126, 4, True, dict(groups=2, top_groups=2, sigmoid=True)),
+    (256, 9, True, {}), (192, 16, False, dict(sigmoid=True)), (60, 3, False, dict(groups=3, top_groups=2)),
+    (512, 8, True, dict(groups=8, top_groups=4)), (1000, 8, False, dict(sigmoid=True)), (260, 6, True, {})])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_of_many_tokens(E, k, bf16, opts, biased):
+    say("route many", E, k, bf16, opts, biased)
+    rng = np.random.default_rng(E * 31 + k)
+    x = rng.standard_normal((MANY, E)) * 1.5
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32) if biased else None
+    _route(x, bf16, k, bias, full=(E + k) % 2 == 0, seed=E, **dict(opts))
+
+
+@pytest.mark.parametrize("T", [37, MANY])
+@pytest.mark.parametrize("E", [24, 64, 256, 320])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_of_equals_with_a_bias(T, E, sigmoid):
+    """Few logits and few biases: equal sums of equal and of different terms,
+    and experts that are left out next to equals that are chosen."""
+    say("route equals biased", T, E, sigmoid)
+    rng = np.random.default_rng(E)
+    x = rng.integers(-1, 2, (T, E)).astype(np.float32)
+    bias = (rng.integers(0, 2, E) * 0.25).astype(np.float32)
+    _route(x, True, 8, bias, sigmoid=sigmoid)
+    _route(x, False, 6, None, sigmoid=sigmoid, groups=8, top_groups=3, group_top=2)
+    _route(x, False, 5, bias, sigmoid=sigmoid, groups=4, top_groups=2, group_top=1)
+
+
+@pytest.mark.parametrize("E", [64, 256, 512])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("groups", [1, 8])
+def test_route_of_many_tells_scores_apart_past_float32(E, sigmoid, groups):
+    """A bias that cancels the scores but for what lies below a float32 step."""
+    say("route close many", E, sigmoid, groups)
+    rng = np.random.default_rng(E + groups)
+    x = (rng.standard_normal((1, E)) * 1.5).astype(np.float32).repeat(MANY, 0)
+    x[1::2] = np.roll(x[1::2], 1, axis=1)
+    bias = (0.5 - OE.scores(x[:1], sigmoid)[0]).astype(np.float32)
+    _route(x, False, 8, bias, train=False, sigmoid=sigmoid, groups=groups, top_groups=max(1, groups // 2),
+           group_top=2 if groups > 1 else 1)
+
+
+@pytest.mark.parametrize("T", [64, MANY])
+@pytest.mark.parametrize("E", [40, 256, 300])
+def test_route_tells_scores_of_neighbouring_logits_apart(T, E):
+    """Logits next to each other in float32 where the sigmoid is flat: scores
+    that differ by a part in 2^48."""
+    say("route neighbours", T, E)
+    rng = np.random.default_rng(E)
+    at = np.float32(20.0) + np.arange(E, dtype=np.float32) * np.float32(2.0 ** -19)
+    x = np.stack([rng.permutation(at) for _ in range(T)])
+    _route(x, False, 8, sigmoid=True)
+    _route(x, False, 8)
+
+
+@pytest.mark.parametrize("E,groups", [(40, 1), (64, 4), (256, 8), (400, 8)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_of_many_with_logits_that_are_masked(E, groups, sigmoid):
+    say("route masked many", E, groups, sigmoid)
+    rng = np.random.default_rng(5)
+    x = (rng.standard_normal((MANY, E)) * 2).astype(np.float32)
+    x[0::13, :] = -np.inf
+    x[1::13, 1:] = -np.inf
+    x[2::13, : E // 2] = -np.inf
+    x[3::13, ::2] = -np.inf
+    x[4::13, :] = -60.0
+    x[5::13, :] = 80.0
+    x[6::13, 0] = -3e38
+    x[7::13, 3:] = -1e9
+    x[8::13, 2:] -= 700.0
+    _route(x, False, 6, sigmoid=sigmoid, groups=groups, top_groups=max(1, groups // 2))
+    b = np.zeros(E, np.float32)
+    b[5] = -np.inf
+    b[6] = 3.0
+    _route(x, False, 4, b, sigmoid=sigmoid, groups=groups, top_groups=max(1, groups // 2), group_top=2)
+
+
+@pytest.mark.parametrize("E", [40, 256, 500])
+def test_route_ids_of_many_are_experts_whatever_the_logits(E):
+    torch = _torch()
+    say("route NaN many", E)
+    x = torch.randn(MANY, E, device="cuda")
+    x[0::9] = float("nan")
+    x[1::9, 5] = float("nan")
+    x[2::9, 7] = float("inf")
+    x[3::9, :] = float("inf")
+    for kw in (dict(), dict(score=bsq.BSQ_SIGMOID), dict(groups=4, top_groups=2, group_top=2)):
+        ids, w = filled((MANY, 8), torch.int32, -7), empty((MANY, 8), torch.float32)
+        bsq.bsq_moe_route(x, ids, w, **kw)
+        got = host(ids)
+        assert got.min() >= 0 and got.max() < E and all(len(set(r)) == 8 for r in got.tolist())
+
+
+def test_route_backward_of_many_passes_over_ids_that_are_none():
+    torch = _torch()
+    say("route backward none many")
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((MANY, 20)).astype(np.float32)
+    ids = np.stack([rng.permutation(24)[:3] for _ in range(MANY)]).astype(np.int32)
+    ids[ids >= 22] = -1
+    dw = rng.standard_normal((MANY, 3)).astype(np.float32)
+    for sigmoid in (False, True):
+        dl = filled((MANY, 20), torch.float32, float("nan"))
+        bsq.bsq_moe_route_backward(to_dev(x), to_dev(ids), to_dev(dw), dl, score=int(sigmoid))
+        want, size = OE.route_backward(x, ids, dw, None, sigmoid)
+        _within(_values(dl), want, 6 * _span(x) * size + TINY, "dlogits")
+
+
 # ------------------------------------------------------------------ rows --
 
 @pytest.mark.parametrize("n,E,align", [(0, 4, 128), (1, 1, 1), (1, 256, 128), (63, 5, 32), (128, 256, 1), (1000, 8, 128),
