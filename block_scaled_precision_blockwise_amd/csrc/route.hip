@@ -234,24 +234,28 @@ constexpr int kTop = 8;
 // e^x to a relative 2^-42 for x <= 0 or so: x = n ln 2 + r (ln 2 in two
 // pieces, the first of 36 bits, so that n times it is exact), the power series of
 // e^r to r^10 (|r| <= ln 2 / 2: the next term is below 2.3e-13).
-__device__ __forceinline__ double exp_near(double x) {
-  x = __builtin_fmax(x, -800.0);  // 2^-1154: zero either way
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = fma(n, -0x1.62e42fefa0000p-1, x);
-  r = fma(n, -0x1.cf79abc9e3b3ap-40, r);
-  double y = 1.0 / 3628800.0;
-  y = fma(y, r, 1.0 / 362880.0);
-  y = fma(y, r, 1.0 / 40320.0);
-  y = fma(y, r, 1.0 / 5040.0);
-  y = fma(y, r, 1.0 / 720.0);
-  y = fma(y, r, 1.0 / 120.0);
-  y = fma(y, r, 1.0 / 24.0);
-  y = fma(y, r, 1.0 / 6.0);
-  y = fma(y, r, 0.5);
-  y = fma(y, r, 1.0);
-  y = fma(y, r, 1.0);
-  return __builtin_ldexp(y, int(n));
-}
+struct ExpSeries {
+  double c[8];  // 1 / 10!, ..., 1 / 3!
+  __device__ ExpSeries()
+      : c{1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0} {
+    // kept in registers: as constants they would be moved there before each use
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("" : "+v"(c[i]));
+  }
+  __device__ __forceinline__ double operator()(double x) const {
+    x = __builtin_fmax(x, -800.0);  // 2^-1154: zero either way
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    double r = fma(n, -0x1.62e42fefa0000p-1, x);
+    r = fma(n, -0x1.cf79abc9e3b3ap-40, r);
+    double y = c[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) y = fma(y, r, c[i]);
+    y = fma(y, r, 0.5);
+    y = fma(y, r, 1.0);
+    y = fma(y, r, 1.0);
+    return __builtin_ldexp(y, int(n));
+  }
+};
 
 // 1 / d for 1 <= d < 2^1000: the hardware's start and one Newton step.
 __device__ __forceinline__ double recip_near(double d) {
@@ -260,9 +264,10 @@ __device__ __forceinline__ double recip_near(double d) {
 }
 
 constexpr double kFar = 690.0;
-__device__ __forceinline__ double sigmoid_near(double x) {
+__device__ __forceinline__ double sigmoid_near(const ExpSeries& exp_near, double x) {
   // 0 from e^690 on (kFar), where the true score is below 2^-995
-  return x < -kFar ? 0.0 : recip_near(1.0 + exp_near(-x));
+  const double p = recip_near(1.0 + exp_near(__builtin_fmin(-x, kFar)));
+  return x < -kFar ? 0.0 : p;
 }
 
 union Bits64 {
@@ -275,7 +280,9 @@ union Bits64 {
 // within rows of 16).
 template <int STEP>
 __device__ __forceinline__ uint32_t partner(uint32_t v) {
-  return dpp_mov<STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140>(v);
+  // quad permutations, then the half row and the row mirrored: every lane has a source
+  constexpr int kCtrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
+  return uint32_t(__builtin_amdgcn_mov_dpp(int(v), kCtrl, 0xF, 0xF, true));
 }
 // Both values of the pair, in an order that both lanes agree on or not (for
 // commutative use); steps 4 and 5 exchange rows and halves.
@@ -360,8 +367,9 @@ __device__ __attribute__((noinline)) void route_token_apart(RouteArgs a, int64_t
   route_token<BF16, EPL>(a, t, lane, cs);
 }
 
-template <int BF16, int L, int S>
+template <int BF16, int SIGMOID, int L, int S>
 __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
+  const ExpSeries exp_near;
   constexpr int kSlow = L * S / 64;  // scores per lane of the general path
   __shared__ double cs[4][64 * kSlow];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -386,9 +394,9 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
   // ---- scores
   double c[S];
   double top = 0.0, inv = 0.0;
-  if (a.sigmoid) {
+  if (SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) c[i] = sigmoid_near(double(x[i]));
+    for (int i = 0; i < S; ++i) c[i] = sigmoid_near(exp_near, double(x[i]));
   } else {
     float m = -INFINITY;
 #pragma unroll
@@ -398,7 +406,8 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       // a row of -inf alone has scores of zero
-      c[i] = x[i] == -INFINITY ? 0.0 : exp_near(double(x[i]) - top);
+      const double v = exp_near(double(x[i]) - top);
+      c[i] = x[i] == -INFINITY ? 0.0 : v;
       sum += c[i];
     }
     sum = lanes_sum<L>(sum);
@@ -423,10 +432,18 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
     }
   }
   // ---- what the choice goes by
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int q = 0; q < S / V; ++q) {
+      float b[V];
+      load4<0>(a.bias, g * per, at(q * V), per, whole, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[V * q + i] += double(b[i]);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     const int o = at(i);
-    if (a.bias != nullptr) c[i] += o < per ? double(a.bias[g * per + o]) : 0.0;
     // infinities stay numbers beside the expert's number; NaN comes last
     c[i] = __builtin_fmin(__builtin_fmax(c[i], kNever), -kNever);
     if (o >= per) c[i] = -INFINITY;
@@ -499,7 +516,7 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
   const float xm = logit_at<BF16>(a.logits, row + id);
   const double bm = a.bias != nullptr ? double(a.bias[id]) : 0.0;
   double p = 0.0;
-  if (on) p = a.sigmoid ? sigmoid_near(double(xm)) : xm == -INFINITY ? 0.0 : exp_near(double(xm) - top) * inv;
+  if (on) p = SIGMOID ? sigmoid_near(exp_near, double(xm)) : xm == -INFINITY ? 0.0 : exp_near(double(xm) - top) * inv;
   const double total = lanes_sum<16>(p);
 
   // ---- neighbours in the order, and the last against what was left out
@@ -507,7 +524,7 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
   const float x_next = __shfl_down(xm, 1);
   close |= l + 1 < a.k && next > kNever * 0.999 &&
                fabs(mine.d - next) <= (fabs(mine.d) + p + p_next) * 0x1p-38 && !(xm == x_next && bm == b_next);
-  close |= a.sigmoid && on && xm < -kFar && xm > -760.f;  // a weight of what sigmoid_near leaves out
+  close |= SIGMOID && on && xm < -kFar && xm > -760.f;  // a weight of what sigmoid_near leaves out
   if (last > kNever * 0.999) {
     const int from = (lane & ~(L - 1)) + a.k - 1;
     const double lim = last - (fabs(last) + (a.bias != nullptr ? 1.0 : 0.0)) * 0x1p-38;
@@ -776,8 +793,12 @@ bsq_status launch_route(const RouteLaunch& L, hipStream_t st) {
       const int64_t per = lanes == 16 ? 16 : 4, want = (L.T + per - 1) / per;
       const unsigned grid = unsigned(want);
       auto go = [&](auto l, auto s) {
-        if (L.bf16) hipLaunchKernelGGL((k_route_top<1, l.value, s.value>), grid, 256, 0, st, a);
-        else hipLaunchKernelGGL((k_route_top<0, l.value, s.value>), grid, 256, 0, st, a);
+        switch ((L.bf16 ? 1 : 0) | (L.sigmoid ? 2 : 0)) {
+          case 0: hipLaunchKernelGGL((k_route_top<0, 0, l.value, s.value>), grid, 256, 0, st, a); break;
+          case 1: hipLaunchKernelGGL((k_route_top<1, 0, l.value, s.value>), grid, 256, 0, st, a); break;
+          case 2: hipLaunchKernelGGL((k_route_top<0, 1, l.value, s.value>), grid, 256, 0, st, a); break;
+          default: hipLaunchKernelGGL((k_route_top<1, 1, l.value, s.value>), grid, 256, 0, st, a);
+        }
       };
       auto by_slots = [&](auto l) {
         if (slots <= 4) go(l, std::integral_constant<int, 4>{});
