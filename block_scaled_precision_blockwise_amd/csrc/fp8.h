@@ -112,4 +112,178 @@ __device__ __forceinline__ void store8(void* p, int64_t elem, const float (&v)[8
   }
 }
 
+// ------------------------------------- tiles written in both orientations --
+// A workgroup of 256 threads holds a 128 x 128 tile in LDS and writes its
+// codes transposed: eight lanes own a column, 16 rows (16 bytes) each, so
+// that one store instruction writes whole 128-byte lines; two neighbouring
+// lanes share a block of 32 rows.  Chunks of eight columns are XORed with the
+// lane's share of the rows, so that the 64 lanes' reads (8 columns x 8
+// shares) fall on 64 banks and the writers keep 16-byte stores.
+constexpr int kTile = 128;
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+__device__ __forceinline__ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The conversions below saturate (MODE.FP16_OVFL), so that an infinite value
+// takes the largest code, as the clamp of mx_encode4 gives it.
+__device__ __forceinline__ void saturate_fp8() { __builtin_amdgcn_s_setreg(1 | (23 << 6), 1); }
+
+// Four values times 2^-E as codes; `scale` is 2^E.  Two at a time in one
+// instruction, which rounds once, to nearest even.
+template <int CODE>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float scale) {
+  s16x2 q{};
+  if constexpr (CODE == 0) {
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, a, b, scale, false);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, c, d, scale, true);
+  } else {
+    q = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(q, a, b, scale, false);
+    q = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(q, c, d, scale, true);
+  }
+  return __builtin_bit_cast(uint32_t, q);
+}
+template <int CODE>
+__device__ __forceinline__ uint32_t encode4(uint32_t ab, uint32_t cd, float scale) {  // of bfloat16 pairs
+  const bf16x2 x = __builtin_bit_cast(bf16x2, ab), y = __builtin_bit_cast(bf16x2, cd);
+  s16x2 q{};
+  if constexpr (CODE == 0) {
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(q, x, scale, false);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(q, y, scale, true);
+  } else {
+    q = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(q, x, scale, false);
+    q = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(q, y, scale, true);
+  }
+  return __builtin_bit_cast(uint32_t, q);
+}
+__device__ __forceinline__ float power_of_two(int E) { return __uint_as_float(uint32_t(E + 127) << 23); }
+
+// Stores that nothing reads again soon: they leave the L2 to what is shared.
+__device__ __forceinline__ void stnt(void* p, uint32_t a, uint32_t b) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(u32x2_t{a, b}, static_cast<u32x2_t*>(p));
+}
+__device__ __forceinline__ void stnt(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  __builtin_nontemporal_store(u32x4_t{a, b, c, d}, static_cast<u32x4_t*>(p));
+}
+
+// Values of the lane N further on in the row of 16 (its first 16 - N lanes).
+template <int N>
+__device__ __forceinline__ uint32_t lane_ahead(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x100 + N, 0xF, 0xF, true));
+}
+
+// The scale of block f8 / 4 of a row of 16 lanes, four lanes to a block.  Where
+// the row's four blocks are all there and start a word, one lane writes the
+// word: a byte at a time cost 15 of 133 us.
+__device__ __forceinline__ void put_scale(uint8_t* scales, int64_t f8, bool in, bool words, int E) {
+  const uint32_t e = uint32_t(E + 127);
+  if (words) {
+    uint32_t w = e | (lane_ahead<4>(e) << 8);
+    w |= lane_ahead<8>(w) << 16;
+    if (in && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (f8 >> 2)) = w;
+  } else if (in && (f8 & 3) == 0) {
+    scales[f8 >> 2] = uint8_t(e);
+  }
+}
+
+// Eight neighbours of a row, four lanes to a block, 16 to the tile's row:
+// codes and scale (`words`: see put_scale).  The
+// values are floats, or four words of bfloat16 pairs.  Every lane of the wave
+// takes part in the maximum; `in` guards the stores.
+template <int CODE>
+__device__ __forceinline__ void put_row(uint8_t* codes, uint8_t* scales, int64_t f8, bool in, bool words,
+                                        const float (&x)[8]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
+  const int E = mx_exponent<CODE == 0 ? 8 : 15>(__uint_as_float(group_max_bits<4>(m)));
+  const float s = power_of_two(E);
+  put_scale(scales, f8, in, words, E);
+  if (in) stnt(codes + 8 * f8, encode4<CODE>(x[0], x[1], x[2], x[3], s), encode4<CODE>(x[4], x[5], x[6], x[7], s));
+}
+template <int CODE>
+__device__ __forceinline__ void put_row(uint8_t* codes, uint8_t* scales, int64_t f8, bool in, bool words,
+                                        const uint32_t (&x)[4]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_u16x2(m, x[i] & 0x7FFF7FFFu);
+  m = group_max_bits<4>(max(m & 0xFFFFu, m >> 16));
+  const int E = mx_exponent<CODE == 0 ? 8 : 15>(decode_bf16(m));
+  const float s = power_of_two(E);
+  put_scale(scales, f8, in, words, E);
+  if (in) stnt(codes + 8 * f8, encode4<CODE>(x[0], x[1], s), encode4<CODE>(x[2], x[3], s));
+}
+
+// Where tile keeps eight columns from 8 c8 of row `r` (a float each), or of
+// the pair of rows `r` (one word, the even row in the low half).
+template <int PAIRS>
+__device__ __forceinline__ int tile_at(int r, int c8) {
+  return r * kTile + 8 * (c8 ^ ((r >> (PAIRS ? 3 : 4)) & 7));
+}
+
+// The tile at rows r0 .., columns c0 .. as codes_t [cols, rows].
+template <int CODE, int PAIRS>
+__device__ __forceinline__ void put_columns(const uint32_t* tile, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
+                                            uint8_t* codes_t, uint8_t* scales_t) {
+  constexpr int EMAX = CODE == 0 ? 8 : 15;
+  const int share = threadIdx.x & 7;
+  const int64_t r = r0 + 16 * share;
+  const bool words = rows % kTile == 0 && aligned4(scales_t);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int oc = (threadIdx.x >> 3) + 32 * it;
+    const int64_t c = c0 + oc;
+    const bool in = r < rows && c < cols;
+    uint32_t q[4];
+    int E;
+    if constexpr (PAIRS) {
+      uint32_t x[8], m = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = tile[tile_at<1>(8 * share + i, oc >> 3) + (oc & 7)];
+        m = max_u16x2(m, x[i] & 0x7FFF7FFFu);
+      }
+      E = mx_exponent<EMAX>(decode_bf16(group_max_bits<2>(max(m & 0xFFFFu, m >> 16))));
+      const float s = power_of_two(E);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = encode4<CODE>(x[2 * i], x[2 * i + 1], s);
+    } else {
+      float x[16];
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = __uint_as_float(tile[tile_at<0>(16 * share + i, oc >> 3) + (oc & 7)]);
+        m = max(m, abs_bits(x[i]));
+      }
+      E = mx_exponent<EMAX>(__uint_as_float(group_max_bits<2>(m)));
+      const float s = power_of_two(E);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = encode4<CODE>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], s);
+    }
+    if (words) {
+      const uint32_t e = uint32_t(E + 127);
+      uint32_t w = e | (lane_ahead<2>(e) << 8);
+      w |= lane_ahead<4>(w) << 16;
+      if (in && share == 0) *reinterpret_cast<uint32_t*>(scales_t + c * (rows / 32) + r / 32) = w;
+    } else if (in && (share & 1) == 0) {
+      scales_t[c * (rows / 32) + r / 32] = uint8_t(E + 127);
+    }
+    if (in) stnt(codes_t + c * rows + r, q[0], q[1], q[2], q[3]);
+  }
+}
+
+// Tile number of workgroup L of n: workgroups are dealt to the 8 XCDs
+// round-robin, and XCD x takes the x-th contiguous eighth of the tiles.
+__device__ __forceinline__ int64_t xcd_run(int64_t L, int64_t n) {
+  const int64_t per = n / 8;
+  return L < 8 * per ? (L & 7) * per + (L >> 3) : L;
+}
+
 }  // namespace bsq

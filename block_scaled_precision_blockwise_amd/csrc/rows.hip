@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(PlanArgs a) {
   extern __shared__ int lds[];
   int* const wcnt = lds;                          // [kPlanWaves][E]
   int* const base = lds + kPlanWaves * a.E;       // [E] next row of each expert in this workgroup
-  int64_t* const part = reinterpret_cast<int64_t*>(lds + ((kPlanWaves + 1) * a.E + 1) / 2 * 2);  // [kPlanWaves]
+  int64_t* const part_sum = reinterpret_cast<int64_t*>(lds + ((kPlanWaves + 1) * a.E + 1) / 2 * 2);
   const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
   const int E = a.E, nb = gridDim.x, me = blockIdx.x;
   const int nt = blockDim.x, nw = nt >> 6;
@@ -76,41 +76,58 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(PlanArgs a) {
     }
     __syncthreads();
   }
+  // totals of all workgroups and of the earlier ones: a power of two of
+  // threads per expert, each over its share of the workgroups
+  int* const sums = lds;  // total [E], before [E]
   int total = 0, before = 0;
-  if (tid < E) {
-    if (ONE) {
-      total = base[tid];
-    } else {
-      for (int b = 0; b < nb; ++b) {
-        const int c = a.space[int64_t(b) * E + tid];
+  if (ONE) {
+    if (tid < E) total = base[tid];
+  } else {
+    const int x = tid & ((1 << a.bits) - 1), part = tid >> a.bits, parts = nt >> a.bits;
+    for (int e = tid; e < 2 * E; e += nt) sums[e] = 0;
+    __syncthreads();
+    if (x < E) {
+      for (int b = part; b < nb; b += parts) {
+        const int c = a.space[int64_t(b) * E + x];
         total += c;
         before += b < me ? c : 0;
       }
+      atomicAdd(&sums[x], total);
+      atomicAdd(&sums[E + x], before);
     }
+    __syncthreads();
+    total = tid < E ? sums[tid] : 0;
+    before = tid < E ? sums[E + tid] : 0;
+    __syncthreads();
   }
   // first rows: the sum of the earlier experts' segments
   const int64_t held = tid < E ? (int64_t(total) + a.align - 1) / a.align * a.align : 0;
   const int64_t in = wave_scan(held, lane);
-  if (lane == 63) part[w] = in;
+  if (lane == 63) part_sum[w] = in;
   __syncthreads();
   int64_t first = in - held, all = 0;
   for (int v = 0; v < nw; ++v) {
-    if (v < w) first += part[v];
-    all += part[v];
+    if (v < w) first += part_sum[v];
+    all += part_sum[v];
   }
+  int* const hole = lds;  // first and past-the-end row without a choice, of each expert
   if (tid < E) {
     base[tid] = int(first) + before;
+    hole[tid] = int(first) + total;
+    hole[E + tid] = int(first + held);
     if (me == 0) {
       a.offsets[tid] = int(first);
       a.counts[tid] = total;
       if (tid == E - 1) a.offsets[E] = int(all);
     }
-    // the segment's rows without a choice
-    if (tid % nb == me)
-      for (int64_t r = first + total; r < first + held; ++r)
-        if (r < a.cap) a.rows[r] = -1;
   }
+  __syncthreads();
+  if (a.align > 1)
+    for (int e = me * nw + w; e < E; e += nb * nw)
+      for (int64_t r = int64_t(hole[e]) + lane; r < hole[E + e]; r += 64)
+        if (r < a.cap) a.rows[r] = -1;
   for (int64_t r = all + int64_t(me) * nt + tid; r < a.cap; r += int64_t(nb) * nt) a.rows[r] = -1;
+  __syncthreads();
 
   for (int64_t i0 = begin; i0 < end; i0 += nt) {
     for (int e = tid; e < nw * E; e += nt) wcnt[e] = 0;
@@ -152,37 +169,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(PlanArgs a) {
 // ----------------------------------------------------------------- gather --
 // Rows of x in the experts' order as 8-bit operands: along rows for the
 // product, and transposed, in blocks of 32 rows, for the weight gradient.
-// A workgroup takes 128 rows x 64 columns; the values go through LDS once,
-// so that x is read once for both and a line of the transposed codes is
-// written whole.  Rows without a choice are zeros.
-constexpr int kTR = 128, kTC = 64;
-
-// One 32-row block of a column per thread: codes and scale of rows
-// r0 + 32 seg .. + 31 of column c0 + oc, transposed.
-template <int CODE>
-__device__ __forceinline__ void put_transposed(const float (*tile)[kTC + 1], int64_t r0, int64_t c0, int64_t rows,
-                                               int64_t cols, uint8_t* codes_t, uint8_t* scales_t) {
-  constexpr int EMAX = CODE == 0 ? 8 : 15;
-  const int oc = threadIdx.x >> 2, seg = threadIdx.x & 3;
-  const int64_t r = r0 + 32 * seg, c = c0 + oc;
-  if (r >= rows || c >= cols) return;
-  float x[32];
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    x[i] = tile[32 * seg + i][oc];
-    m = max(m, abs_bits(x[i]));
-  }
-  const int E = mx_exponent<EMAX>(__uint_as_float(m));
-  uint32_t q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = mx_encode4<CODE>(&x[4 * i], E);
-  uint4* o = reinterpret_cast<uint4*>(codes_t + c * rows + r);
-  o[0] = make_uint4(q[0], q[1], q[2], q[3]);
-  o[1] = make_uint4(q[4], q[5], q[6], q[7]);
-  scales_t[c * (rows / 32) + r / 32] = uint8_t(E + 127);
-}
-
+// A workgroup takes 128 rows x 128 columns; the values go through LDS once,
+// so that x is read once for both.  Bfloat16 values without weights stay
+// pairs of 16 bits throughout (the hardware converts a pair under a block
+// scale in one instruction), else they are float32.  Rows without a choice
+// are zeros.
 struct GatherArgs {
   int64_t T, H, cap;
   int k;
@@ -192,43 +183,86 @@ struct GatherArgs {
   uint8_t *codes, *scales, *codes_t, *scales_t;
 };
 
-template <int SRC_BF16, int CODE>
+template <int SRC_BF16, int PAIRS, int CODE>
 __global__ void __launch_bounds__(256) k_gather_mx(GatherArgs a) {
-  constexpr int EMAX = CODE == 0 ? 8 : 15;
-  __shared__ float tile[kTR][kTC + 1];
-  const int64_t tiles_c = (a.H + kTC - 1) / kTC;
-  const int64_t r0 = int64_t(blockIdx.x) / tiles_c * kTR, c0 = int64_t(blockIdx.x) % tiles_c * kTC;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * kTile / (PAIRS ? 2 : 1)];
+  __shared__ int src[kTile];
+  __shared__ float wt[kTile];
+  const int64_t tiles_r = (a.cap + kTile - 1) / kTile;
+  const int64_t t = xcd_run(blockIdx.x, gridDim.x);
+  const int64_t r0 = t % tiles_r * kTile, c0 = t / tiles_r * kTile;
   const int tx = threadIdx.x;
+  if (tx < kTile) {
+    int at = r0 + tx < a.cap ? a.rows[r0 + tx] : -1;
+    int from = at >= 0 ? at / a.k : -1;
+    if (from >= a.T) from = -1;
+    src[tx] = from;
+    if (!PAIRS) wt[tx] = from >= 0 && a.weights != nullptr ? a.weights[at] : 1.0f;
+  }
+  saturate_fp8();
+  __syncthreads();
+  const int c8 = tx & 15;
+  const int64_t c = c0 + 8 * c8;
+  const bool words = a.H % kTile == 0 && aligned4(a.scales);
+  if constexpr (PAIRS) {
+    uint4 v[4][2];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int r = (tx >> 3) + 32 * s, cg = (tx & 7) * 8;
-    const bool in = r0 + r < a.cap && c0 + cg < a.H;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int at = in ? a.rows[r0 + r] : -1;
-    const int64_t t = at >= 0 ? at / a.k : a.T;
-    if (t < a.T) {
-      load8<SRC_BF16>(a.x, t * a.H + c0 + cg, x);
-      if (a.weights != nullptr) {
-        const float wt = a.weights[at];
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= wt;
+      for (int h = 0; h < 2; ++h) {
+        const int from = src[2 * ((tx >> 4) + 16 * s) + h];
+        v[s][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (from >= 0 && c < a.H)
+          v[s][h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + from * a.H + c);
+      }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int rp = (tx >> 4) + 16 * s;
+      const uint32_t lo[4] = {v[s][0].x, v[s][0].y, v[s][0].z, v[s][0].w};
+      const uint32_t hi[4] = {v[s][1].x, v[s][1].y, v[s][1].z, v[s][1].w};
+      const int64_t r = r0 + 2 * rp;
+      if (a.codes != nullptr) {
+        put_row<CODE>(a.codes, a.scales, (r * a.H + c) / 8, r < a.cap && c < a.H, words, lo);
+        put_row<CODE>(a.codes, a.scales, ((r + 1) * a.H + c) / 8, r + 1 < a.cap && c < a.H, words, hi);
+      }
+      if (a.codes_t != nullptr) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = __builtin_amdgcn_perm(hi[i], lo[i], 0x05040100u);      // column 2 i of both rows
+          w[2 * i + 1] = __builtin_amdgcn_perm(hi[i], lo[i], 0x07060302u);  // column 2 i + 1
+        }
+        uint4* o = reinterpret_cast<uint4*>(tile + tile_at<1>(rp, c8));
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
-    uint32_t m = 0u;
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
-    const int E = mx_exponent<EMAX>(__uint_as_float(group_max_bits<4>(m)));
-    if (in && a.codes != nullptr) {
-      const int64_t f = ((r0 + r) * a.H + c0 + cg) / 8;
-      reinterpret_cast<uint2*>(a.codes)[f] = make_uint2(mx_encode4<CODE>(&x[0], E), mx_encode4<CODE>(&x[4], E));
-      if ((tx & 3) == 0) a.scales[f >> 2] = uint8_t(E + 127);
+    for (int s = 0; s < 8; ++s) {
+      const int rr = (tx >> 4) + 16 * s;
+      const int64_t r = r0 + rr;
+      const int from = src[rr];
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (from >= 0 && c < a.H) {
+        load8<SRC_BF16>(a.x, from * a.H + c, x);
+        if (a.weights != nullptr) {
+          const float f = wt[rr];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= f;
+        }
+      }
+      if (a.codes != nullptr) put_row<CODE>(a.codes, a.scales, (r * a.H + c) / 8, r < a.cap && c < a.H, words, x);
+      if (a.codes_t != nullptr) {
+        float4* o = reinterpret_cast<float4*>(tile + tile_at<0>(rr, c8));
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) tile[r][cg + i] = x[i];
   }
   if (a.codes_t == nullptr) return;
   __syncthreads();
-  put_transposed<CODE>(tile, r0, c0, a.cap, a.H, a.codes_t, a.scales_t);
+  put_columns<CODE, PAIRS>(tile, r0, c0, a.cap, a.H, a.codes_t, a.scales_t);
 }
 
 // ---------------------------------------------------------------- combine --
@@ -315,12 +349,15 @@ bsq_status launch_gather_mx(int64_t T, int64_t H, int64_t cap, int k, const void
                             const float* weights, bool e5m2, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
                             uint8_t* scales_t, hipStream_t st) {
   const GatherArgs a{T, H, cap, k, x, rows, weights, codes, scales, codes_t, scales_t};
-  const unsigned grid = unsigned(((cap + kTR - 1) / kTR) * ((H + kTC - 1) / kTC));
-  switch ((bf16 ? 1 : 0) | (e5m2 ? 2 : 0)) {
-    case 0: hipLaunchKernelGGL((k_gather_mx<0, 0>), grid, 256, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((k_gather_mx<1, 0>), grid, 256, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_gather_mx<0, 1>), grid, 256, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_gather_mx<1, 1>), grid, 256, 0, st, a);
+  const unsigned grid = unsigned(((cap + kTile - 1) / kTile) * ((H + kTile - 1) / kTile));
+  const int form = !bf16 ? 0 : weights != nullptr ? 1 : 2;
+  switch (form | (e5m2 ? 4 : 0)) {
+    case 0: hipLaunchKernelGGL((k_gather_mx<0, 0, 0>), grid, 256, 0, st, a); break;
+    case 1: hipLaunchKernelGGL((k_gather_mx<1, 0, 0>), grid, 256, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((k_gather_mx<1, 1, 0>), grid, 256, 0, st, a); break;
+    case 4: hipLaunchKernelGGL((k_gather_mx<0, 0, 1>), grid, 256, 0, st, a); break;
+    case 5: hipLaunchKernelGGL((k_gather_mx<1, 0, 1>), grid, 256, 0, st, a); break;
+    default: hipLaunchKernelGGL((k_gather_mx<1, 1, 1>), grid, 256, 0, st, a);
   }
   return launch_status("moe_gather_mx");
 }

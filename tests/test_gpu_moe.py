@@ -375,6 +375,50 @@ def test_gather(T, H, E, k, align, bf16, e5m2, weighted):
         assert_bytes_equal(host(g), r, name + " alone")
 
 
+@pytest.mark.parametrize("e5m2", [False, True])
+@pytest.mark.parametrize("bf16,order", [(True, "pattern"), (True, "mixed"), (False, "mixed")])
+def test_gather_codes_every_value_as_the_quantizer_does(e5m2, bf16, order):
+    """Every bfloat16 but NaN (infinities among them), next to its neighbours
+    and next to any other, along rows and down columns."""
+    torch = _torch()
+    say("gather every value", e5m2, bf16, order)
+    bits = np.arange(65536, dtype=np.uint32)
+    bits = bits[(bits & 0x7FFF) <= 0x7F80]
+    bits = np.concatenate([bits, bits[:-len(bits) % 4096 or None][: -len(bits) % 4096]]).astype(np.uint16)
+    if order == "mixed":
+        bits = np.random.default_rng(1).permutation(bits)
+    T, H = len(bits) // 64, 64
+    x = to_dev(bits.view(np.int16).reshape(T, H)).view(torch.bfloat16)
+    if not bf16:
+        x = x.float()
+    cd = bsq.BSQ_E5M2 if e5m2 else bsq.BSQ_E4M3
+    rows = torch.arange(T, dtype=torch.int32, device="cuda")
+    shapes = ((T, H), (T, H // 32), (H, T), (H, T // 32))
+    got, want = ([filled(s, torch.uint8, 0x55) for s in shapes] for _ in range(2))
+    bsq.bsq_moe_gather_mx(x, rows, 1, *got, code_dtype=cd)
+    bsq.bsq_quant_mx(x, want[0], want[1], 1, cd)
+    bsq.bsq_quant_mx(x, want[2], want[3], 0, cd)
+    for name, g, r in zip(("codes", "scales", "codes_t", "scales_t"), got, want):
+        assert_bytes_equal(host(g), host(r), name)
+
+
+@pytest.mark.parametrize("T,H,k,bf16,weighted", [(300, 416, 2, True, False), (300, 416, 2, True, True),
+                                                 (1000, 160, 3, False, False), (257, 128, 1, True, False)])
+def test_gather_over_several_tiles(T, H, k, bf16, weighted):
+    torch = _torch()
+    say("gather tiles", T, H, k, bf16, weighted)
+    ids, cap, offsets, counts, rows, pos = _planned(T, 5, k, 32, T + H, none=0.1)
+    rng = np.random.default_rng(T)
+    dx, xv = _dev_values(rng.standard_normal((T, H)) * np.exp(rng.uniform(-8, 8, (T, 1))), bf16)
+    w = rng.random((T, k)).astype(np.float32) if weighted else None
+    v = OE.gather(xv.astype(np.float32), rows, k, w)
+    want = (*OQ.mx_axis(v, 1, F.E4M3), *OQ.mx_axis(v, 0, F.E4M3))
+    outs = [filled(s.shape, torch.uint8, 0x55) for s in want]
+    bsq.bsq_moe_gather_mx(dx, to_dev(rows), k, *outs, weights=None if w is None else to_dev(w))
+    for name, g, r in zip(("codes", "scales", "codes_t", "scales_t"), outs, want):
+        assert_bytes_equal(host(g), r, name)
+
+
 def test_gather_of_rows_that_point_nowhere():
     torch = _torch()
     say("gather nowhere")
