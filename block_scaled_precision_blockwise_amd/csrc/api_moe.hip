@@ -279,7 +279,7 @@ bsq_status bsq_swiglu_mx(int64_t R, int64_t F, const void* gu, int gu_dtype, int
   BSQ_CHECK(ht == nullptr || R % 32 == 0, BSQ_ERR_SHAPE, "R must be a multiple of 32 for the transposed codes");
   BSQ_CHECK((ht == nullptr) == (ht_scales == nullptr) && (kept == nullptr) == (kept_scales == nullptr), BSQ_ERR_NULL,
             "codes and their scales come together");
-  BSQ_CHECK(((R + 127) / 128) * ((F + 63) / 64) <= kMaxInt, BSQ_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles");
+  BSQ_CHECK(R <= kMaxInt * 2048 / (F < 1 ? 1 : F), BSQ_ERR_UNSUPPORTED, "more than 2^31 - 1 workgroups");
   if (R == 0 || F == 0) return ok();
   BSQ_CHECK_PTR(gu);
   BSQ_CHECK_PTR(h);

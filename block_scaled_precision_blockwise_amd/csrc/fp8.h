@@ -173,6 +173,22 @@ __device__ __forceinline__ void stnt(void* p, uint32_t a, uint32_t b, uint32_t c
   __builtin_nontemporal_store(u32x4_t{a, b, c, d}, static_cast<u32x4_t*>(p));
 }
 
+// store8 as such a store.
+template <int BF16>
+__device__ __forceinline__ void store8nt(void* p, int64_t elem, const float (&v)[8]) {
+  if (BF16) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = encode_bf16(v[2 * i]) | (encode_bf16(v[2 * i + 1]) << 16);
+    stnt(static_cast<uint16_t*>(p) + elem, u[0], u[1], u[2], u[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      stnt(static_cast<float*>(p) + elem + 4 * i, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+  }
+}
+
 // Values of the lane N further on in the row of 16 (its first 16 - N lanes).
 template <int N>
 __device__ __forceinline__ uint32_t lane_ahead(uint32_t v) {

@@ -6,14 +6,25 @@
 #include "fp8.h"
 #include "moe.h"
 
+#include <type_traits>
+
 namespace bsq {
 
 namespace {
 
-constexpr int kTR = 128, kTC = 64;
-
-// 1 / (1 + e^-g) in float32; e^-g = inf gives 0.
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// 1 / (1 + e^-g) in float32 within 4 steps of 2^-23: -g log2 e in two pieces
+// (the hardware's 2^t of the first, times 1 + ln 2 of the second), and the
+// hardware's reciprocal, of a sixteenth of the sum so that a result near
+// 2^-126 is not flushed.  e^-g = inf gives 0.  9 instructions; the library's
+// expf and division took 40, and with them the training pass was bound by
+// instruction issue.
+__device__ __forceinline__ float sigmoid(float g) {
+  constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;  // log2 e = kLog2e + kRest
+  const float t = -g * kLog2e;
+  const float lo = fmaf(-g, kRest, fmaf(-g, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * fmaf(lo, 0x1.62e43p-1f, 1.0f);
+  return __builtin_amdgcn_rcpf(fmaf(e, 0.0625f, 0.0625f)) * 0.0625f;
+}
 
 struct GateArgs {
   int64_t R, F;
@@ -21,66 +32,115 @@ struct GateArgs {
   uint8_t *h, *hs, *ht, *hts, *kept, *kepts;
 };
 
-template <int CODE>
-__device__ __forceinline__ void put_row8(uint8_t* codes, uint8_t* scales, int64_t f8, const float (&x)[8], bool in) {
-  constexpr int EMAX = CODE == 0 ? 8 : 15;
-  uint32_t m = 0u;
+// Eight columns of g, from element `at` of gu, and of u as loaded (zeros where
+// not `in`).
+template <int SRC_BF16>
+struct Raw {
+  uint4 g[SRC_BF16 ? 1 : 2], u[SRC_BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const GateArgs& a, int64_t at, bool in) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
-  const int E = mx_exponent<EMAX>(__uint_as_float(group_max_bits<4>(m)));
-  if (!in) return;
-  reinterpret_cast<uint2*>(codes)[f8] = make_uint2(mx_encode4<CODE>(&x[0], E), mx_encode4<CODE>(&x[4], E));
-  if ((f8 & 3) == 0) scales[f8 >> 2] = uint8_t(E + 127);
+    for (int i = 0; i < (SRC_BF16 ? 1 : 2); ++i) {
+      g[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (in) {
+        const char* p = static_cast<const char*>(a.gu) + at * (SRC_BF16 ? 2 : 4) + 16 * i;
+        g[i] = ldnt(reinterpret_cast<const uint4*>(p));
+        u[i] = ldnt(reinterpret_cast<const uint4*>(p + a.F * (SRC_BF16 ? 2 : 4)));
+      }
+    }
+  }
+};
+__device__ __forceinline__ void widen(const uint32_t (&w)[4], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = decode_bf16(w[i] & 0xFFFFu);
+    x[2 * i + 1] = decode_bf16(w[i] >> 16);
+  }
+}
+
+// Writes the checkpoint's codes of those columns and, from element `out` on,
+// h's, 16 lanes to 128 columns, and leaves h in x.
+template <int SRC_BF16, int CODE>
+__device__ __forceinline__ void gate8(const GateArgs& a, const Raw<SRC_BF16>& raw, int64_t at, int64_t out,
+                                      bool in, bool words, float (&x)[8]) {
+  float g[8], u[8];
+  if constexpr (SRC_BF16) {
+    const uint32_t gw[4] = {raw.g[0].x, raw.g[0].y, raw.g[0].z, raw.g[0].w};
+    const uint32_t uw[4] = {raw.u[0].x, raw.u[0].y, raw.u[0].z, raw.u[0].w};
+    if (a.kept != nullptr) {
+      put_row<CODE>(a.kept, a.kepts, at / 8, in, words, gw);
+      put_row<CODE>(a.kept, a.kepts, (at + a.F) / 8, in, words, uw);
+    }
+    widen(gw, g);
+    widen(uw, u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 &gq = raw.g[i / 4], &uq = raw.u[i / 4];
+      g[i] = __uint_as_float(i % 4 == 0 ? gq.x : i % 4 == 1 ? gq.y : i % 4 == 2 ? gq.z : gq.w);
+      u[i] = __uint_as_float(i % 4 == 0 ? uq.x : i % 4 == 1 ? uq.y : i % 4 == 2 ? uq.z : uq.w);
+    }
+    if (a.kept != nullptr) {
+      put_row<CODE>(a.kept, a.kepts, at / 8, in, words, g);
+      put_row<CODE>(a.kept, a.kepts, (at + a.F) / 8, in, words, u);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = g[i] * sigmoid(g[i]) * u[i];
+  put_row<CODE>(a.h, a.hs, out / 8, in, words, x);
+}
+
+// Without the transposed operand: a stream of rows, eight columns per thread.
+template <int SRC_BF16, int CODE>
+__global__ void __launch_bounds__(256) k_swiglu_mx_rows(GateArgs a) {
+  saturate_fp8();
+  const int64_t f8 = a.F / 8, f = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const bool in = f < a.R * f8, words = a.F % kTile == 0 && aligned4(a.hs) && aligned4(a.kepts);
+  const int64_t r = in ? f / f8 : 0, c = in ? (f - r * f8) * 8 : 0;
+  Raw<SRC_BF16> raw;
+  raw.load(a, r * 2 * a.F + c, in);
+  float x[8];
+  gate8<SRC_BF16, CODE>(a, raw, r * 2 * a.F + c, r * a.F + c, in, words, x);
 }
 
 template <int SRC_BF16, int CODE>
 __global__ void __launch_bounds__(256) k_swiglu_mx(GateArgs a) {
-  constexpr int EMAX = CODE == 0 ? 8 : 15;
-  __shared__ float tile[kTR][kTC + 1];
-  const int64_t tiles_c = (a.F + kTC - 1) / kTC;
-  const int64_t r0 = int64_t(blockIdx.x) / tiles_c * kTR, c0 = int64_t(blockIdx.x) % tiles_c * kTC;
-  const int tx = threadIdx.x;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * kTile];
+  const int64_t tiles_c = (a.F + kTile - 1) / kTile;
+  const int64_t t = xcd_run(blockIdx.x, gridDim.x);
+  const int64_t r0 = t / tiles_c * kTile, c0 = t % tiles_c * kTile;
+  const int tx = threadIdx.x, c8 = tx & 15;
+  const int64_t c = c0 + 8 * c8;
+  const bool words = a.F % kTile == 0 && aligned4(a.hs) && aligned4(a.kepts);
+  saturate_fp8();
+  // every load first: 64 KiB of LDS leave two workgroups to a CU, so each
+  // has to keep its whole tile in flight
+  constexpr int kAhead = SRC_BF16 ? 8 : 4;
+  const int64_t out0 = (r0 + (tx >> 4)) * a.F + c, at0 = 2 * out0 - c;
+  auto rows = [&](auto whole) {  // whole: no column or row of the tile is outside
+    constexpr bool kWhole = decltype(whole)::value;
+    for (int s0 = 0; s0 < 8; s0 += kAhead) {
+      Raw<SRC_BF16> raw[kAhead];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int r = (tx >> 3) + 32 * s, cg = (tx & 7) * 8;
-    const bool in = r0 + r < a.R && c0 + cg < a.F;
-    float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int64_t at = (r0 + r) * 2 * a.F + c0 + cg;
-    if (in) {
-      load8<SRC_BF16>(a.gu, at, g);
-      load8<SRC_BF16>(a.gu, at + a.F, u);
+      for (int s = 0; s < kAhead; ++s) {
+        const int rr = (tx >> 4) + 16 * (s0 + s);
+        raw[s].load(a, at0 + 32 * (s0 + s) * a.F, kWhole || (r0 + rr < a.R && c < a.F));
+      }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int rr = (tx >> 4) + 16 * (s0 + s);
+        float x[8];
+        gate8<SRC_BF16, CODE>(a, raw[s], at0 + 32 * (s0 + s) * a.F, out0 + 16 * (s0 + s) * a.F,
+                              kWhole || (r0 + rr < a.R && c < a.F), words, x);
+        float4* o = reinterpret_cast<float4*>(tile + tile_at<0>(rr, c8));
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+      }
     }
-    if (a.kept != nullptr) {
-      put_row8<CODE>(a.kept, a.kepts, at / 8, g, in);
-      put_row8<CODE>(a.kept, a.kepts, (at + a.F) / 8, u, in);
-    }
-    float h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
-    put_row8<CODE>(a.h, a.hs, ((r0 + r) * a.F + c0 + cg) / 8, h, in);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) tile[r][cg + i] = h[i];
-  }
-  if (a.ht == nullptr) return;
+  };
+  if (r0 + kTile <= a.R && c0 + kTile <= a.F) rows(std::true_type{});
+  else rows(std::false_type{});
   __syncthreads();
-  const int oc = tx >> 2, seg = tx & 3;
-  const int64_t r = r0 + 32 * seg, c = c0 + oc;
-  if (r >= a.R || c >= a.F) return;
-  float x[32];
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    x[i] = tile[32 * seg + i][oc];
-    m = max(m, abs_bits(x[i]));
-  }
-  const int E = mx_exponent<EMAX>(__uint_as_float(m));
-  uint32_t q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = mx_encode4<CODE>(&x[4 * i], E);
-  uint4* o = reinterpret_cast<uint4*>(a.ht + c * a.R + r);
-  o[0] = make_uint4(q[0], q[1], q[2], q[3]);
-  o[1] = make_uint4(q[4], q[5], q[6], q[7]);
-  a.hts[c * (a.R / 32) + r / 32] = uint8_t(E + 127);
+  put_columns<CODE, 0>(tile, r0, c0, a.R, a.F, a.ht, a.hts);
 }
 
 // ------------------------------------------------------------- gradient --
@@ -122,8 +182,8 @@ __global__ void __launch_bounds__(256) k_swiglu_mx_backward(GateBwdArgs a) {
       du[i] = dh[i] * g[i] * s;
       dg[i] = dh[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
     }
-    store8<BF16>(a.dgu, gi * 8, dg);
-    store8<BF16>(a.dgu, ui * 8, du);
+    store8nt<BF16>(a.dgu, gi * 8, dg);
+    store8nt<BF16>(a.dgu, ui * 8, du);
   }
 }
 
@@ -132,8 +192,19 @@ __global__ void __launch_bounds__(256) k_swiglu_mx_backward(GateBwdArgs a) {
 bsq_status launch_swiglu_mx(int64_t R, int64_t F, const void* gu, bool bf16, bool e5m2, uint8_t* h, uint8_t* h_scales,
                             uint8_t* ht, uint8_t* ht_scales, uint8_t* kept, uint8_t* kept_scales, hipStream_t st) {
   const GateArgs a{R, F, gu, h, h_scales, ht, ht_scales, kept, kept_scales};
-  const unsigned grid = unsigned(((R + kTR - 1) / kTR) * ((F + kTC - 1) / kTC));
-  switch ((bf16 ? 1 : 0) | (e5m2 ? 2 : 0)) {
+  const int form = (bf16 ? 1 : 0) | (e5m2 ? 2 : 0);
+  if (ht == nullptr) {
+    const unsigned grid = unsigned((R * (F / 8) + 255) / 256);
+    switch (form) {
+      case 0: hipLaunchKernelGGL((k_swiglu_mx_rows<0, 0>), grid, 256, 0, st, a); break;
+      case 1: hipLaunchKernelGGL((k_swiglu_mx_rows<1, 0>), grid, 256, 0, st, a); break;
+      case 2: hipLaunchKernelGGL((k_swiglu_mx_rows<0, 1>), grid, 256, 0, st, a); break;
+      default: hipLaunchKernelGGL((k_swiglu_mx_rows<1, 1>), grid, 256, 0, st, a);
+    }
+    return launch_status("swiglu_mx");
+  }
+  const unsigned grid = unsigned(((R + kTile - 1) / kTile) * ((F + kTile - 1) / kTile));
+  switch (form) {
     case 0: hipLaunchKernelGGL((k_swiglu_mx<0, 0>), grid, 256, 0, st, a); break;
     case 1: hipLaunchKernelGGL((k_swiglu_mx<1, 0>), grid, 256, 0, st, a); break;
     case 2: hipLaunchKernelGGL((k_swiglu_mx<0, 1>), grid, 256, 0, st, a); break;

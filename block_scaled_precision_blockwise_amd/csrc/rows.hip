@@ -298,27 +298,44 @@ __global__ void __launch_bounds__(256) k_combine(CombineArgs a) {
   }
 }
 
-// dweights[t, j] = y[pos[t, j]] . dout[t], one wave per token.
+// dweights[t, j] = y[pos[t, j]] . dout[t], one wave per token; kBatch choices
+// at a time, so that dout is read once for them and their rows' loads are all
+// under way together.
+constexpr int kBatch = 8;
 template <int BF16>
 __global__ void __launch_bounds__(256) k_combine_backward(CombineArgs a) {
   const int lane = threadIdx.x & 63;
-  for (int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); t < a.T; t += int64_t(gridDim.x) * 4) {
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t r = a.pos[t * a.k + j];
-      float s = 0.f;
-      if (r >= 0 && r < a.cap) {
-        for (int64_t c = lane * 8; c < a.H; c += 512) {
-          float y[8], d[8];
-          load8<BF16>(a.y, r * a.H + c, y);
-          load8<BF16>(a.dout, t * a.H + c, d);
+  const int64_t t = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.T) return;
+  for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+    int64_t row[kBatch];
+    float s[kBatch];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s = fmaf(y[i], d[i], s);
-        }
-      }
-#pragma unroll
-      for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
-      if (lane == 0) static_cast<float*>(a.out)[t * a.k + j] = s;
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = j0 + j < a.k ? a.pos[t * a.k + j0 + j] : -1;
+      row[j] = r >= 0 && r < a.cap ? int64_t(r) : -1;
+      s[j] = 0.f;
     }
+    for (int64_t c = lane * 8; c < a.H; c += 512) {
+      float d[8], y[kBatch][8];
+      load8<BF16>(a.dout, t * a.H + c, d);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (row[j] >= 0) load8<BF16>(a.y, row[j] * a.H + c, y[j]);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (row[j] >= 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[j] = fmaf(y[j][i], d[i], s[j]);
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+      for (int m = 32; m > 0; m >>= 1) s[j] += __shfl_xor(s[j], m);
+      if (lane == j) mine = s[j];
+    }
+    if (lane < kBatch && j0 + lane < a.k) static_cast<float*>(a.out)[t * a.k + j0 + lane] = mine;
   }
 }
 
@@ -375,8 +392,7 @@ bsq_status launch_combine(int64_t T, int64_t H, int64_t cap, int k, const void* 
 bsq_status launch_combine_backward(int64_t T, int64_t H, int64_t cap, int k, const void* y, bool bf16,
                                    const int32_t* pos, const void* dout, float* dweights, hipStream_t st) {
   const CombineArgs a{T, H, cap, k, y, pos, nullptr, dout, dweights};
-  const int64_t want = (T + 3) / 4;
-  const unsigned grid = unsigned(want < (1 << 20) ? want : (1 << 20));
+  const unsigned grid = unsigned((T + 3) / 4);
   if (bf16) hipLaunchKernelGGL(k_combine_backward<1>, grid, 256, 0, st, a);
   else hipLaunchKernelGGL(k_combine_backward<0>, grid, 256, 0, st, a);
   return launch_status("moe_combine_backward");
