@@ -576,6 +576,29 @@ def test_wgrad(blocks, N, K, e5m2, bf16):
     assert np.array_equal(first, host(out)), "two runs differ"
 
 
+LONG = [700, 0, 513, 1, 900, 1200, 3, 880]
+
+
+@pytest.mark.parametrize("lengths,T,N,K,k,opts", [
+    # more big tiles than workgroups that go through them
+    (LONG, 1400, 3344, 256, 3, dict(tail=5)), (LONG, 900, 3344, 128, 5, dict(e5m2=True, bf16=False)),
+    # contractions of 1, 2, 3 and more steps, odd and even, around the four that share their scales' load
+    ([600, 1030], 815, 272, 512, 2, dict(bf16=False)), ([600, 1030], 815, 272, 640, 2, {}),
+    ([1024], 512, 16, 896, 2, dict(e5m2=True)), ([513, 511], 512, 240, 1152, 2, dict(bf16=False, e5m2=True))])
+def test_matmul_of_long_segments(lengths, T, N, K, k, opts):
+    say("moe matmul long", len(lengths), sum(lengths), T, N, K, k, opts)
+    _check_product(lengths, T, N, K, k, **opts)
+
+
+@pytest.mark.parametrize("e5m2,bf16", [(True, True), (False, False)])
+def test_wgrad_of_many_big_tiles(e5m2, bf16):
+    """More 256 x 256 tiles than workgroups, segments of 0 to 5 steps; 30 tiles
+    to an expert (nearly full chunks of 32), and 6 (few of one)."""
+    say("wgrad big", e5m2, bf16)
+    test_wgrad([3, 0, 1, 2, 5, 1, 0, 2, 1, 4], 1296, 1056, e5m2, bf16)
+    test_wgrad([1, 0, 2] * 15, 528, 272, e5m2, bf16)
+
+
 # ------------------------------------------------------------------ gate --
 
 # h of float32 arithmetic: the exponential (2 steps), 1 + e, the division
