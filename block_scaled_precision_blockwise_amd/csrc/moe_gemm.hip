@@ -82,6 +82,13 @@ __device__ __forceinline__ void dma16(i32x4 r, uint32_t voff, uint32_t lds) {
                : "s"(scalar(int(lds))), "v"(voff), "s"(r)
                : "memory");
 }
+// 4 bytes per lane: lane i fills [lds + 4 i, + 4).
+__device__ __forceinline__ void dma4(i32x4 r, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(scalar(int(lds))), "v"(voff), "s"(r)
+               : "memory");
+}
 // From a 32-bit offset to a base in scalar registers, to `at` (a constant
 // where it is inlined) past lds.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds, int at) {
@@ -89,6 +96,15 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_
                :
                : "s"(lds), "v"(off), "s"(base), "i"(at)
                : "memory", "scc");
+}
+
+// s_waitcnt's operand: at most n vector memory operations under way.
+constexpr int vmcnt(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+// A barrier that no access of the compiler's moves across.
+__device__ __forceinline__ void barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_of(const uint8_t* p) {
@@ -281,19 +297,20 @@ __device__ __forceinline__ int source_of(const MoeArgs& p, int choice) {
 }
 
 // A tile's operands: rows of A (a row number per tile row, clamped) and B.
-template <int WM, int WN, int MB, int NB, int FA, int OUT_BF16, int WGRAD>
+template <int WM, int WN, int MB, int NB, int S, int FA, int OUT_BF16, int WGRAD>
 __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
   constexpr int NW = WM * WN;
   constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
   constexpr int SA_ = TM / 8 / NW, SB_ = TN / 8 / NW;  // 8-row slices per wave
   static_assert(TM % (8 * NW) == 0 && TN % (8 * NW) == 0, "whole slices");
-  static_assert(TM % 64 == 0 && TN % 64 == 0, "scale rows by the 64");
+  constexpr int SM = (TM + 63) / 64 * 64;  // scale rows of A: by the 64
+  static_assert(TN % 64 == 0, "scale rows by the 64");
   constexpr int kStage = (TM + TN) * BK;
   constexpr int kRowB = NB * 64 + 16;  // bytes of a staged output row of a wave, padded
   constexpr int kOut = NW * 16 * kRowB;
-  constexpr int kAB = 2 * kStage > kOut ? 2 * kStage : kOut;
+  constexpr int kAB = S * kStage > kOut ? S * kStage : kOut;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kAB];
-  __shared__ __attribute__((aligned(16))) uint32_t lds_s[2][(TM + TN) * 4];
+  __shared__ __attribute__((aligned(16))) uint32_t lds_s[S][SM + TN];
   __shared__ int src[TM];  // row of A of each tile row, -1: none
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -324,35 +341,26 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
   for (int s = 0; s < SB_; ++s)
     pb[s] = view.b(t) + int64_t(min(t.n0 + 8 * (w + NW * s) + lrow, view.rows_b() - 1)) * view.pitch() + t.k0 + chunk;
   const uint32_t la = lds_of(lds + 8 * w * BK), lb = lds_of(lds + TM * BK + 8 * w * BK);
-  // step ks (past the last one: the last again, into a stage nobody reads)
-  auto load_a = [&](int ks, int st, int s) {
-    dma16(pa[s] + int64_t(min(ks, nk - 1)) * BK, la + uint32_t(st * kStage + 8 * NW * s * BK));
-  };
-  auto load_b = [&](int ks, int st, int s) {
-    dma16(pb[s] + int64_t(min(ks, nk - 1)) * BK, lb + uint32_t(st * kStage + 8 * NW * s * BK));
-  };
-
-  // ---- scales: rows 64 s .. of A, then of B, four steps (16 bytes) each
+  // scales: a step's four bytes of each row; wave w brings 64 rows of A's and
+  // then B's (again, where there are fewer rows than lanes, so that every wave
+  // has as many loads under way)
+  constexpr int SS = (SM + TN) / 64;
+  static_assert(SS <= NW, "a wave has one load of scales to a step");
   const int64_t spitch = view.pitch() / 32;
-  constexpr int SS = (TM + TN) / 64, SPW = (SS + NW - 1) / NW;
-  uint32_t soff[SPW];
   const int64_t n_sa = int64_t(view.rows_a()) * spitch, n_sb = int64_t(view.rows_b()) * spitch;
-  const i32x4 rsa = rsrc(p.SA, n_sa), rsb = rsrc(view.sb(t), n_sb);
+  const int sw = w % SS;
+  const i32x4 rs = sw < SM / 64 ? rsrc(p.SA, n_sa) : rsrc(view.sb(t), n_sb);
+  const int srow = 64 * sw + lane;
+  const uint32_t soff = uint32_t(
+      (srow < SM ? a_row(min(srow, TM - 1)) : min(t.n0 + srow - SM, view.rows_b() - 1)) * spitch + t.k0 / 32);
+  const uint32_t ls = lds_of(reinterpret_cast<const uint8_t*>(&lds_s[0][64 * sw]));
+  constexpr int kLoads = SA_ + SB_ + 1;  // of a wave and step
+  auto load = [&](int ks, int st) {
 #pragma unroll
-  for (int i = 0; i < SPW; ++i) {
-    const int s = w + NW * i, r = 64 * s + lane;
-    const int64_t row = r < TM ? a_row(min(r, TM - 1)) : min(t.n0 + r - TM, view.rows_b() - 1);
-    soff[i] = uint32_t(row * spitch + t.k0 / 32);
-  }
-  const uint32_t ls = lds_of(reinterpret_cast<const uint8_t*>(&lds_s[0][0]));
-  auto load_scales = [&](int q) {
+    for (int s = 0; s < SA_; ++s) dma16(pa[s] + int64_t(ks) * BK, la + uint32_t(st * kStage + 8 * NW * s * BK));
 #pragma unroll
-    for (int i = 0; i < SPW; ++i) {
-      const int s = w + NW * i;
-      if (s < SS)
-        dma16(s < TM / 64 ? rsa : rsb, soff[i] + 16u * uint32_t(q),
-              ls + uint32_t((q & 1) * (TM + TN) * 16 + 64 * s * 16));
-    }
+    for (int s = 0; s < SB_; ++s) dma16(pb[s] + int64_t(ks) * BK, lb + uint32_t(st * kStage + 8 * NW * s * BK));
+    dma4(rs, soff + 4u * uint32_t(ks), ls + uint32_t(st * (SM + TN) * 4));
   };
 
   const int wm = w % WM, wn = w / WM, g = lane >> 4, r16 = lane & 15;
@@ -363,27 +371,24 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  if (nk > 0) {
-#pragma unroll
-    for (int s = 0; s < SA_; ++s) load_a(0, 0, s);
-#pragma unroll
-    for (int s = 0; s < SB_; ++s) load_b(0, 0, s);
-    load_scales(0);
-  }
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-  __syncthreads();
+  for (int ks = 0; ks < min(nk, S - 1); ++ks) load(ks, ks);
 
+  int st = 0;
   for (int ks = 0; ks < nk; ++ks) {
-    const int st = ks & 1;
-    if ((ks & 3) == 3 && ks + 1 < nk) load_scales((ks + 1) >> 2);
+    // S - 2 steps stay under way; near the end, where fewer are, all are waited for
+    if (ks + S - 2 < nk) __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads));
+    else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    barrier();
+    // past the barrier nobody reads the stage before this one
+    if (ks + S - 1 < nk) load(ks + S - 1, st == 0 ? S - 1 : st - 1);
     const uint8_t* ta = lds + st * kStage;
     const uint8_t* tb = ta + TM * BK;
-    const uint32_t* ss = &lds_s[(ks >> 2) & 1][ks & 3];
+    const uint32_t* ss = lds_s[st];
     uint32_t qa[MB], qb[NB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) qa[i] = ss[(16 * MB * wm + 16 * i + r16) * 4];
+    for (int i = 0; i < MB; ++i) qa[i] = ss[16 * MB * wm + 16 * i + r16];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) qb[j] = ss[(TM + 16 * NB * wn + 16 * j + r16) * 4];
+    for (int j = 0; j < NB; ++j) qb[j] = ss[SM + 16 * NB * wn + 16 * j + r16];
     __builtin_amdgcn_sched_barrier(0);
     auto bfrag = [&](int j) {
       const int row = 16 * NB * wn + 16 * j + r16;
@@ -399,13 +404,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
     if (NB > 1) fb[1] = bfrag(1);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      // two slices of the next step at the head of each block of columns
-#pragma unroll
-      for (int s = 0; s < SA_; ++s)
-        if (s / ((SA_ + NB - 1) / NB) == j) load_a(ks + 1, st ^ 1, s);
-#pragma unroll
-      for (int s = 0; s < SB_; ++s)
-        if (s / ((SB_ + NB - 1) / NB) == j) load_b(ks + 1, st ^ 1, s);
       v8i next{};
       if (j + 2 < NB) next = bfrag(j + 2);
       const int b = int((qb[j] >> (8 * g)) & 0xFFu);
@@ -417,8 +415,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
       fb[1] = next;
       __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
+    st = st == S - 1 ? 0 : st + 1;
   }
 
   // ---- out: 16 rows of the wave at a time through LDS, so that a store
@@ -619,8 +616,8 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
       a_half(4 + x / 2, x & 1);
       if (x & 1) qa[4 + x / 2] = a_scale(4 + x / 2);
     });
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    barrier();
     if (LOADS && (ks & 3) == 2) load_scales((ks + 2) >> 2);
     next_scales(ks + 1);
 #pragma unroll
@@ -733,7 +730,7 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
     const bool more = find_place<TM, TN, WGRAD>(p, lane, deal, L, next);
     const int choice = WGRAD || !more ? -1 : choice_at(p, next, tid);
     const int nk = cur.nk;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt(vmcnt(0));
     __syncthreads();
     if (nk > 0) {
       o[0] = ra + c0;
@@ -772,14 +769,14 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
   }
 }
 
-template <int WM, int WN, int MB, int NB, int WGRAD>
+template <int WM, int WN, int MB, int NB, int S, int WGRAD>
 bsq_status launch(const MoeArgs& a, bool e5m2, bool bf16, int64_t grid, hipStream_t st) {
   const dim3 g = dim3(unsigned(grid)), b = dim3(64 * WM * WN);
   switch ((e5m2 ? 1 : 0) | (bf16 ? 2 : 0)) {
-    case 0: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, 0, 0, WGRAD>), g, b, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, 1, 0, WGRAD>), g, b, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, 0, 1, WGRAD>), g, b, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, 1, 1, WGRAD>), g, b, 0, st, a);
+    case 0: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 0, 0, WGRAD>), g, b, 0, st, a); break;
+    case 1: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 1, 0, WGRAD>), g, b, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 0, 1, WGRAD>), g, b, 0, st, a); break;
+    default: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 1, 1, WGRAD>), g, b, 0, st, a);
   }
   return launch_status(WGRAD ? "moe_wgrad" : "moe_matmul");
 }
@@ -812,15 +809,16 @@ bsq_status launch_moe_product(const MoeGemmLaunch& L, hipStream_t st) {
   auto grid = [&](int tm, int tn) { return (L.cap / tm + L.E + 1) * up_to(L.N, tn); };
   // the big tiles address rows with 32 bits
   if (L.cap / L.E >= 512 && L.T * L.K < (int64_t(1) << 32)) return launch_big<0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
-  if (L.cap / L.E >= 64) return launch<2, 2, 4, 4, 0>(a, L.a_e5m2, L.out_bf16, grid(128, 128), st);
-  return launch<2, 2, 2, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
+  if (L.cap / L.E >= 64) return launch<2, 2, 4, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(128, 128), st);
+  if (L.cap / L.E <= 16) return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
+  return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
 }
 
 bsq_status launch_moe_wgrad(const MoeGemmLaunch& L, hipStream_t st) {
   const MoeArgs a = args_of(L);
   const int64_t big = up_to(L.N, 256) * up_to(L.K, 256) * L.E;
   if (big >= 256 && L.cap * 256 < (int64_t(1) << 32)) return launch_big<1>(a, L.a_e5m2, L.out_bf16, big, st);
-  return launch<2, 2, 4, 4, 1>(a, L.a_e5m2, L.out_bf16, up_to(L.N, 128) * up_to(L.K, 128) * L.E, st);
+  return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, up_to(L.N, 128) * up_to(L.K, 128) * L.E, st);
 }
 
 }  // namespace bsq
