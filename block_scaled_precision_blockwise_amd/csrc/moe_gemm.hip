@@ -15,14 +15,24 @@
 // Offsets and row numbers are clamped to their arrays, so that no content of
 // theirs makes an access out of range.
 //
-// One tile: WM x WN waves, each with MB x NB blocks of 16 x 16
-// (v_mfma_scale_f32_16x16x128_f8f6f4, both E8M0 scales applied in the matrix
-// core, float32 accumulators).  K goes in steps of 128 bytes through two LDS
-// stages filled by direct loads, 16-byte chunks XOR-swizzled over the rows so
-// that a fragment read spreads over the banks; the next step's loads are
-// issued between this step's MFMAs.  The scales of four steps come as one
-// 16-byte piece per row.  The MFMA's first operand is the B fragment, so that
-// a lane's four results are four neighbours of one output row.
+// Two kernels.  k_moe_big takes 256 x 256 tiles (many rows to an expert);
+// k_moe_gemm takes the rest: WM x WN waves, each with MB x NB blocks of 16 x
+// 16 (v_mfma_scale_f32_16x16x128_f8f6f4, both E8M0 scales applied in the
+// matrix core, float32 accumulators).  K goes in steps of 128 bytes through a
+// ring of S LDS stages filled by direct loads, 16-byte chunks XOR-swizzled
+// over the rows so that a fragment read spreads over the banks.  A step waits
+// for its own loads only (they retire in order), so that S - 2 more steps
+// stay under way.  The MFMA's first operand is the B fragment, so that a
+// lane's four results are four neighbours of one output row.
+//
+// Measured (MI355X): 65536 rows over 32 experts, N 4096, K 2048: 542 us, 2.03
+// PFLOP/s; the weight gradients of 32768 rows over 16 experts, N = K = 2048:
+// 155 us, 1.78 PFLOP/s.  A big tile's 16 steps take 45 k cycles, 2800 a step
+// where its 256 MFMAs take 2048; with every load a hit in the L2 2700, without
+// loads 2500; the rest of a tile (search, first loads, output) 10 k.  The
+// clock is held to 1.9 - 2.0 GHz by power: pure MFMAs on such operands run at
+// 16 - 19 ns per 16 x 16 x 128, not the 13.3 of 2.4 GHz.  8 tokens over 32
+// experts (N 4096, K 2048): 33 us, 5.3 TB/s of weights.
 #include "moe.h"
 
 #include <type_traits>
@@ -807,18 +817,37 @@ bsq_status launch_moe_product(const MoeGemmLaunch& L, hipStream_t st) {
   // a segment's last tile may be part full: at most one such tile for each
   // expert and for the rows past the last segment
   auto grid = [&](int tm, int tn) { return (L.cap / tm + L.E + 1) * up_to(L.N, tn); };
-  // the big tiles address rows with 32 bits
-  if (L.cap / L.E >= 512 && L.T * L.K < (int64_t(1) << 32)) return launch_big<0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
-  if (L.cap / L.E >= 64) return launch<2, 2, 4, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(128, 128), st);
-  if (L.cap / L.E <= 16) return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
-  return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
+  // rows that hold a choice, as far as the host knows, and per expert
+  const int64_t n = L.rows != nullptr && L.T < L.cap / L.k ? L.T * L.k : L.cap, rows = n / L.E;
+  // us at (rows per expert, experts, N, K), 256 x 256 tiles against the next:
+  // (256, 16, 2048, 2048) 32 / 41, (192, 64, 2048, 1024) 65 / 78; with fewer
+  // tiles than most CUs (255, 8, 1792, 1024) 18.5 / 12.1.  The big tiles
+  // address rows with 32 bits.
+  if (rows >= 160 && (n / 256 + L.E / 2) * up_to(L.N, 256) >= 160 && L.T * L.K < (int64_t(1) << 32))
+    return launch_big<0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
+  // 64 x 128 against 128 x 128: (255, 8, 1792, 1024) 12.1 / 14.8, (192, 64,
+  // 2048, 1024) 79 / 78; against 64 x 64: (37, 32, 2048, 1024, segments
+  // aligned to 128) 26 / 32
+  if (rows >= 32) return launch<2, 2, 2, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
+  // few rows, where the weights' bytes are most of the work: three stages
+  // against two (1, 32, 4096, 2048) 33 / 42; 32 rows against 64 (8, 32, 2048,
+  // 1024) 13.8 / 16.4
+  if (rows > 16) return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
+  return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
 }
 
 bsq_status launch_moe_wgrad(const MoeGemmLaunch& L, hipStream_t st) {
   const MoeArgs a = args_of(L);
+  // us with 256 x 256 tiles against 128 x 128 at (big tiles, rows per expert):
+  // (128, 512) 20 / 17, (64, 8192) 85 / 60
   const int64_t big = up_to(L.N, 256) * up_to(L.K, 256) * L.E;
   if (big >= 256 && L.cap * 256 < (int64_t(1) << 32)) return launch_big<1>(a, L.a_e5m2, L.out_bf16, big, st);
-  return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, up_to(L.N, 128) * up_to(L.K, 128) * L.E, st);
+  const int64_t tiles = up_to(L.N, 128) * up_to(L.K, 128) * L.E;
+  // a workgroup to a CU: three stages for it; more: two, so that two fit.  us
+  // with three / two at (tiles, rows per expert): (256, 2048) 27 / 33, (256,
+  // 8192) 48 / 60, (512, 512) 21 / 17
+  if (tiles <= kCUs) return launch<2, 2, 4, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles, st);
+  return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, tiles, st);
 }
 
 }  // namespace bsq
