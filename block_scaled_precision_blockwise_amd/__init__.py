@@ -148,9 +148,15 @@ def _raise(status: int, what: str):
 
 # ------------------------------------------------------------ helpers ----
 
+_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
 
 
 def _stream(stream) -> Optional[int]:
@@ -168,11 +174,11 @@ def _ptr(t) -> Optional[int]:
 
 
 def _dev(*ts):
-    torch = _torch()
+    kind = _torch().Tensor
     for t in ts:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, kind):
             raise TypeError("expected a torch.Tensor")
         if not t.is_cuda:
             raise ValueError("tensors must be on the GPU")
@@ -180,17 +186,22 @@ def _dev(*ts):
             raise ValueError("tensors must be contiguous")
 
 
+_one_byte = None
+
+
 def _bytes1(t, name):
-    torch = _torch()
-    ok = (torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu)
-    if t.dtype not in ok:
+    global _one_byte
+    if _one_byte is None:
+        torch = _torch()
+        _one_byte = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu))
+    if t.dtype not in _one_byte:
         raise TypeError(f"{name} must hold one byte per element, got {t.dtype}")
 
 
 def _expect(t, dtype, shape, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
