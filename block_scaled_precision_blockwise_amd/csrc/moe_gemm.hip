@@ -25,9 +25,9 @@
 // stay under way.  The MFMA's first operand is the B fragment, so that a
 // lane's four results are four neighbours of one output row.
 //
-// Measured (MI355X): 65536 rows over 32 experts, N 4096, K 2048: 542 us, 2.03
+// Measured (MI355X): 65536 rows over 32 experts, N 4096, K 2048: 539 us, 2.04
 // PFLOP/s; the weight gradients of 32768 rows over 16 experts, N = K = 2048:
-// 155 us, 1.78 PFLOP/s.  A big tile's 16 steps take 45 k cycles, 2800 a step
+// 151 us, 1.82 PFLOP/s.  A big tile's 16 steps take 45 k cycles, 2800 a step
 // where its 256 MFMAs take 2048; with every load a hit in the L2 2700, without
 // loads 2500; the rest of a tile (search, first loads, output) 10 k.  The
 // clock is held to 1.9 - 2.0 GHz by power: pure MFMAs on such operands run at
@@ -108,6 +108,14 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_
                : "memory", "scc");
 }
 
+// The same, to be dropped from the L2 first.
+__device__ __forceinline__ void dma16_stream(const uint8_t* base, uint32_t off, uint32_t lds, int at) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+               :
+               : "s"(lds), "v"(off), "s"(base), "i"(at)
+               : "memory", "scc");
+}
+
 // s_waitcnt's operand: at most n vector memory operations under way.
 constexpr int vmcnt(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 // A barrier that no access of the compiler's moves across.
@@ -178,7 +186,10 @@ __device__ __forceinline__ Segment find_tile(const MoeArgs& a, int tm, int lane,
 
 // Tile order: workgroups are dealt to the 8 XCDs round-robin by linear id,
 // and each XCD has its own L2, so XCD x takes the x-th contiguous eighth of
-// an order that walks bands of kBand tile rows column by column.
+// an order that walks bands of kBand tile rows column by column.  65536 rows
+// over 32 experts, N 4096, K 2048: bands of 2, 4, 6, 8, 16 rows 662, 628, 610,
+// 649, 673 us with an earlier output, of 4, 5, 6 rows 543, 531, 533 us with the
+// present one; bands that end with the segments are no faster.
 __device__ __forceinline__ void tile_order(int L, int tiles_m, int tiles_n, int& tm, int& tn) {
   constexpr int kBand = 5;
   const int T = tiles_m * tiles_n, per = T / 8;
@@ -505,7 +516,12 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
   const uint32_t lbase = lds_of(lds + 8 * w * BK), ls = lds_of(lds_s + 64 * w * 16);
   uint32_t to = lbase;  // stage that is loaded
   auto load = [&](int s, uint32_t to) {
-    dma16(s < 8 ? pa : pb, off[s], to, (s < 8 ? 0 : TM * BK) + 8 * NW * (s & 7) * BK);
+    const int at = (s < 8 ? 0 : TM * BK) + 8 * NW * (s & 7) * BK;
+    // of the weight gradients' chunks of 4 x 8 tiles (32 to an XCD) the eight
+    // go first: 151 us against 165 (all kept) and 155 (the four first); the
+    // products lose by either (568, 627 against 537 us)
+    if (WGRAD && s >= 8) dma16_stream(pb, off[s], to, at);
+    else dma16(s < 8 ? pa : pb, off[s], to, at);
   };
   auto loaded = [&] {  // a whole step
     pa += BK;
