@@ -113,7 +113,7 @@ __device__ __forceinline__ void store8(void* p, int64_t elem, const float (&v)[8
 }
 
 // ------------------------------------- tiles written in both orientations --
-// A workgroup of 256 threads holds a 128 x 128 tile in LDS and writes its
+// A workgroup of NT threads holds a 128 x 128 tile in LDS and writes its
 // codes transposed: eight lanes own a column, 16 rows (16 bytes) each, so
 // that one store instruction writes whole 128-byte lines; two neighbouring
 // lanes share a block of 32 rows.  Chunks of eight columns are XORed with the
@@ -162,7 +162,15 @@ __device__ __forceinline__ uint32_t encode4(uint32_t ab, uint32_t cd, float scal
   }
   return __builtin_bit_cast(uint32_t, q);
 }
-__device__ __forceinline__ float power_of_two(int E) { return __uint_as_float(uint32_t(E + 127) << 23); }
+// mx_exponent plus 127 from the bits of a block's largest magnitude: the scale
+// byte, and 23 places up the scale 2^E itself.  The significand passes 1.75
+// where adding 2^23 - 1 - 0x600000 carries into the exponent; from the floor
+// on no clamp can be reached.
+template <int CODE>
+__device__ __forceinline__ uint32_t mx_byte(uint32_t bits) {
+  return ((max(bits, __float_as_uint(scale_floor())) + 0x1FFFFFu) >> 23) - (CODE == 0 ? 8u : 15u);
+}
+__device__ __forceinline__ float mx_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // Stores that nothing reads again soon: they leave the L2 to what is shared.
 __device__ __forceinline__ void stnt(void* p, uint32_t a, uint32_t b) {
@@ -198,8 +206,7 @@ __device__ __forceinline__ uint32_t lane_ahead(uint32_t v) {
 // The scale of block f8 / 4 of a row of 16 lanes, four lanes to a block.  Where
 // the row's four blocks are all there and start a word, one lane writes the
 // word: a byte at a time cost 15 of 133 us.
-__device__ __forceinline__ void put_scale(uint8_t* scales, int64_t f8, bool in, bool words, int E) {
-  const uint32_t e = uint32_t(E + 127);
+__device__ __forceinline__ void put_scale(uint8_t* scales, int64_t f8, bool in, bool words, uint32_t e) {
   if (words) {
     uint32_t w = e | (lane_ahead<4>(e) << 8);
     w |= lane_ahead<8>(w) << 16;
@@ -219,8 +226,8 @@ __device__ __forceinline__ void put_row(uint8_t* codes, uint8_t* scales, int64_t
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
-  const int E = mx_exponent<CODE == 0 ? 8 : 15>(__uint_as_float(group_max_bits<4>(m)));
-  const float s = power_of_two(E);
+  const uint32_t E = mx_byte<CODE>(group_max_bits<4>(m));
+  const float s = mx_scale(E);
   put_scale(scales, f8, in, words, E);
   if (in) stnt(codes + 8 * f8, encode4<CODE>(x[0], x[1], x[2], x[3], s), encode4<CODE>(x[4], x[5], x[6], x[7], s));
 }
@@ -231,8 +238,8 @@ __device__ __forceinline__ void put_row(uint8_t* codes, uint8_t* scales, int64_t
 #pragma unroll
   for (int i = 0; i < 4; ++i) m = max_u16x2(m, x[i] & 0x7FFF7FFFu);
   m = group_max_bits<4>(max(m & 0xFFFFu, m >> 16));
-  const int E = mx_exponent<CODE == 0 ? 8 : 15>(decode_bf16(m));
-  const float s = power_of_two(E);
+  const uint32_t E = mx_byte<CODE>(m << 16);
+  const float s = mx_scale(E);
   put_scale(scales, f8, in, words, E);
   if (in) stnt(codes + 8 * f8, encode4<CODE>(x[0], x[1], s), encode4<CODE>(x[2], x[3], s));
 }
@@ -245,20 +252,18 @@ __device__ __forceinline__ int tile_at(int r, int c8) {
 }
 
 // The tile at rows r0 .., columns c0 .. as codes_t [cols, rows].
-template <int CODE, int PAIRS>
+template <int CODE, int PAIRS, int NT>
 __device__ __forceinline__ void put_columns(const uint32_t* tile, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
                                             uint8_t* codes_t, uint8_t* scales_t) {
-  constexpr int EMAX = CODE == 0 ? 8 : 15;
   const int share = threadIdx.x & 7;
   const int64_t r = r0 + 16 * share;
   const bool words = rows % kTile == 0 && aligned4(scales_t);
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int oc = (threadIdx.x >> 3) + 32 * it;
+  for (int it = 0; it < kTile * 8 / NT; ++it) {
+    const int oc = (threadIdx.x >> 3) + NT / 8 * it;
     const int64_t c = c0 + oc;
     const bool in = r < rows && c < cols;
-    uint32_t q[4];
-    int E;
+    uint32_t q[4], E;
     if constexpr (PAIRS) {
       uint32_t x[8], m = 0u;
 #pragma unroll
@@ -266,8 +271,8 @@ __device__ __forceinline__ void put_columns(const uint32_t* tile, int64_t r0, in
         x[i] = tile[tile_at<1>(8 * share + i, oc >> 3) + (oc & 7)];
         m = max_u16x2(m, x[i] & 0x7FFF7FFFu);
       }
-      E = mx_exponent<EMAX>(decode_bf16(group_max_bits<2>(max(m & 0xFFFFu, m >> 16))));
-      const float s = power_of_two(E);
+      E = mx_byte<CODE>(group_max_bits<2>(max(m & 0xFFFFu, m >> 16)) << 16);
+      const float s = mx_scale(E);
 #pragma unroll
       for (int i = 0; i < 4; ++i) q[i] = encode4<CODE>(x[2 * i], x[2 * i + 1], s);
     } else {
@@ -278,18 +283,17 @@ __device__ __forceinline__ void put_columns(const uint32_t* tile, int64_t r0, in
         x[i] = __uint_as_float(tile[tile_at<0>(16 * share + i, oc >> 3) + (oc & 7)]);
         m = max(m, abs_bits(x[i]));
       }
-      E = mx_exponent<EMAX>(__uint_as_float(group_max_bits<2>(m)));
-      const float s = power_of_two(E);
+      E = mx_byte<CODE>(group_max_bits<2>(m));
+      const float s = mx_scale(E);
 #pragma unroll
       for (int i = 0; i < 4; ++i) q[i] = encode4<CODE>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], s);
     }
     if (words) {
-      const uint32_t e = uint32_t(E + 127);
-      uint32_t w = e | (lane_ahead<2>(e) << 8);
+      uint32_t w = E | (lane_ahead<2>(E) << 8);
       w |= lane_ahead<4>(w) << 16;
       if (in && share == 0) *reinterpret_cast<uint32_t*>(scales_t + c * (rows / 32) + r / 32) = w;
     } else if (in && (share & 1) == 0) {
-      scales_t[c * (rows / 32) + r / 32] = uint8_t(E + 127);
+      scales_t[c * (rows / 32) + r / 32] = uint8_t(E);
     }
     if (in) stnt(codes_t + c * rows + r, q[0], q[1], q[2], q[3]);
   }

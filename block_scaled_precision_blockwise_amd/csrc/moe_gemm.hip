@@ -10,8 +10,8 @@
 //            dyt[n, r] xt[k, r].
 //
 // The segments are known on the device only.  A workgroup finds its tile by
-// a scan of the offsets; the grid covers the most tiles that any split of
-// `cap` rows over E experts can have, and what is left over ends at once.
+// a scan of the offsets; there are tiles for the most that any split of `cap`
+// rows over E experts can have, and a workgroup without one ends at once.
 // Offsets and row numbers are clamped to their arrays, so that no content of
 // theirs makes an access out of range.
 //
@@ -241,8 +241,8 @@ __device__ __forceinline__ Deal deal_tiles(const MoeArgs& p, int lane) {
   }
   const int per = ((p.N + TM - 1) / TM) * ((p.K + TN - 1) / TN), chunks = (per + 31) / 32;
   // chunks that are mostly full, experts that fit the lanes; 16 experts of
-  // 2048 x 2048 over 32768 rows, segments of 0.5 to 2 times the mean: 213 us
-  // by eighths (one XCD had 1.38 times the mean's steps)
+  // 2048 x 2048 over 32768 rows, segments of 0.5 to 2 times the mean: 165 us
+  // against 213 by eighths (one XCD had 1.38 times the mean's steps)
   if (p.E > 64 || gridDim.x != kCUs || 8 * per < 7 * 32 * chunks) return d;
   d.total = 1;
   int len = -1;

@@ -9,6 +9,13 @@
 // The choice is a discrete answer: it is made on scores in 64 bits, so that
 // two experts whose scores differ only past the 24th bit are still put in
 // their true order.
+//
+// Bound by instruction issue: 32768 tokens of 256 experts (sigmoid, bias, 4 of
+// 8 groups, 8 choices, all scores) take 32 us for 50 MB (137 us with a token
+// to a wave and rounds of argmax, 40 with the exponential's coefficients moved
+// into registers before each use and branches around each score); its
+// gradient 17 us for 67 MB (23 us with a token to a wave and 2-byte loads).
+// One token: 4.0 us, 12 before.
 #include <math.h>
 
 #include <type_traits>
@@ -772,7 +779,10 @@ void by_width(int E, F&& f) {
   else f(std::integral_constant<int, 16>{});
 }
 
-// From this many tokens on, four share a wave.
+// From this many tokens on, four share a wave; below, a wave each fills more
+// of the chip and is done sooner.  Forward, us of four to a wave against one:
+// 1024 tokens of 256 experts 8.2 / 6.1, 2048 8.2 / 7.5, 4096 9.0 / 10.7; of
+// 128 experts 5.3 / 5.2, 5.2 / 6.3, 5.6 / 9.3.
 constexpr int64_t kRowTokens = 2048;
 
 unsigned token_grid(int64_t T) {
