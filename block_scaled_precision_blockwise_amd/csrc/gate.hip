@@ -8,7 +8,7 @@
 // reads 272 and writes 268 (backward, 84 us); the two calls take 199 us, 5.4
 // TB/s, the rate of a large copy.  What it took: g and u as pairs of 16 bits
 // to the conversion that scales, tiles of 128 columns so that codes are
-// written in whole lines both ways, non-temporal stores, and a sigmoid of 9
+// written in whole lines both ways, non-temporal stores, and a sigmoid of 10
 // instructions; with the library's, single conversions and 64-column tiles it
 // was bound by instruction issue (245 us).
 #include "fp8.h"
@@ -23,11 +23,12 @@ namespace {
 // 1 / (1 + e^-g) in float32 within 4 steps of 2^-23: -g log2 e in two pieces
 // (the hardware's 2^t of the first, times 1 + ln 2 of the second), and the
 // hardware's reciprocal, of a sixteenth of the sum so that a result near
-// 2^-126 is not flushed.  e^-g = inf gives 0.  9 instructions; the library's
+// 2^-126 is not flushed.  e^-g = inf gives 0.  10 instructions; the library's
 // expf and division took 40, and with them the training pass was bound by
 // instruction issue.
 __device__ __forceinline__ float sigmoid(float g) {
   constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;  // log2 e = kLog2e + kRest
+  g = __builtin_amdgcn_fmed3f(g, -128.f, 128.f);  // 0 and 1 from there on; keeps infinities out of `lo`
   const float t = -g * kLog2e;
   const float lo = fmaf(-g, kRest, fmaf(-g, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t) * fmaf(lo, 0x1.62e43p-1f, 1.0f);

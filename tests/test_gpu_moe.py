@@ -582,6 +582,8 @@ LONG = [700, 0, 513, 1, 900, 1200, 3, 880]
 @pytest.mark.parametrize("lengths,T,N,K,k,opts", [
     # more big tiles than workgroups that go through them
     (LONG, 1400, 3344, 256, 3, dict(tail=5)), (LONG, 900, 3344, 128, 5, dict(e5m2=True, bf16=False)),
+    (LONG, 4200, 3344, 128, 1, dict(gather=False, tail=300)),
+    ([500, 0, 300, 1, 200, 257, 30, 12], 650, 4624, 640, 2, dict(tail=2)),
     # contractions of 1, 2, 3 and more steps, odd and even, around the four that share their scales' load
     ([600, 1030], 815, 272, 512, 2, dict(bf16=False)), ([600, 1030], 815, 272, 640, 2, {}),
     ([1024], 512, 16, 896, 2, dict(e5m2=True)), ([513, 511], 512, 240, 1152, 2, dict(bf16=False, e5m2=True))])
@@ -597,6 +599,40 @@ def test_wgrad_of_many_big_tiles(e5m2, bf16):
     say("wgrad big", e5m2, bf16)
     test_wgrad([3, 0, 1, 2, 5, 1, 0, 2, 1, 4], 1296, 1056, e5m2, bf16)
     test_wgrad([1, 0, 2] * 15, 528, 272, e5m2, bf16)
+
+
+def test_wgrad_of_long_contractions():
+    """Segments of up to 9 steps, around the four that share their scales' load."""
+    say("wgrad long")
+    test_wgrad([9, 7, 6, 8, 0, 4, 1, 3, 2], 1296, 1056, True, True)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_swiglu_of_infinite_values(bf16):
+    """silu(inf) u = inf u, which takes the block's largest code; -inf has no
+    value (-inf 0): its block is left out here, and the rest is as without it."""
+    torch = _torch()
+    say("swiglu infinite", bf16)
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((64, 256)).astype(np.float32)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gu = to_dev(x).to(dt)
+    plain = [filled(s, torch.uint8, 0x55) for s in ((64, 128), (64, 4), (128, 64), (128, 2))]
+    bsq.bsq_swiglu_mx(gu, *plain)
+    gu[3, 5] = float("inf")
+    gu[40, 70] = -float("inf")
+    got = [filled(s, torch.uint8, 0x55) for s in ((64, 128), (64, 4), (128, 64), (128, 2))]
+    bsq.bsq_swiglu_mx(gu, *got)
+    h, want = host(got[0]), host(plain[0])
+    assert h[3, 5] == (0x7E if float(gu[3, 5 + 128]) > 0 else 0xFE)
+    keep = np.ones((64, 128), bool)
+    keep[3, 0:32] = False
+    keep[40, 64:96] = False
+    assert np.array_equal(h[keep], want[keep])
+    keep_t = np.ones((128, 64), bool)
+    keep_t[5, 0:32] = False
+    keep_t[70, 32:64] = False
+    assert host(got[2])[5, 3] == h[3, 5] and np.array_equal(host(got[2])[keep_t], host(plain[2])[keep_t])
 
 
 # ------------------------------------------------------------------ gate --
