@@ -27,7 +27,7 @@
 //
 // Measured (MI355X): 65536 rows over 32 experts, N 4096, K 2048: 539 us, 2.04
 // PFLOP/s; the weight gradients of 32768 rows over 16 experts, N = K = 2048:
-// 151 us, 1.82 PFLOP/s.  A big tile's 16 steps take 45 k cycles, 2800 a step
+// 152 us, 1.81 PFLOP/s.  A big tile's 16 steps take 45 k cycles, 2800 a step
 // where its 256 MFMAs take 2048; with every load a hit in the L2 2700, without
 // loads 2500; the rest of a tile (search, first loads, output) 10 k.  The
 // clock is held to 1.9 - 2.0 GHz by power: pure MFMAs on such operands run at
@@ -232,6 +232,11 @@ struct View {
 struct Deal {
   int total, before, mine;
 };
+// Chunks that are mostly full, experts that fit the lanes.
+__host__ __device__ inline bool dealt(int per, int E) {
+  const int chunks = (per + 31) / 32;
+  return E <= 64 && 8 * per >= 7 * 32 * chunks;
+}
 template <int TM, int TN, int WGRAD>
 __device__ __forceinline__ Deal deal_tiles(const MoeArgs& p, int lane) {
   Deal d{0, 0, 0};
@@ -239,11 +244,9 @@ __device__ __forceinline__ Deal deal_tiles(const MoeArgs& p, int lane) {
     d.total = tiles_total(p, TM, lane, d.before, d.mine);
     return d;
   }
-  const int per = ((p.N + TM - 1) / TM) * ((p.K + TN - 1) / TN), chunks = (per + 31) / 32;
-  // chunks that are mostly full, experts that fit the lanes; 16 experts of
-  // 2048 x 2048 over 32768 rows, segments of 0.5 to 2 times the mean: 165 us
-  // against 213 by eighths (one XCD had 1.38 times the mean's steps)
-  if (p.E > 64 || gridDim.x != kCUs || 8 * per < 7 * 32 * chunks) return d;
+  // 16 experts of 2048 x 2048 over 32768 rows, segments of 0.5 to 2 times the
+  // mean: 165 us against 213 by eighths (one XCD had 1.38 times the mean's steps)
+  if (gridDim.x != kCUs || !dealt(((p.N + TM - 1) / TM) * ((p.K + TN - 1) / TN), p.E)) return d;
   d.total = 1;
   int len = -1;
   if (lane < p.E) len = max(bounded(p.offsets[lane + 1], p.cap) / BK - bounded(p.offsets[lane], p.cap) / BK, 0);
@@ -487,11 +490,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
 // after next follow it, and have until the next barrier to land.
 //
 // A workgroup goes through the tiles blockIdx.x + gridDim.x i.  Between two of
-// them the loads of the next one's first two steps come first, then the
-// search for the one after, then the output of the last one, which goes from
-// the accumulators to memory without LDS: lanes exchange halves until each
-// holds 16 neighbouring bytes of a row.
-template <int FA, int OUT_BF16, int WGRAD>
+// them the output of the last one goes from the accumulators to memory without
+// LDS (lanes exchange halves until each holds 16 neighbouring bytes of a row),
+// the loads of the next one's first two steps beside it; the search for the
+// one after follows while they land.
+template <int FA, int OUT_BF16, int WGRAD, int STREAM_A>
 __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
   constexpr int TM = 256, TN = 256, NW = 4;
   constexpr int kStage = (TM + TN) * BK;
@@ -517,10 +520,7 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
   uint32_t to = lbase;  // stage that is loaded
   auto load = [&](int s, uint32_t to) {
     const int at = (s < 8 ? 0 : TM * BK) + 8 * NW * (s & 7) * BK;
-    // of the weight gradients' chunks of 4 x 8 tiles (32 to an XCD) the eight
-    // go first: 151 us against 165 (all kept) and 155 (the four first); the
-    // products lose by either (568, 627 against 537 us)
-    if (WGRAD && s >= 8) dma16_stream(pb, off[s], to, at);
+    if (STREAM_A && s < 8) dma16_stream(pa, off[s], to, at);
     else dma16(s < 8 ? pa : pb, off[s], to, at);
   };
   auto loaded = [&] {  // a whole step
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
     dma16(rsrc(p.SA, n_sa), soff[0] + 16u * uint32_t(q), ls + uint32_t((q & 1) * (TM + TN) * 16));
     dma16(rsrc(psb, n_sb), soff[1] + 16u * uint32_t(q), ls + uint32_t((q & 1) * (TM + TN) * 16 + TM * 16));
   };
-  // Addresses of tile t, whose rows of A are in src[buf]; loads of two steps.
+  // Addresses of tile t, whose rows of A are in src[buf], and its first scales.
   auto begin = [&](const Place& t, int buf) {
     const int m0 = t.m0, n0 = t.n0, nk = t.nk;
     if (nk == 0) return;
@@ -558,16 +558,15 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
     soff[0] = uint32_t((a_row(64 * w + lane) + (WGRAD ? m0 : 0)) * spitch + t.k0 / 32);
     soff[1] = uint32_t(min(n0 + 64 * w + lane, view.rows_b() - 1) * spitch + t.k0 / 32);
     to = lbase;
-    const uint32_t first = uint32_t(scalar(int(lbase))), second = uint32_t(scalar(int(lbase + kStage)));
     load_scales(0);
+  };
+  // Quarter q of the loads of a tile's first two steps.
+  auto preload = [&](int nk, int q) {
+    if (nk <= q / 2) return;
+    const uint32_t stage = uint32_t(scalar(int(lbase + (q < 2 ? 0 : kStage))));
 #pragma unroll
-    for (int s = 0; s < 16; ++s) load(s, first);
-    loaded();
-    if (nk > 1) {
-#pragma unroll
-      for (int s = 0; s < 16; ++s) load(s, second);
-      loaded();
-    }
+    for (int s = 0; s < 8; ++s) load(8 * (q & 1) + s, stage);
+    if (q & 1) loaded();
   };
 
   const int wm = w & 1, wn = w >> 1, g = lane >> 4, r16 = lane & 15;
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
   // then neighbouring rows trade one pair of blocks each, so that a store
   // writes whole 128-byte lines (64 bytes of a row at a time wrote 1.5 times
   // the bytes to memory: 604 against 542 us for 65536 rows, N 4096, K 2048).
-  auto output = [&](const Place& t, int buf) {
+  auto output = [&](const Place& t, int buf, auto&& beside) {
     constexpr int kElem = OUT_BF16 ? 2 : 4;
     const int64_t pitch = int64_t(view.rows_b()) * kElem;
     const int n0 = t.n0 + 128 * wn, left = view.rows_b() - n0;  // columns of the wave
@@ -687,6 +686,7 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
     at += r16 * pitch + 16 * g;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      beside(i);
       const int tr = 128 * wm + 16 * i + r16;
       const bool none = !WGRAD && src[buf][tr] < 0, in = t.m0 + tr < t.m_end;
       if constexpr (OUT_BF16) {
@@ -750,6 +750,8 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
   if (!find_place<TM, TN, WGRAD>(p, lane, deal, L, cur)) return;
   publish(cur, 0, WGRAD ? 0 : choice_at(p, cur, tid));
   begin(cur, 0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) preload(cur.nk, q);
   clear();
   for (;;) {
     L += gridDim.x;
@@ -788,7 +790,10 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
       publish(cur, buf ^ 1, choice);
       begin(cur, buf ^ 1);
     }
-    output(done, buf);
+    const int ahead = more ? cur.nk : 0;
+    output(done, buf, [&](int i) {
+      if (i < 4) preload(ahead, i);
+    });
     if (!more) return;
     buf ^= 1;
     clear();
@@ -807,15 +812,15 @@ bsq_status launch(const MoeArgs& a, bool e5m2, bool bf16, int64_t grid, hipStrea
   return launch_status(WGRAD ? "moe_wgrad" : "moe_matmul");
 }
 
-template <int WGRAD>
+template <int WGRAD, int STREAM_A>
 bsq_status launch_big(const MoeArgs& a, bool e5m2, bool bf16, int64_t grid, hipStream_t st) {
   // one workgroup to a CU, each going through its share of the tiles
   const dim3 g = dim3(unsigned(grid < kCUs ? grid : kCUs)), b = dim3(256);
   switch ((e5m2 ? 1 : 0) | (bf16 ? 2 : 0)) {
-    case 0: hipLaunchKernelGGL((k_moe_big<0, 0, WGRAD>), g, b, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((k_moe_big<1, 0, WGRAD>), g, b, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_moe_big<0, 1, WGRAD>), g, b, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_moe_big<1, 1, WGRAD>), g, b, 0, st, a);
+    case 0: hipLaunchKernelGGL((k_moe_big<0, 0, WGRAD, STREAM_A>), g, b, 0, st, a); break;
+    case 1: hipLaunchKernelGGL((k_moe_big<1, 0, WGRAD, STREAM_A>), g, b, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((k_moe_big<0, 1, WGRAD, STREAM_A>), g, b, 0, st, a); break;
+    default: hipLaunchKernelGGL((k_moe_big<1, 1, WGRAD, STREAM_A>), g, b, 0, st, a);
   }
   return launch_status(WGRAD ? "moe_wgrad" : "moe_matmul");
 }
@@ -840,7 +845,7 @@ bsq_status launch_moe_product(const MoeGemmLaunch& L, hipStream_t st) {
   // tiles than most CUs (255, 8, 1792, 1024) 18.5 / 12.1.  The big tiles
   // address rows with 32 bits.
   if (rows >= 160 && (n / 256 + L.E / 2) * up_to(L.N, 256) >= 160 && L.T * L.K < (int64_t(1) << 32))
-    return launch_big<0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
+    return launch_big<0, 0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
   // 64 x 128 against 128 x 128: (255, 8, 1792, 1024) 12.1 / 14.8, (192, 64,
   // 2048, 1024) 79 / 78; against 64 x 64: (37, 32, 2048, 1024, segments
   // aligned to 128) 26 / 32
@@ -857,7 +862,19 @@ bsq_status launch_moe_wgrad(const MoeGemmLaunch& L, hipStream_t st) {
   // us with 256 x 256 tiles against 128 x 128 at (big tiles, rows per expert):
   // (128, 512) 20 / 17, (64, 8192) 85 / 60
   const int64_t big = up_to(L.N, 256) * up_to(L.K, 256) * L.E;
-  if (big >= 256 && L.cap * 256 < (int64_t(1) << 32)) return launch_big<1>(a, L.a_e5m2, L.out_bf16, big, st);
+  if (big >= 256 && L.cap * 256 < (int64_t(1) << 32)) {
+    // Where an XCD's chunk of 32 tiles (deal_tiles) reads more than its 4 MB of
+    // L2, one operand is better off leaving it first.  us so / kept, (N, K,
+    // experts, rows per expert): (2048, 2048, 16, 2048) 152 / 163, (2048, 2048,
+    // 8, 4096) 136 / 147, (4096, 2048, 8, 4096) 248 / 270, (2048, 4096, 8, 4096)
+    // 280 / 280, (2048, 1024, 16, 2048) 80 / 88; where it fits, (2048, 2048, 16,
+    // 1125) 100 / 93, and where tiles are dealt by eighths, (1280, 2048, 12,
+    // 2048) 117 / 107.  The products lose by it: 627 / 537.
+    const int64_t across = up_to(L.K, 256), cols = across < 32 ? across : 32, rows = up_to(32, cols);
+    if (dealt(int(big / L.E), L.E) && (rows + cols) * 256 * (L.cap / L.E) > (int64_t(4) << 20))
+      return launch_big<1, 1>(a, L.a_e5m2, L.out_bf16, big, st);
+    return launch_big<1, 0>(a, L.a_e5m2, L.out_bf16, big, st);
+  }
   const int64_t tiles = up_to(L.N, 128) * up_to(L.K, 128) * L.E;
   // a workgroup to a CU: three stages for it; more: two, so that two fit.  us
   // with three / two at (tiles, rows per expert): (256, 2048) 27 / 33, (256,
