@@ -176,14 +176,13 @@ def _ptr(t) -> Optional[int]:
 def _dev(*ts):
     kind = _torch().Tensor
     for t in ts:
-        if t is None:
+        if t is None or (isinstance(t, kind) and t.is_cuda and t.is_contiguous()):
             continue
         if not isinstance(t, kind):
             raise TypeError("expected a torch.Tensor")
         if not t.is_cuda:
             raise ValueError("tensors must be on the GPU")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+        raise ValueError("tensors must be contiguous")
 
 
 _one_byte = None
@@ -565,9 +564,15 @@ def bsq_scaled_matmul_nvfp4(lhs, rhs, lhs_scales, rhs_scales, out, workspace, st
 
 # ------------------------------------------------------ expert layers ----
 
+_wide_codes = None
+
+
 def _wide(t, name):
-    torch = _torch()
-    code = {torch.float32: BSQ_F32, torch.bfloat16: BSQ_BF16}.get(t.dtype)
+    global _wide_codes
+    if _wide_codes is None:
+        torch = _torch()
+        _wide_codes = {torch.float32: BSQ_F32, torch.bfloat16: BSQ_BF16}
+    code = _wide_codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     return code
