@@ -875,12 +875,18 @@ bsq_status launch_moe_wgrad(const MoeGemmLaunch& L, hipStream_t st) {
       return launch_big<1, 1>(a, L.a_e5m2, L.out_bf16, big, st);
     return launch_big<1, 0>(a, L.a_e5m2, L.out_bf16, big, st);
   }
-  const int64_t tiles = up_to(L.N, 128) * up_to(L.K, 128) * L.E;
+  // Few tiles leave CUs idle: the smallest tiles of which no CU gets two.  us
+  // with 64 x 64 / 64 x 128 / 128 x 128 at (N, K, experts, rows per expert):
+  // (512, 512, 4, 8192) 25 / 33 / 44, (1024, 512, 4, 8192) 45 / 36 / 44, (1024,
+  // 768, 4, 4096) 48 / 43 / 34, (640, 640, 8, 4096) 64 / 46 / 36
+  auto tiles = [&](int tn, int tk) { return up_to(L.N, tn) * up_to(L.K, tk) * L.E; };
+  if (tiles(64, 64) <= kCUs) return launch<2, 2, 2, 2, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(64, 64), st);
+  if (tiles(64, 128) <= kCUs) return launch<2, 2, 2, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(64, 128), st);
   // a workgroup to a CU: three stages for it; more: two, so that two fit.  us
   // with three / two at (tiles, rows per expert): (256, 2048) 27 / 33, (256,
   // 8192) 48 / 60, (512, 512) 21 / 17
-  if (tiles <= kCUs) return launch<2, 2, 4, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles, st);
-  return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, tiles, st);
+  if (tiles(128, 128) <= kCUs) return launch<2, 2, 4, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(128, 128), st);
+  return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, tiles(128, 128), st);
 }
 
 }  // namespace bsq

@@ -607,6 +607,15 @@ def test_wgrad_of_long_contractions():
     test_wgrad([9, 7, 6, 8, 0, 4, 1, 3, 2], 1296, 1056, True, True)
 
 
+@pytest.mark.parametrize("blocks,N,K", [
+    # 64 x 64 tiles, 64 x 128, 128 x 128 (one to a CU, then more), by how many there are
+    ([5, 0, 4], 1040, 272), ([3, 0, 1, 6], 1040, 272), ([1, 2, 0, 5, 3, 1], 1040, 272), ([1, 0, 2, 1] * 25, 80, 272)])
+@pytest.mark.parametrize("e5m2,bf16", [(True, True), (False, False), (True, False), (False, True)])
+def test_wgrad_of_few_tiles(blocks, N, K, e5m2, bf16):
+    say("wgrad few tiles", e5m2, bf16)
+    test_wgrad(blocks, N, K, e5m2, bf16)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_swiglu_of_infinite_values(bf16):
     """silu(inf) u = inf u, which takes the block's largest code; -inf has no
