@@ -846,13 +846,26 @@ bsq_status launch_moe_product(const MoeGemmLaunch& L, hipStream_t st) {
   // address rows with 32 bits.
   if (rows >= 160 && (n / 256 + L.E / 2) * up_to(L.N, 256) >= 160 && L.T * L.K < (int64_t(1) << 32))
     return launch_big<0, 0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
-  // 64 x 128 against 128 x 128: (255, 8, 1792, 1024) 12.1 / 14.8, (192, 64,
-  // 2048, 1024) 79 / 78; against 64 x 64: (37, 32, 2048, 1024, segments
-  // aligned to 128) 26 / 32
-  if (rows >= 32) return launch<2, 2, 2, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
+  // Few tiles leave CUs idle: the smallest tiles of which no CU gets two (half
+  // a part-full tile to an expert on average; rows that a plan's alignment
+  // leaves empty count, as their workgroups start too).  us so / with 64 x 128
+  // and two stages at (rows per expert, experts, N, K): 32 x 64 tiles (250, 4,
+  // 256, 4096) 13 / 26, 64 x 64 (256, 4, 512, 4096) 16 / 26, 64 x 128 (250, 4,
+  // 1536, 2048) 13 / 16; with more tiles than that, (325, 4, 1536, 2048), 64 x
+  // 64 takes 19, 64 x 128 with three stages 18, with two 17
+  auto few = [&](int tm, int tn) { return (L.cap / tm + (L.E + 1) / 2) * up_to(L.N, tn) <= kCUs; };
+  if (few(32, 64)) return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
+  if (rows >= 32) {
+    if (few(64, 64)) return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
+    if (few(64, 128)) return launch<2, 2, 2, 4, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
+    // 64 x 128 against 128 x 128: (255, 8, 1792, 1024) 12.1 / 14.8, (192, 64,
+    // 2048, 1024) 79 / 78; against 64 x 64: (37, 32, 2048, 1024, segments
+    // aligned to 128) 26 / 32
+    return launch<2, 2, 2, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
+  }
   // few rows, where the weights' bytes are most of the work: three stages
   // against two (1, 32, 4096, 2048) 33 / 42; 32 rows against 64 (8, 32, 2048,
-  // 1024) 13.8 / 16.4
+  // 1024) 13.8 / 16.4, (25, 32, 4096, 2048) 74 / 70
   if (rows > 16) return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
   return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
 }

@@ -519,6 +519,17 @@ def test_matmul(lengths, T, N, K, k, opts):
     _check_product(lengths, T, N, K, k, **opts)
 
 
+@pytest.mark.parametrize("N,lengths", [
+    # 64 x 64 tiles, 64 x 128 in three stages and in two, by how many there are; 64 x 64 for 17 to 31 rows an expert
+    (784, [300, 0, 500, 3]), (1296, [300, 0, 500, 3]), (2576, [300, 0, 500, 3]), (720, [25, 0, 64, 1] * 5)])
+@pytest.mark.parametrize("K,opts", [(128, dict(bf16=False)), (384, dict(e5m2=True, tail=3)), (512, dict(gather=False)),
+                                    (256, dict(e5m2=True, bf16=False))])
+def test_matmul_by_number_of_tiles(N, lengths, K, opts):
+    T = sum(lengths) if not opts.get("gather", True) else 90
+    say("moe matmul tiles", len(lengths), sum(lengths), T, N, K, opts)
+    _check_product(lengths, T, N, K, 1 if T > 90 else 2, **opts)
+
+
 def test_matmul_without_tokens_or_contraction_writes_zeros():
     torch = _torch()
     say("moe matmul empty")
