@@ -574,9 +574,22 @@ struct RouteBwdArgs {
   void* dlogits;
 };
 
-// With total = the sum of the chosen p: dp at a choice is
-// scale (dw - sum(dw p) / total) / total where renormalised, else scale dw,
-// plus dscores; softmax dx = p (dp - sum p dp), sigmoid dx = dp p (1 - p).
+// Softmax dx = p (dp - sum p dp), sigmoid dx = dp p (1 - p), with dp the sum
+// of dscores and, at a choice, of scale dw.  Renormalised, w = p / sum p over
+// the choices: p dp is scale w (dw - sum w dw) there, and these sum to nothing
+// over the choices.  w is an ordinary number also where p and the sum are
+// nothing in 32 bits (a bias steers the choice only), so p dp is made of w, and
+// w of e^x relative to the largest chosen x; 1 / sum p is never formed.
+
+// A choice's share of the sum, before the division: e^(x - m), or e^-m /
+// (1 + e^-x), m the largest chosen x, of sigmoids at most 0.
+__device__ __forceinline__ float share(bool sigmoid, float x, float m) {
+  if (x == -INFINITY) return 0.f;
+  if (!sigmoid) return expf(x - m);
+  const float r = 1.0f / (1.0f + expf(-fabsf(x)));
+  return expf(fminf(x, 0.f) - fminf(m, 0.f)) * r;
+}
+
 // One wave per token; `dps` is E floats of LDS that belong to this wave.
 template <int BF16, int EPL>
 __device__ void route_backward_token(const RouteBwdArgs& a, int64_t t, int lane, float* dps) {
@@ -610,20 +623,16 @@ __device__ void route_backward_token(const RouteBwdArgs& a, int64_t t, int lane,
 #pragma unroll
     for (int i = 0; i < EPL; ++i) p[i] *= r;
   }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) dps[lane + 64 * i] = p[i];
-  __builtin_amdgcn_wave_barrier();
-  __threadfence_block();
   const int id = lane < a.k ? a.ids[t * a.k + lane] : -1;
   const bool on = id >= 0 && id < E;
-  const float pc = on ? dps[id] : 0.f;
+  const float xc = on ? logit_at<BF16>(a.logits, t * E + id) : -INFINITY;
   float d = on ? a.dweights[t * a.k + lane] * a.scale : 0.f;
   if (a.renorm) {
-    const float total = wave_sum(pc);
-    const float r = total == 0.f ? 0.f : 1.0f / total;
-    d = (d - wave_sum(d * (pc * r))) * r;
+    const float s = share(a.sigmoid, xc, wave_max(xc)), total = wave_sum(s);
+    const float w = total == 0.f ? 0.f : s / total;
+    d = w * (d - wave_sum(w * d));
+    if (a.sigmoid) d *= 1.0f / (1.0f + expf(xc));
   }
-  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int i = 0; i < EPL; ++i) dps[lane + 64 * i] = 0.f;
   __builtin_amdgcn_wave_barrier();
@@ -631,11 +640,12 @@ __device__ void route_backward_token(const RouteBwdArgs& a, int64_t t, int lane,
   if (on) dps[id] = d;
   __builtin_amdgcn_wave_barrier();
   __threadfence_block();
-  float dot = 0.f;
+  float c[EPL], dot = 0.f;  // c: what the choices add to dx
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
-    dp[i] = dps[e];
+    c[i] = a.renorm ? dps[e] : 0.f;
+    dp[i] = a.renorm ? 0.f : dps[e];
     if (a.dscores != nullptr && e < E) dp[i] += a.dscores[t * E + e];
     if (e < E) dot += p[i] * dp[i];
   }
@@ -645,7 +655,7 @@ __device__ void route_backward_token(const RouteBwdArgs& a, int64_t t, int lane,
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     if (e < E) {
-      const float dx = a.sigmoid ? dp[i] * p[i] * q[i] : p[i] * (dp[i] - dot);
+      const float dx = c[i] + (a.sigmoid ? dp[i] * p[i] * q[i] : p[i] * (dp[i] - dot));
       if (BF16)
         static_cast<uint16_t*>(a.dlogits)[t * E + e] = uint16_t(encode_bf16(dx));
       else
@@ -688,11 +698,8 @@ __global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
     *reinterpret_cast<float4*>(mine + o) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __builtin_amdgcn_wave_barrier();
-  float r = 0.f, top = 0.f, pc;
-  if (a.sigmoid) {
-    pc = 1.0f / (1.0f + expf(-xc));
-  } else {
-    top = p[0];
+  if (!a.sigmoid) {
+    float top = p[0];
 #pragma unroll
     for (int i = 1; i < S; ++i) top = fmaxf(top, p[i]);
     top = row_max(top);
@@ -703,27 +710,29 @@ __global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
       sum += p[i];
     }
     sum = row_sum(sum);
-    r = sum == 0.f ? 0.f : 1.0f / sum;
+    const float r = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < S; ++i) p[i] *= r;
-    pc = xc == -INFINITY ? 0.f : expf(xc - top) * r;
   }
   if (a.renorm) {
-    const float total = row_sum(on ? pc : 0.f);
-    const float rt = total == 0.f ? 0.f : 1.0f / total;
-    d = (d - row_sum(d * (pc * rt))) * rt;
+    const float s = share(a.sigmoid, xc, row_max(xc)), total = row_sum(s);
+    const float w = total == 0.f ? 0.f : s / total;
+    d = w * (d - row_sum(w * d));
+    if (a.sigmoid) d *= 1.0f / (1.0f + expf(xc));
   }
   if (on) mine[id] = d;
   __builtin_amdgcn_wave_barrier();
   __threadfence_block();
-  float dp[S], dot = 0.f;
+  float c[S], dp[S], dot = 0.f;  // c: what the choices add to dx
 #pragma unroll
   for (int q = 0; q < S / 4; ++q) {
     const float4 v = *reinterpret_cast<const float4*>(mine + (q * 16 + l) * 4);
-    dp[4 * q] = v.x;
-    dp[4 * q + 1] = v.y;
-    dp[4 * q + 2] = v.z;
-    dp[4 * q + 3] = v.w;
+    const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[4 * q + i] = a.renorm ? u[i] : 0.f;
+      dp[4 * q + i] = a.renorm ? 0.f : u[i];
+    }
   }
   if (a.dscores != nullptr)
 #pragma unroll
@@ -742,9 +751,9 @@ __global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
       if (a.sigmoid) {
         // p and 1 - p, without the cancellation
         const float z = expf(-fabsf(p[j])), rz = 1.0f / (1.0f + z);
-        dx[i] = dp[j] * (z * rz) * rz;
+        dx[i] = c[j] + dp[j] * (z * rz) * rz;
       } else {
-        dx[i] = p[j] * (dp[j] - dot);
+        dx[i] = c[j] + p[j] * (dp[j] - dot);
       }
     }
     const int o = (q * 16 + l) * 4;

@@ -23,6 +23,20 @@ def scores(x, sigmoid: bool) -> np.ndarray:
         return np.where(total > 0, p / np.where(total > 0, total, 1.0), 0.0)
 
 
+def shares(x, on, sigmoid: bool) -> np.ndarray:
+    """p / sum of p over the logits [T, k] that are `on`: of e^x or
+    1 / (1 + e^-x) times a power of e that makes the row's largest ordinary, so
+    that no row of finite logits is lost to underflow; zeros for a row of -inf."""
+    x = np.where(on, np.asarray(x, np.float64), -np.inf)
+    with np.errstate(over="ignore", invalid="ignore"):
+        m = x.max(1, keepdims=True)
+        m = np.minimum(m, 0.0) if sigmoid else m
+        m = np.where(m == -np.inf, 0.0, m)
+        a = np.exp(np.minimum(x, 0.0) - m) / (1.0 + np.exp(-np.abs(x))) if sigmoid else np.exp(x - m)
+        total = a.sum(1, keepdims=True)
+    return np.where(total == 0, 0.0, a / np.where(total == 0, 1.0, total))
+
+
 def route(x, k, bias=None, groups=1, top_groups=1, group_top=1, sigmoid=False, renorm=True, scale=1.0):
     """(ids [T, k], weights [T, k], p [T, E])."""
     p = scores(x, sigmoid)
@@ -56,23 +70,24 @@ def route_backward(x, ids, dw, ds=None, sigmoid=False, renorm=True, scale=1.0):
     d = np.where(on, np.asarray(dw, np.float64) * scale, 0.0)
     m = np.abs(d)
     if renorm:
-        total = pc.sum(1, keepdims=True)
-        r = np.where(total > 0, 1.0 / np.where(total > 0, total, 1.0), 0.0)
-        d = (d - (d * pc * r).sum(1, keepdims=True)) * r
-        m = (m + (m * pc * r).sum(1, keepdims=True)) * r
-    dp, mp = np.zeros((T, E)), np.zeros((T, E))
+        # of w = p / sum: w (d - sum w d) = p dp, the factor 1 - p of a sigmoid aside
+        w = shares(np.take_along_axis(np.asarray(x, np.float64), at, 1), on, sigmoid)
+        d, m = w * (d - (w * d).sum(1, keepdims=True)), w * (m + (w * m).sum(1, keepdims=True))
+    else:
+        d, m = d * pc, m * pc
+    c, mc = np.zeros((T, E)), np.zeros((T, E))  # p dp of the choices
     for t in range(T):
         for j in range(ids.shape[1]):
             if on[t, j]:
-                dp[t, ids[t, j]] += d[t, j]
-                mp[t, ids[t, j]] += m[t, j]
+                c[t, ids[t, j]] += d[t, j]
+                mc[t, ids[t, j]] += m[t, j]
     if ds is not None:
-        dp += ds
-        mp += np.abs(ds)
+        c += p * ds
+        mc += p * np.abs(ds)
     if sigmoid:
         q = scores(-np.asarray(x, np.float64), True)
-        return dp * p * q, mp * p * q
-    return p * (dp - (p * dp).sum(1, keepdims=True)), p * (mp + (p * mp).sum(1, keepdims=True))
+        return c * q, mc * q
+    return c - p * c.sum(1, keepdims=True), mc + p * mc.sum(1, keepdims=True)
 
 
 def plan(ids, E, align, cap):

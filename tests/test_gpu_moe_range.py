@@ -1,0 +1,119 @@
+"""Expert-layer operators at the ends of their range, against oracle/moe.py:
+scores that are nothing in 32 or in 64 bits, biases that rule experts out,
+NaN.
+
+Bounds.  Forward: scores and weights are made in 64 bits to a relative 2^-38
+and rounded once, half a step of 2^-24 relative, or of the least number of 32
+bits.  Gradient, in 32 bits: an exponential's argument is off by half a step
+of itself, which becomes a relative error of the result (at most 104 steps: a
+larger argument gives less than the least number); beside it at most 32
+roundings (exponentials, sums over the lanes, divisions, products); three such
+factors in a term and as much again for the sums that are taken off it.
+"""
+import numpy as np
+import pytest
+
+import block_scaled_precision_blockwise_amd as bsq
+from oracle import formats as F
+from oracle import moe as OE
+
+from gpu_helpers import filled, host, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+TINY = 1e-37  # below this float32 results are denormal
+LEAST = 2.0 ** -149
+FEW, MANY = 37, 2051  # a wave to a token, and four tokens to a wave
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _logits(x, bf16):
+    """(device tensor, the float64 values it holds)."""
+    torch = _torch()
+    x = np.asarray(x, np.float32)
+    if not bf16:
+        return to_dev(x), x.astype(np.float64)
+    bits = F.encode_bf16(x)
+    return to_dev(bits.view(np.int16)).view(torch.bfloat16), F.decode_bf16(bits).astype(np.float64)
+
+
+def _values(t):
+    h = host(t)
+    return F.decode_bf16(h).astype(np.float64) if h.dtype == np.uint16 else h.astype(np.float64)
+
+
+def _within(got, want, bound, what):
+    got = np.asarray(got, np.float64)
+    assert np.all(np.isfinite(got)), f"{what}: not finite at {np.argwhere(~np.isfinite(got))[:3].tolist()}"
+    bad = np.argwhere(~(np.abs(got - want) <= bound))
+    if len(bad):
+        i = tuple(bad[0])
+        raise AssertionError(f"{what}: {len(bad)} of {got.size} outside; first {i}: {got[i]!r} for {want[i]!r}, "
+                             f"bound {np.broadcast_to(bound, got.shape)[i]!r}")
+
+
+def _span(x, ids):
+    """Relative error of a gradient's exponentials (see above)."""
+    top = x.max(1, keepdims=True)
+    chosen = np.take_along_axis(x, np.where((ids >= 0) & (ids < x.shape[1]), ids, 0).astype(np.int64), 1)
+    far = np.maximum(np.abs(np.where(np.isfinite(x), x - np.where(np.isfinite(top), top, 0.0), 0.0)).max(1),
+                     np.where(np.isfinite(chosen), np.ptp(np.where(np.isfinite(chosen), chosen, 0.0), axis=1)[:, None],
+                              0.0).max(1))
+    return (2 * np.minimum(far, 104.0)[:, None] + 32) * 2.0 ** -24
+
+
+def _check_backward(x, bf16, ids, ds=None, sigmoid=False, renorm=True, scale=2.5, seed=0):
+    torch = _torch()
+    dx, xv = _logits(x, bf16)
+    rng = np.random.default_rng(seed + 7)
+    dw = rng.standard_normal(ids.shape).astype(np.float32)
+    dl = filled(xv.shape, dx.dtype, float("nan"))
+    bsq.bsq_moe_route_backward(dx, to_dev(np.asarray(ids, np.int32)), to_dev(dw), dl,
+                               dscores=None if ds is None else to_dev(ds), score=int(sigmoid), renorm=renorm, scale=scale)
+    want, size = OE.route_backward(xv, ids, dw, ds, sigmoid, renorm, scale)
+    half = 2.0 ** -8 if bf16 else 2.0 ** -24
+    _within(_values(dl), want, 6 * _span(xv, np.asarray(ids)) * size + half * np.abs(want) + TINY, "dlogits")
+    if renorm and ids.shape[1] > 1:
+        assert np.abs(want).max() > 0.01  # the case has a gradient to lose
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("far", [60, 86, 88.5, 90, 100, 110, 200, 700, 740, 3000])
+def test_route_gradient_of_chosen_scores_that_are_nothing_in_32_bits(T, sigmoid, far):
+    """Softmax: a bias has steered the choice to experts `far` below the row's
+    largest logit.  Sigmoid: every logit is near -far.  The weights p / sum
+    are ordinary numbers, and so are their gradients."""
+    say("route gradient far", T, sigmoid, far)
+    rng = np.random.default_rng(int(far) + T)
+    for E, k, bf16 in ((5, 2, False), (96, 6, False), (256, 8, True), (20, 1, False), (320, 12, False)):
+        x = rng.standard_normal((T, E)) - far
+        if not sigmoid:
+            x[:, E - 2:] += far  # never chosen
+        ids = np.stack([rng.permutation(E - 2 if E > 5 else 3)[:k] for _ in range(T)]).astype(np.int32)
+        ds = (rng.standard_normal((T, E)) * 0.1).astype(np.float32) if E != 96 else None
+        _check_backward(x, bf16, ids, ds, sigmoid, seed=E)
+        _check_backward(x, bf16, ids, ds, sigmoid, renorm=False, seed=E)
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_gradient_beside_masked_logits_and_ids_that_are_none(T, sigmoid):
+    say("route gradient masked", T, sigmoid)
+    rng = np.random.default_rng(T)
+    E, k = 24, 4
+    x = (rng.standard_normal((T, E)) * 2).astype(np.float32)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    x[0::6] = -np.inf                                   # a row of nothing
+    np.put_along_axis(x[1::6], ids[1::6].astype(np.int64), -np.inf, 1)   # nothing chosen is left
+    np.put_along_axis(x[2::6], ids[2::6, :2].astype(np.int64), -np.inf, 1)
+    np.put_along_axis(x[3::6], ids[3::6, 1:2].astype(np.int64), -1e9, 1)
+    np.put_along_axis(x[4::6], ids[4::6].astype(np.int64), x[4::6, :k] - 95.0, 1)
+    ids[::5, 0] = -1
+    ids[1::5, 1] = E
+    for ds in (None, (rng.standard_normal((T, E)) * 0.1).astype(np.float32)):
+        _check_backward(x, False, ids, ds, sigmoid, seed=1)
