@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsq.so")
 SOURCES = ["api.hip", "api_moe.hip", "quant.hip", "gemm.hip", "route.hip", "rows.hip", "gate.hip", "moe_gemm.hip"]
-HEADERS = ["common.h", "fp8.h", "quant.h", "gemm.h", "moe.h"]
+HEADERS = ["common.h", "fp8.h", "quant.h", "gemm.h", "moe.h", "moe_index.h"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

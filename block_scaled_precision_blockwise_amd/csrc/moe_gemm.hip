@@ -34,6 +34,7 @@
 // 16 - 19 ns per 16 x 16 x 128, not the 13.3 of 2.4 GHz.  8 tokens over 32
 // experts (N 4096, K 2048): 33 us, 5.3 TB/s of weights.
 #include "moe.h"
+#include "moe_index.h"
 
 #include <type_traits>
 
@@ -136,48 +137,31 @@ __device__ __forceinline__ v8i frag(const uint8_t* tile, int off0, int off1) {
   return v8i{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
 }
 
-__device__ __forceinline__ int bounded(int v, int64_t cap) { return v < 0 ? 0 : (v > cap ? int(cap) : v); }
-
-// Segment of the mt-th tile of TM rows when every segment is cut into tiles
-// from its first row: expert (E: the rows past the last segment), first row
-// and end.  `total` is the number of tiles.  Every wave computes it alone:
-// lane l sums the tiles of segments [l c, (l + 1) c), a scan over the lanes
-// finds the lane, and that lane's segments are walked.
-struct Segment {
-  int e, row0, end;
-};
-__device__ __forceinline__ int tiles_total(const MoeArgs& a, int tm, int lane, int& mine_before, int& mine) {
-  const int S = a.E + 1, c = (S + 63) / 64;
-  int n = 0;
-  for (int i = lane * c; i < min((lane + 1) * c, S); ++i) {
-    const int lo = bounded(a.offsets[i], a.cap), hi = i < a.E ? bounded(a.offsets[i + 1], a.cap) : int(a.cap);
-    n += hi > lo ? (hi - lo + tm - 1) / tm : 0;
-  }
-  int s = n;
+// The tiles of all segments (`total`), and the segment of the mt-th.  Every
+// wave computes it alone: lane l sums the tiles of its share of the segments,
+// a scan over the lanes finds the lane, and that lane's segments are walked.
+template <int TM>
+__device__ __forceinline__ Segments<TM> segments(const MoeArgs& a) {
+  return Segments<TM>{a.offsets, a.E, a.cap};
+}
+template <int TM>
+__device__ __forceinline__ int tiles_total(const MoeArgs& a, int lane, uint32_t& mine_before, uint32_t& mine) {
+  mine = segments<TM>(a).lane_tiles(lane);
+  uint32_t s = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(s, d);
+    const uint32_t o = __shfl_up(s, d);
     if (lane >= d) s += o;
   }
-  mine_before = s - n;
-  mine = n;
-  return __builtin_amdgcn_readlane(s, 63);
+  mine_before = s - mine;
+  const uint32_t total = uint32_t(__builtin_amdgcn_readlane(int(s), 63)), limit = uint32_t(segments<TM>(a).limit());
+  return scalar(int(total < limit ? total : limit));
 }
-__device__ __forceinline__ Segment find_tile(const MoeArgs& a, int tm, int lane, int mt, int mine_before, int mine) {
-  const int S = a.E + 1, c = (S + 63) / 64;
-  const uint64_t here = __ballot(mt >= mine_before && mt < mine_before + mine);
+template <int TM>
+__device__ __forceinline__ Segment find_tile(const MoeArgs& a, int mt, uint32_t mine_before, uint32_t mine) {
+  const uint64_t here = __ballot(Segments<TM>::has(mine_before, mine, mt));
   const int l = here ? __ffsll((unsigned long long)here) - 1 : 63;
-  int left = mt - __builtin_amdgcn_readlane(mine_before, l);
-  Segment s{a.E, int(a.cap), int(a.cap)};
-  for (int i = l * c; i < min((l + 1) * c, S); ++i) {
-    const int lo = bounded(a.offsets[i], a.cap), hi = i < a.E ? bounded(a.offsets[i + 1], a.cap) : int(a.cap);
-    const int n = hi > lo ? (hi - lo + tm - 1) / tm : 0;
-    if (left < n) {
-      s = Segment{i, lo + left * tm, hi};
-      break;
-    }
-    left -= n;
-  }
+  Segment s = segments<TM>(a).at(l, mt - __builtin_amdgcn_readlane(int(mine_before), l));
   s.e = __builtin_amdgcn_readfirstlane(s.e);
   s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
   s.end = __builtin_amdgcn_readfirstlane(s.end);
@@ -230,7 +214,8 @@ struct View {
 //            that each gets as many steps (expert e's rank is `before` of lane
 //            e).  0: an eighth of the tiles to each XCD.
 struct Deal {
-  int total, before, mine;
+  int total;
+  uint32_t before, mine;
 };
 // Chunks that are mostly full, experts that fit the lanes.
 __host__ __device__ inline bool dealt(int per, int E) {
@@ -241,7 +226,7 @@ template <int TM, int TN, int WGRAD>
 __device__ __forceinline__ Deal deal_tiles(const MoeArgs& p, int lane) {
   Deal d{0, 0, 0};
   if (!WGRAD) {
-    d.total = tiles_total(p, TM, lane, d.before, d.mine);
+    d.total = tiles_total<TM>(p, lane, d.before, d.mine);
     return d;
   }
   // 16 experts of 2048 x 2048 over 32768 rows, segments of 0.5 to 2 times the
@@ -272,7 +257,7 @@ __device__ __forceinline__ bool find_place(const MoeArgs& p, int lane, const Dea
         if (q >= chunks * p.E) return false;
         in = q % chunks * 32 + (L % int(kCUs)) / 8;
         if (in >= per) continue;
-        t.e = __ffsll((unsigned long long)__ballot(lane < p.E && d.before == q / chunks)) - 1;
+        t.e = __ffsll((unsigned long long)__ballot(lane < p.E && int(d.before) == q / chunks)) - 1;
         break;
       }
     } else {
@@ -292,7 +277,7 @@ __device__ __forceinline__ bool find_place(const MoeArgs& p, int lane, const Dea
     if (unsigned(L) >= unsigned(d.total) * unsigned(tiles_n)) return false;
     int tm, tn;
     tile_order(L, d.total, tiles_n, tm, tn);
-    const Segment s = find_tile(p, TM, lane, tm, d.before, d.mine);
+    const Segment s = find_tile<TM>(p, tm, d.before, d.mine);
     t.e = s.e < p.E ? s.e : 0;
     t.m0 = s.row0;
     t.m_end = s.end;

@@ -1,0 +1,122 @@
+"""The whole-number arithmetic of the ragged products (csrc/moe_index.h),
+compiled for the host and run over offsets that no plan writes and over
+arrays near the largest that the calls accept.  CPU only."""
+import os
+import shutil
+import subprocess
+import textwrap
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "block_scaled_precision_blockwise_amd", "csrc")
+
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="no C++ compiler")
+
+
+def _run(tmp_path, body):
+    """Compiles `body` (statements that call EXPECT) and runs it; signed
+    overflow ends it."""
+    src = tmp_path / "index.cpp"
+    src.write_text(textwrap.dedent(r"""
+        #include <cstdio>
+        #include <cstdlib>
+        #include <random>
+        #include <type_traits>
+        #include <vector>
+        #include "moe_index.h"
+        using namespace bsq;
+        #define EXPECT(c, ...) do { if (!(c)) { printf("line %d: %s: ", __LINE__, #c); printf(__VA_ARGS__); printf("\n"); \
+          exit(1); } } while (0)
+        // What the 64 lanes of a wave make of the segments.
+        template <int TM> struct Wave {
+          Segments<TM> s; uint32_t before[64], mine[64]; int total;
+          explicit Wave(Segments<TM> s_) : s(s_), total(0) {
+            uint64_t sum = 0;
+            for (int l = 0; l < 64; ++l) {
+              before[l] = uint32_t(sum);
+              sum += mine[l] = s.lane_tiles(l);
+            }
+            EXPECT(sum < uint64_t(1) << 32, "the lanes' sum");
+            total = sum < uint64_t(s.limit()) ? int(sum) : s.limit();
+          }
+          Segment at(int mt) const {
+            int found = -1;
+            for (int l = 0; l < 64; ++l)
+              if (s.has(before[l], mine[l], mt)) {
+                EXPECT(found < 0, "tile %d in two lanes", mt);
+                found = l;
+              }
+            EXPECT(found >= 0, "no lane has tile %d of %d", mt, total);
+            return s.at(found, mt - int(before[found]));
+          }
+        };
+        int main() {
+    """) + textwrap.dedent(body) + "\nputs(\"ok\"); return 0; }\n")
+    exe = tmp_path / "index"
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-fsanitize=signed-integer-overflow",
+                        "-fno-sanitize-recover=all", "-I", CSRC, str(src), "-o", str(exe)],
+                       capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_tiles_of_ascending_offsets(tmp_path):
+    """Every row is in one tile, in the order of the rows."""
+    _run(tmp_path, r"""
+        std::mt19937 g(1);
+        auto check = [&](auto tm) {
+          constexpr int TM = decltype(tm)::value;
+          for (int E : {1, 2, 63, 64, 65, 300, 1024})
+            for (int rep = 0; rep < 20; ++rep) {
+              std::vector<int32_t> o(E + 1);
+              int at = g() % 3;
+              for (int i = 0; i <= E; ++i) { o[i] = at; at += g() % 4 == 0 ? g() % 700 : g() % 2; }
+              const int64_t cap = o[E] + (rep % 2 ? g() % 500 : 0);
+              Wave<TM> w(Segments<TM>{o.data(), E, cap});
+              int row = o[0], mt = 0;
+              for (; mt < w.total; ++mt) {
+                const Segment s = w.at(mt);
+                EXPECT(s.row0 == row && s.end > row && s.end <= cap, "tile %d: row %d, not %d", mt, s.row0, row);
+                EXPECT(s.end == (s.e < E ? o[s.e + 1] : cap), "end of tile %d", mt);
+                row = s.row0 + TM < s.end ? s.row0 + TM : s.end;
+              }
+              EXPECT(row == cap, "rows up to %d of %d", row, int(cap));
+              EXPECT(w.total <= w.s.limit(), "%d tiles", w.total);
+            }
+        };
+        check(std::integral_constant<int, 32>{});
+        check(std::integral_constant<int, 64>{});
+        check(std::integral_constant<int, 256>{});
+    """)
+
+
+def test_tiles_of_offsets_that_do_not_ascend(tmp_path):
+    """Segments that overlap ask for up to E cap / tm tiles, past 2^31: there
+    are no more than ascending ones can have, and each is inside the arrays."""
+    _run(tmp_path, r"""
+        std::mt19937 g(2);
+        auto check = [&](auto tm) {
+          constexpr int TM = decltype(tm)::value;
+          for (int64_t cap : {int64_t(40), int64_t(65536), int64_t(1) << 27, (int64_t(1) << 27) + 77, int64_t(0x70000000)})
+            for (int E : {2, 64, 65, 1024})
+              for (int kind = 0; kind < 3; ++kind) {
+                std::vector<int32_t> o(E + 1);
+                for (int i = 0; i <= E; ++i)
+                  o[i] = kind == 0 ? (i & 1 ? int32_t(cap) : 0) : kind == 1 ? (i & 1 ? INT32_MAX : INT32_MIN)
+                                                                        : int32_t(g());
+                Wave<TM> w(Segments<TM>{o.data(), E, cap});
+                EXPECT(w.total >= 0 && w.total <= cap / TM + E + 1, "%d tiles of %d rows", w.total, TM);
+                for (int rep = 0; rep < 200 && w.total > 0; ++rep) {
+                  const int mt = rep == 0 ? 0 : rep == 1 ? w.total - 1 : int(g() % unsigned(w.total));
+                  const Segment s = w.at(mt);
+                  EXPECT(s.e >= 0 && s.e <= E && s.row0 >= 0 && s.row0 < s.end && s.end <= cap,
+                         "tile %d: segment %d, rows %d .. %d", mt, s.e, s.row0, s.end);
+                }
+              }
+        };
+        check(std::integral_constant<int, 32>{});
+        check(std::integral_constant<int, 64>{});
+        check(std::integral_constant<int, 256>{});
+    """)
