@@ -4,6 +4,7 @@
 
 #include "common.h"
 #include "moe.h"
+#include "moe_index.h"
 
 using namespace bsq;
 
@@ -205,7 +206,7 @@ bsq_status bsq_moe_matmul(int64_t T, int64_t cap, int64_t E, int64_t N, int64_t 
   BSQ_CHECK(is_wide(out_dtype), BSQ_ERR_UNSUPPORTED, "out_dtype must be F32 or BF16");
   BSQ_CHECK(K % 128 == 0 && N % 16 == 0, BSQ_ERR_UNSUPPORTED, "the library needs K % 128 == 0 and N % 16 == 0");
   BSQ_CHECK(E <= kMaxExperts, BSQ_ERR_UNSUPPORTED, "at most 1024 experts");
-  BSQ_CHECK(T <= kMaxInt && cap <= kMaxInt && k <= kMaxInt && N <= (int64_t(1) << 30) && K <= kMaxContraction,
+  BSQ_CHECK(T <= kMaxInt && cap <= kMaxRows && k <= kMaxInt && N <= (int64_t(1) << 30) && K <= kMaxContraction,
             BSQ_ERR_UNSUPPORTED, "extent too large");
   // the scale rows are addressed with 32-bit byte offsets
   BSQ_CHECK(elems_fit(E, N, K) && elems_fit(cap, N) && T * (K / 32) <= int64_t(0xFFFFFFFF) &&

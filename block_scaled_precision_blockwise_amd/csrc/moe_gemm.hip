@@ -297,7 +297,7 @@ __device__ __forceinline__ bool find_place(const MoeArgs& p, int lane, const Dea
 // The row of A of a tile's row r, -1 for none (product only): the choice at
 // the row, and the row of it.
 __device__ __forceinline__ int choice_at(const MoeArgs& p, const Place& t, int r) {
-  if (t.m0 + r >= t.m_end || t.nk == 0) return -1;
+  if (!row_in(t.m0, r, t.m_end) || t.nk == 0) return -1;
   return p.rows != nullptr ? p.rows[t.m0 + r] : t.m0 + r;
 }
 __device__ __forceinline__ int source_of(const MoeArgs& p, int choice) {
@@ -444,11 +444,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
     for (int q = 0; q < 16 / RPI; ++q) {
       const int rr = RPI * q + lane / LPR, cc = 4 * (lane % LPR);
       const int tr = 16 * MB * wm + 16 * i + rr;
-      const int m = t.m0 + tr, n = t.n0 + 16 * NB * wn + cc;
+      const int n = t.n0 + 16 * NB * wn + cc;
       v4f v = *reinterpret_cast<const v4f*>(stg + rr * kRowB + cc * 4);
       if (!WGRAD && src[tr] < 0) v = v4f{0.f, 0.f, 0.f, 0.f};
-      if (m < t.m_end && n < view.rows_b()) {
-        const int64_t o = view.out0(t) + int64_t(m) * view.rows_b() + n;
+      if (row_in(t.m0, tr, t.m_end) && n < view.rows_b()) {
+        const int64_t o = view.out0(t) + (int64_t(t.m0) + tr) * view.rows_b() + n;
         if (OUT_BF16) {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
           const uint32_t lo = encode_bf16(v[0]) | (encode_bf16(v[1]) << 16);
@@ -673,9 +673,9 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
     for (int i = 0; i < 8; ++i) {
       beside(i);
       const int tr = 128 * wm + 16 * i + r16;
-      const bool none = !WGRAD && src[buf][tr] < 0, in = t.m0 + tr < t.m_end;
+      const bool none = !WGRAD && src[buf][tr] < 0, in = row_in(t.m0, tr, t.m_end);
       if constexpr (OUT_BF16) {
-        const bool even_in = t.m0 + (tr & ~1) < t.m_end, odd_in = t.m0 + (tr | 1) < t.m_end;
+        const bool even_in = row_in(t.m0, tr & ~1, t.m_end), odd_in = row_in(t.m0, tr | 1, t.m_end);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {  // 64 columns
           uint32_t v[2][4];            // 8 columns of 32, twice

@@ -20,6 +20,9 @@ BSQ_INDEX int bounded(int v, int64_t cap) { return v < 0 ? 0 : (v > cap ? int(ca
 // stay below 2^32.
 constexpr int64_t kMaxRows = 0x7FFFFFFF - 0xFFFF;
 
+// Whether row r of a tile whose first row is row0 is before `end`.
+BSQ_INDEX bool row_in(int row0, int r, int end) { return r < end - row0; }
+
 // A tile's segment (E: the rows past the last), first row and segment's end.
 struct Segment {
   int e, row0, end;
@@ -38,7 +41,7 @@ struct Segments {
   BSQ_INDEX int hi(int i) const { return i < E ? bounded(offsets[i + 1], cap) : int(cap); }
   BSQ_INDEX int share() const { return (E + 64) / 64; }
   BSQ_INDEX int end(int lane) const { return (lane + 1) * share() < E + 1 ? (lane + 1) * share() : E + 1; }
-  static BSQ_INDEX int tiles(int lo, int hi) { return hi > lo ? (hi - lo + TM - 1) / TM : 0; }
+  static BSQ_INDEX int tiles(int lo, int hi) { return hi > lo ? (hi - lo - 1) / TM + 1 : 0; }
   // No more than these where the offsets ascend.  Others may ask for up to E
   // times as many, past 2^31: what passes the limit is not there.
   BSQ_INDEX int limit() const { return int(cap / TM) + E + 1; }

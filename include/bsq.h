@@ -425,8 +425,8 @@ bsq_status bsq_moe_combine_backward(int64_t T, int64_t H, int64_t cap, int64_t k
  *   offsets int32 [E + 1] (any row numbers, also unaligned), rows int32 [cap]
  *   out [cap, N] of out_dtype (BSQ_F32 or BSQ_BF16)
  * The input's gradient is the same call with the transposed weights.
- * Rules: K % 128 == 0, N % 16 == 0, T K / 32 and N K / 32 below 2^32 (else
- * UNSUPPORTED). */
+ * Rules: K % 128 == 0, N % 16 == 0, T K / 32 and N K / 32 below 2^32, cap
+ * at most 2^31 - 2^16 (else UNSUPPORTED). */
 bsq_status bsq_moe_matmul(int64_t T, int64_t cap, int64_t E, int64_t N, int64_t K, int64_t k,
                           const uint8_t* a, int a_dtype, const uint8_t* a_scales, const uint8_t* b,
                           int b_dtype, const uint8_t* b_scales, const int32_t* offsets,

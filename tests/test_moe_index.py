@@ -120,3 +120,30 @@ def test_tiles_of_offsets_that_do_not_ascend(tmp_path):
         check(std::integral_constant<int, 64>{});
         check(std::integral_constant<int, 256>{});
     """)
+
+
+def test_tiles_of_the_longest_segments(tmp_path):
+    """One segment as long as the arrays may be: its tiles are all there, and a
+    row of its last tile is inside if it is before the segment's end."""
+    _run(tmp_path, r"""
+        auto check = [&](auto tm) {
+          constexpr int TM = decltype(tm)::value;
+          for (int64_t cap : {kMaxRows, kMaxRows - 1, kMaxRows - TM + 1, int64_t(1) << 30})
+            for (int E : {1, 3, 1024})
+              for (int first : {0, 1, TM - 1, 70000}) {
+                std::vector<int32_t> o(E + 1, int32_t(cap));
+                o[0] = first;
+                Wave<TM> w(Segments<TM>{o.data(), E, cap});
+                const int want = int((cap - first + TM - 1) / TM);
+                EXPECT(w.total == want, "%d tiles, not %d", w.total, want);
+                const Segment s = w.at(want - 1);
+                EXPECT(s.row0 == first + int64_t(want - 1) * TM && s.end == cap, "last tile at %d", s.row0);
+                for (int r = 0; r < TM; ++r)
+                  EXPECT(row_in(s.row0, r, s.end) == (int64_t(s.row0) + r < cap), "row %d of the last tile", r);
+              }
+        };
+        check(std::integral_constant<int, 32>{});
+        check(std::integral_constant<int, 64>{});
+        check(std::integral_constant<int, 256>{});
+        EXPECT(row_in(0x7FFFFFFF - 0xFFFF - 3, 2, 0x7FFFFFFF - 0xFFFF) && !row_in(0x7FFFFFFF - 40, 255, 0x7FFFFFFF), "rows");
+    """)
