@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
     constexpr int kElem = OUT_BF16 ? 2 : 4;
     const int64_t pitch = int64_t(view.rows_b()) * kElem;
     const int n0 = t.n0 + 128 * wn, left = view.rows_b() - n0;  // columns of the wave
-    uint8_t* at = static_cast<uint8_t*>(p.out) + view.out0(t) * kElem + int64_t(t.m0 + 128 * wm) * pitch + n0 * kElem;
+    uint8_t* at = static_cast<uint8_t*>(p.out) + view.out0(t) * kElem + byte_at(t.m0, 128 * wm, pitch, n0, kElem);
     const bool odd = r16 & 1;
     uint8_t* const pair = at + (r16 & 14) * pitch + (odd ? 64 : 0) + 16 * g;
     at += r16 * pitch + 16 * g;

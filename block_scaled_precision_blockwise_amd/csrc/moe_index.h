@@ -23,6 +23,12 @@ constexpr int64_t kMaxRows = 0x7FFFFFFF - 0xFFFF;
 // Whether row r of a tile whose first row is row0 is before `end`.
 BSQ_INDEX bool row_in(int row0, int r, int end) { return r < end - row0; }
 
+// Byte of column n0 of row row0 + r of an array with `pitch` bytes to a row and
+// `elem` to a column.
+BSQ_INDEX int64_t byte_at(int row0, int r, int64_t pitch, int n0, int elem) {
+  return (int64_t(row0) + r) * pitch + int64_t(n0) * elem;
+}
+
 // A tile's segment (E: the rows past the last), first row and segment's end.
 struct Segment {
   int e, row0, end;

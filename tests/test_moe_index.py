@@ -147,3 +147,17 @@ def test_tiles_of_the_longest_segments(tmp_path):
         check(std::integral_constant<int, 256>{});
         EXPECT(row_in(0x7FFFFFFF - 0xFFFF - 3, 2, 0x7FFFFFFF - 0xFFFF) && !row_in(0x7FFFFFFF - 40, 255, 0x7FFFFFFF), "rows");
     """)
+
+
+def test_bytes_of_the_widest_outputs(tmp_path):
+    """Columns up to 2^30 of 4 bytes, rows of 2^32 bytes: no product of them
+    is cut to 32 bits."""
+    _run(tmp_path, r"""
+        for (int elem : {2, 4})
+          for (int n0 : {0, 128, 1 << 29, (1 << 29) + 256, (1 << 30) - 128})
+            for (int row0 : {0, 256, (1 << 30) - 256}) {  // of at most 2^60 elements
+              const int64_t pitch = (int64_t(1) << 30) * elem;
+              const __int128 want = (__int128(row0) + 128) * pitch + __int128(n0) * elem;
+              EXPECT(byte_at(row0, 128, pitch, n0, elem) == want, "row %d, column %d of %d bytes", row0, n0, elem);
+            }
+    """)
