@@ -13,6 +13,7 @@
 // was bound by instruction issue (245 us).
 #include "fp8.h"
 #include "moe.h"
+#include "moe_index.h"
 
 #include <type_traits>
 
@@ -39,6 +40,7 @@ struct GateArgs {
   int64_t R, F;
   const void* gu;
   uint8_t *h, *hs, *ht, *hts, *kept, *kepts;
+  int64_t first;  // workgroup or tile of this launch
 };
 
 // Eight columns of g, from element `at` of gu, and of u as loaded (zeros where
@@ -102,7 +104,7 @@ __device__ __forceinline__ void gate8(const GateArgs& a, const Raw<SRC_BF16>& ra
 template <int SRC_BF16, int CODE>
 __global__ void __launch_bounds__(256) k_swiglu_mx_rows(GateArgs a) {
   saturate_fp8();
-  const int64_t f8 = a.F / 8, f = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t f8 = a.F / 8, f = (a.first + blockIdx.x) * 256 + threadIdx.x;
   const bool in = f < a.R * f8, words = a.F % kTile == 0 && aligned4(a.hs) && aligned4(a.kepts);
   const int64_t r = in ? f / f8 : 0, c = in ? (f - r * f8) * 8 : 0;
   Raw<SRC_BF16> raw;
@@ -117,7 +119,7 @@ template <int SRC_BF16, int CODE>
 __global__ void __launch_bounds__(kThreads) k_swiglu_mx(GateArgs a) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * kTile];
   const int64_t tiles_c = (a.F + kTile - 1) / kTile;
-  const int64_t t = xcd_run(blockIdx.x, gridDim.x);
+  const int64_t t = a.first + xcd_run(blockIdx.x, gridDim.x);
   const int64_t r0 = t / tiles_c * kTile, c0 = t % tiles_c * kTile;
   const int tx = threadIdx.x, c8 = tx & 15;
   const int64_t c = c0 + 8 * c8;
@@ -203,26 +205,32 @@ __global__ void __launch_bounds__(256) k_swiglu_mx_backward(GateBwdArgs a) {
 
 bsq_status launch_swiglu_mx(int64_t R, int64_t F, const void* gu, bool bf16, bool e5m2, uint8_t* h, uint8_t* h_scales,
                             uint8_t* ht, uint8_t* ht_scales, uint8_t* kept, uint8_t* kept_scales, hipStream_t st) {
-  const GateArgs a{R, F, gu, h, h_scales, ht, ht_scales, kept, kept_scales};
   const int form = (bf16 ? 1 : 0) | (e5m2 ? 2 : 0);
+  GateArgs a{R, F, gu, h, h_scales, ht, ht_scales, kept, kept_scales, 0};
   if (ht == nullptr) {
-    const unsigned grid = unsigned((R * (F / 8) + 255) / 256);
+    return in_parts((R * (F / 8) + 255) / 256, kLaunchGroups, [&](int64_t first, int64_t n) {
+      a.first = first;
+      const unsigned grid = unsigned(n);
+      switch (form) {
+        case 0: hipLaunchKernelGGL((k_swiglu_mx_rows<0, 0>), grid, 256, 0, st, a); break;
+        case 1: hipLaunchKernelGGL((k_swiglu_mx_rows<1, 0>), grid, 256, 0, st, a); break;
+        case 2: hipLaunchKernelGGL((k_swiglu_mx_rows<0, 1>), grid, 256, 0, st, a); break;
+        default: hipLaunchKernelGGL((k_swiglu_mx_rows<1, 1>), grid, 256, 0, st, a);
+      }
+      return launch_status("swiglu_mx");
+    });
+  }
+  return in_parts(((R + kTile - 1) / kTile) * ((F + kTile - 1) / kTile), kLaunchGroups, [&](int64_t first, int64_t n) {
+    a.first = first;
+    const unsigned grid = unsigned(n);
     switch (form) {
-      case 0: hipLaunchKernelGGL((k_swiglu_mx_rows<0, 0>), grid, 256, 0, st, a); break;
-      case 1: hipLaunchKernelGGL((k_swiglu_mx_rows<1, 0>), grid, 256, 0, st, a); break;
-      case 2: hipLaunchKernelGGL((k_swiglu_mx_rows<0, 1>), grid, 256, 0, st, a); break;
-      default: hipLaunchKernelGGL((k_swiglu_mx_rows<1, 1>), grid, 256, 0, st, a);
+      case 0: hipLaunchKernelGGL((k_swiglu_mx<0, 0>), grid, kThreads, 0, st, a); break;
+      case 1: hipLaunchKernelGGL((k_swiglu_mx<1, 0>), grid, kThreads, 0, st, a); break;
+      case 2: hipLaunchKernelGGL((k_swiglu_mx<0, 1>), grid, kThreads, 0, st, a); break;
+      default: hipLaunchKernelGGL((k_swiglu_mx<1, 1>), grid, kThreads, 0, st, a);
     }
     return launch_status("swiglu_mx");
-  }
-  const unsigned grid = unsigned(((R + kTile - 1) / kTile) * ((F + kTile - 1) / kTile));
-  switch (form) {
-    case 0: hipLaunchKernelGGL((k_swiglu_mx<0, 0>), grid, kThreads, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((k_swiglu_mx<1, 0>), grid, kThreads, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_swiglu_mx<0, 1>), grid, kThreads, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_swiglu_mx<1, 1>), grid, kThreads, 0, st, a);
-  }
-  return launch_status("swiglu_mx");
+  });
 }
 
 bsq_status launch_swiglu_mx_backward(int64_t R, int64_t F, const uint8_t* kept, const uint8_t* kept_scales, bool e5m2,

@@ -56,6 +56,7 @@ struct MoeArgs {
   const int32_t *offsets, *rows;
   int64_t T, cap;
   int E, N, K, k;
+  int first;  // workgroup of this launch (k_moe_gemm)
 };
 
 // Buffer resource of `records` bytes (in range 0 .. 2^32 - 1) from `base`;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const View<WGRAD> view{p};
   Place t;
-  int L = blockIdx.x;
+  int L = p.first + int(blockIdx.x);
   Deal deal{0, 0, 0};
   if (!WGRAD) deal = deal_tiles<TM, TN, WGRAD>(p, lane);
   if (!find_place<TM, TN, WGRAD>(p, lane, deal, L, t)) return;
@@ -786,15 +787,18 @@ __global__ void __launch_bounds__(256, 1) k_moe_big(MoeArgs p) {
 }
 
 template <int WM, int WN, int MB, int NB, int S, int WGRAD>
-bsq_status launch(const MoeArgs& a, bool e5m2, bool bf16, int64_t grid, hipStream_t st) {
-  const dim3 g = dim3(unsigned(grid)), b = dim3(64 * WM * WN);
-  switch ((e5m2 ? 1 : 0) | (bf16 ? 2 : 0)) {
-    case 0: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 0, 0, WGRAD>), g, b, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 1, 0, WGRAD>), g, b, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 0, 1, WGRAD>), g, b, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 1, 1, WGRAD>), g, b, 0, st, a);
-  }
-  return launch_status(WGRAD ? "moe_wgrad" : "moe_matmul");
+bsq_status launch(MoeArgs a, bool e5m2, bool bf16, int64_t grid, hipStream_t st) {
+  return in_parts(grid, kLaunchGroups, [&](int64_t first, int64_t n) {
+    a.first = int(first);
+    const dim3 g = dim3(unsigned(n)), b = dim3(64 * WM * WN);
+    switch ((e5m2 ? 1 : 0) | (bf16 ? 2 : 0)) {
+      case 0: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 0, 0, WGRAD>), g, b, 0, st, a); break;
+      case 1: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 1, 0, WGRAD>), g, b, 0, st, a); break;
+      case 2: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 0, 1, WGRAD>), g, b, 0, st, a); break;
+      default: hipLaunchKernelGGL((k_moe_gemm<WM, WN, MB, NB, S, 1, 1, WGRAD>), g, b, 0, st, a);
+    }
+    return launch_status(WGRAD ? "moe_wgrad" : "moe_matmul");
+  });
 }
 
 template <int WGRAD, int STREAM_A>
@@ -811,7 +815,7 @@ bsq_status launch_big(const MoeArgs& a, bool e5m2, bool bf16, int64_t grid, hipS
 }
 
 MoeArgs args_of(const MoeGemmLaunch& L) {
-  return MoeArgs{L.A, L.B, L.SA, L.SB, L.out, L.offsets, L.rows, L.T, L.cap, L.E, int(L.N), int(L.K), L.k};
+  return MoeArgs{L.A, L.B, L.SA, L.SB, L.out, L.offsets, L.rows, L.T, L.cap, L.E, int(L.N), int(L.K), L.k, 0};
 }
 
 int64_t up_to(int64_t v, int64_t m) { return (v + m - 1) / m; }

@@ -16,6 +16,21 @@ namespace bsq {
 
 BSQ_INDEX int bounded(int v, int64_t cap) { return v < 0 ? 0 : (v > cap ? int(cap) : v); }
 
+// A launch has less than 2^32 threads.  Calls of one workgroup to a few tokens
+// are cut into launches of at most kLaunchTokens tokens (a multiple of 16, so
+// that every part of an array that is aligned is), calls of one to a tile or a
+// run of elements into launches of at most kLaunchGroups.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+constexpr int64_t kLaunchTokens = int64_t(1) << 24;
+constexpr int64_t kLaunchGroups = int64_t(1) << 22;  // of 256 or 512 threads
+// f(first, count) for each part; ends with the first status that is not zero.
+template <typename F>
+auto in_parts(int64_t n, int64_t most, F&& f) -> decltype(f(n, n)) {
+  decltype(f(n, n)) s{};
+  for (int64_t at = 0; at < n && int(s) == 0; at += most) s = f(at, n - at < most ? n - at : most);
+  return s;
+}
+
 // Rows that the products' arrays may have: 64 lanes with `limit` tiles each
 // stay below 2^32.
 constexpr int64_t kMaxRows = 0x7FFFFFFF - 0xFFFF;

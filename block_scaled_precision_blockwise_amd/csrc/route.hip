@@ -22,6 +22,7 @@
 
 #include "fp8.h"
 #include "moe.h"
+#include "moe_index.h"
 
 namespace bsq {
 
@@ -801,7 +802,7 @@ unsigned token_grid(int64_t T) {
 
 }  // namespace
 
-bsq_status launch_route(const RouteLaunch& L, hipStream_t st) {
+static bsq_status route_part(const RouteLaunch& L, hipStream_t st) {
   const RouteArgs a{L.T, L.E, L.k, L.groups, L.top_groups, L.group_top, L.logits, L.sigmoid, L.renorm, L.scale,
                     L.bias, L.ids, L.weights, L.scores};
   const bool even = (L.groups & (L.groups - 1)) == 0;
@@ -836,7 +837,7 @@ bsq_status launch_route(const RouteLaunch& L, hipStream_t st) {
   return launch_status("moe_route");
 }
 
-bsq_status launch_route_backward(const RouteBackwardLaunch& L, hipStream_t st) {
+static bsq_status route_backward_part(const RouteBackwardLaunch& L, hipStream_t st) {
   const RouteBwdArgs a{L.T, L.E, L.k, L.logits, L.sigmoid, L.renorm, L.scale, L.ids, L.dweights, L.dscores,
                        L.dlogits};
   if (L.E <= 256 && L.k <= 16 && L.T >= kRowTokens) {
@@ -855,6 +856,35 @@ bsq_status launch_route_backward(const RouteBackwardLaunch& L, hipStream_t st) {
     else hipLaunchKernelGGL((k_route_backward<0, epl.value>), token_grid(L.T), 256, 0, st, a);
   });
   return launch_status("moe_route_backward");
+}
+
+static const void* logits_from(const void* p, bool bf16, int64_t elem) {
+  return static_cast<const char*>(p) + elem * (bf16 ? 2 : 4);
+}
+
+bsq_status launch_route(const RouteLaunch& L, hipStream_t st) {
+  return in_parts(L.T, kLaunchTokens, [&](int64_t t, int64_t n) {
+    RouteLaunch P = L;
+    P.T = n;
+    P.logits = logits_from(L.logits, L.bf16, t * L.E);
+    P.ids += t * L.k;
+    P.weights += t * L.k;
+    if (L.scores != nullptr) P.scores += t * L.E;
+    return route_part(P, st);
+  });
+}
+
+bsq_status launch_route_backward(const RouteBackwardLaunch& L, hipStream_t st) {
+  return in_parts(L.T, kLaunchTokens, [&](int64_t t, int64_t n) {
+    RouteBackwardLaunch P = L;
+    P.T = n;
+    P.logits = logits_from(L.logits, L.bf16, t * L.E);
+    P.ids += t * L.k;
+    P.dweights += t * L.k;
+    if (L.dscores != nullptr) P.dscores += t * L.E;
+    P.dlogits = const_cast<void*>(logits_from(L.dlogits, L.bf16, t * L.E));
+    return route_backward_part(P, st);
+  });
 }
 
 }  // namespace bsq

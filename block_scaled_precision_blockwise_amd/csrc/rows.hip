@@ -3,6 +3,7 @@
 // experts' rows back to their tokens with their weights.
 #include "fp8.h"
 #include "moe.h"
+#include "moe_index.h"
 
 #include <type_traits>
 
@@ -191,6 +192,7 @@ struct GatherArgs {
   const int32_t* rows;
   const float* weights;
   uint8_t *codes, *scales, *codes_t, *scales_t;
+  int64_t first;  // tile of this launch
 };
 
 template <int SRC_BF16, int PAIRS, int CODE>
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(256) k_gather_mx(GatherArgs a) {
   __shared__ int src[kTile];
   __shared__ float wt[kTile];
   const int64_t tiles_r = (a.cap + kTile - 1) / kTile;
-  const int64_t t = xcd_run(blockIdx.x, gridDim.x);
+  const int64_t t = a.first + xcd_run(blockIdx.x, gridDim.x);
   const int64_t r0 = t % tiles_r * kTile, c0 = t / tiles_r * kTile;
   const int tx = threadIdx.x;
   if (tx < kTile) {
@@ -376,18 +378,21 @@ bsq_status launch_plan(int64_t n, int E, int align, int64_t cap, const int32_t* 
 bsq_status launch_gather_mx(int64_t T, int64_t H, int64_t cap, int k, const void* x, bool bf16, const int32_t* rows,
                             const float* weights, bool e5m2, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
                             uint8_t* scales_t, hipStream_t st) {
-  const GatherArgs a{T, H, cap, k, x, rows, weights, codes, scales, codes_t, scales_t};
-  const unsigned grid = unsigned(((cap + kTile - 1) / kTile) * ((H + kTile - 1) / kTile));
+  GatherArgs a{T, H, cap, k, x, rows, weights, codes, scales, codes_t, scales_t, 0};
   const int form = !bf16 ? 0 : weights != nullptr ? 1 : 2;
-  switch (form | (e5m2 ? 4 : 0)) {
-    case 0: hipLaunchKernelGGL((k_gather_mx<0, 0, 0>), grid, 256, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((k_gather_mx<1, 0, 0>), grid, 256, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_gather_mx<1, 1, 0>), grid, 256, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((k_gather_mx<0, 0, 1>), grid, 256, 0, st, a); break;
-    case 5: hipLaunchKernelGGL((k_gather_mx<1, 0, 1>), grid, 256, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_gather_mx<1, 1, 1>), grid, 256, 0, st, a);
-  }
-  return launch_status("moe_gather_mx");
+  return in_parts(((cap + kTile - 1) / kTile) * ((H + kTile - 1) / kTile), kLaunchGroups, [&](int64_t first, int64_t n) {
+    a.first = first;
+    const unsigned grid = unsigned(n);
+    switch (form | (e5m2 ? 4 : 0)) {
+      case 0: hipLaunchKernelGGL((k_gather_mx<0, 0, 0>), grid, 256, 0, st, a); break;
+      case 1: hipLaunchKernelGGL((k_gather_mx<1, 0, 0>), grid, 256, 0, st, a); break;
+      case 2: hipLaunchKernelGGL((k_gather_mx<1, 1, 0>), grid, 256, 0, st, a); break;
+      case 4: hipLaunchKernelGGL((k_gather_mx<0, 0, 1>), grid, 256, 0, st, a); break;
+      case 5: hipLaunchKernelGGL((k_gather_mx<1, 0, 1>), grid, 256, 0, st, a); break;
+      default: hipLaunchKernelGGL((k_gather_mx<1, 1, 1>), grid, 256, 0, st, a);
+    }
+    return launch_status("moe_gather_mx");
+  });
 }
 
 bsq_status launch_combine(int64_t T, int64_t H, int64_t cap, int k, const void* y, bool bf16, const int32_t* pos,
@@ -402,11 +407,14 @@ bsq_status launch_combine(int64_t T, int64_t H, int64_t cap, int k, const void* 
 
 bsq_status launch_combine_backward(int64_t T, int64_t H, int64_t cap, int k, const void* y, bool bf16,
                                    const int32_t* pos, const void* dout, float* dweights, hipStream_t st) {
-  const CombineArgs a{T, H, cap, k, y, pos, nullptr, dout, dweights};
-  const unsigned grid = unsigned((T + 3) / 4);
-  if (bf16) hipLaunchKernelGGL(k_combine_backward<1>, grid, 256, 0, st, a);
-  else hipLaunchKernelGGL(k_combine_backward<0>, grid, 256, 0, st, a);
-  return launch_status("moe_combine_backward");
+  return in_parts(T, kLaunchTokens, [&](int64_t t, int64_t n) {
+    const CombineArgs a{n, H, cap, k, y, pos + t * k, nullptr,
+                        static_cast<const char*>(dout) + t * H * (bf16 ? 2 : 4), dweights + t * k};
+    const unsigned grid = unsigned((n + 3) / 4);
+    if (bf16) hipLaunchKernelGGL(k_combine_backward<1>, grid, 256, 0, st, a);
+    else hipLaunchKernelGGL(k_combine_backward<0>, grid, 256, 0, st, a);
+    return launch_status("moe_combine_backward");
+  });
 }
 
 }  // namespace bsq

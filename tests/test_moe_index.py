@@ -161,3 +161,23 @@ def test_bytes_of_the_widest_outputs(tmp_path):
               EXPECT(byte_at(row0, 128, pitch, n0, elem) == want, "row %d, column %d of %d bytes", row0, n0, elem);
             }
     """)
+
+
+def test_launches_are_cut_below_the_threads_that_one_has(tmp_path):
+    """The parts cover every token once, in order; each is a launch that fits,
+    of 4 tokens to a workgroup of 256 threads, or of workgroups of 512."""
+    _run(tmp_path, r"""
+        for (int64_t n : {int64_t(0), int64_t(1), kLaunchTokens, kLaunchTokens + 1, int64_t(67108865), int64_t(0x7FFFFFFF)}) {
+          int64_t next = 0;
+          in_parts(n, kLaunchTokens, [&](int64_t at, int64_t count) {
+            EXPECT(at == next && count > 0 && at % 16 == 0, "part at %lld", (long long)at);
+            EXPECT((count + 3) / 4 * 256 <= kMaxThreads, "%lld tokens", (long long)count);
+            next = at + count;
+            return 0;
+          });
+          EXPECT(next == n, "%lld of %lld tokens", (long long)next, (long long)n);
+        }
+        EXPECT(kLaunchGroups * 512 <= kMaxThreads && kLaunchGroups % 8 == 0, "workgroups");
+        int calls = 0;
+        EXPECT(in_parts(100, 10, [&](int64_t, int64_t) { return ++calls == 3 ? 7 : 0; }) == 7 && calls == 3, "status");
+    """)
