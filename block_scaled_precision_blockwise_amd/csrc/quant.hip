@@ -18,6 +18,7 @@
 // lanes with DPP and permlane operations, which stay in the VALU.
 #include "common.h"
 #include "fp8.h"
+#include "moe_index.h"
 #include "quant.h"
 
 namespace bsq {
@@ -770,15 +771,7 @@ bsq_status launch_mx_cols(const MxT* jobs, int n, bool src_bf16, bool e5m2, hipS
   return launch_status("quant_mx (columns, transposed)");
 }
 
-bsq_status launch_int8_rows(int64_t B, int64_t D, const float* x, int8_t* xq, float* xs,
-                            hipStream_t st) {
-  if (B == 0) return ok();
-  if (D == 0) {
-    // an empty row is all zero: scale 1
-    hipLaunchKernelGGL(k_fill_u32, grid_for(B, 256), 256, 0, st, reinterpret_cast<uint32_t*>(xs), B,
-                       0x3F800000u);
-    return launch_status("int8_quant_rows");
-  }
+static bsq_status int8_rows_part(int64_t B, int64_t D, const float* x, int8_t* xq, float* xs, hipStream_t st) {
   const int64_t d4 = D / 4;
   uint32_t* q4 = reinterpret_cast<uint32_t*>(xq);
   const unsigned g = unsigned(B);
@@ -792,6 +785,21 @@ bsq_status launch_int8_rows(int64_t B, int64_t D, const float* x, int8_t* xq, fl
     hipLaunchKernelGGL(k_int8_rows_any, g, 256, 0, st, x, xq, xs, D);
   }
   return launch_status("int8_quant_rows");
+}
+
+bsq_status launch_int8_rows(int64_t B, int64_t D, const float* x, int8_t* xq, float* xs,
+                            hipStream_t st) {
+  if (B == 0) return ok();
+  if (D == 0) {
+    // an empty row is all zero: scale 1
+    hipLaunchKernelGGL(k_fill_u32, grid_for(B, 256), 256, 0, st, reinterpret_cast<uint32_t*>(xs), B,
+                       0x3F800000u);
+    return launch_status("int8_quant_rows");
+  }
+  // a workgroup to a row, in launches of fewer than 2^32 threads
+  return in_parts(B, kLaunchGroups, [&](int64_t row, int64_t n) {
+    return int8_rows_part(n, D, x + row * D, xq + row * D, xs + row, st);
+  });
 }
 
 bsq_status launch_int8_cols(int64_t D_in, int64_t D_out, const float* w, int8_t* wq, float* ws,

@@ -1,4 +1,4 @@
-"""Expert-layer calls on so many tokens, rows or tiles that one launch cannot
+"""Calls on so many tokens, rows or tiles that one launch cannot
 hold their threads: every block of the input repeats the first, and so has
 every block of the output to."""
 import pytest
@@ -134,3 +134,16 @@ def test_product_of_very_many_tiles():
         seg = out[e * (cap // E):(e + 1) * (cap // E)]
         assert torch.equal(seg[:T], few[e * T:(e + 1) * T])
         _repeats(seg, T, f"expert {e}")
+
+
+@pytest.mark.parametrize("D", [4, 3])
+def test_int8_codes_of_very_many_rows(D):
+    torch = _torch()
+    R = (1 << 24) + BLOCK
+    say("int8 rows large", R, D)
+    x = _repeated(torch.randn(BLOCK, D, device="cuda"), R // BLOCK)
+    q, s = torch.full((R, D), 99, dtype=torch.int8, device="cuda"), torch.full((R,), float("nan"), device="cuda")
+    bsq.bsq_int8_quant_rows(x, q, s)
+    assert torch.allclose(q[:BLOCK].float() * s[:BLOCK, None], x[:BLOCK], rtol=0, atol=float(s[:BLOCK].max()) * 0.501)
+    _repeats(q, BLOCK, "codes")
+    _repeats(s, BLOCK, "scales")
