@@ -107,6 +107,16 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// A choice's share of the sum of p over the choices, before the division: e^(x
+// - m), or e^-m / (1 + e^-x), m the largest chosen x, of sigmoids at most 0.
+// p itself is nothing where a bias has steered the choice to logits that lie
+// 750 below the row's largest; the share is not.
+__device__ __forceinline__ double share(bool sigmoid, double x, double m) {
+  if (x == -INFINITY) return 0.0;
+  if (!sigmoid) return exp(x - m);
+  return exp(fmin(x, 0.0) - fmin(m, 0.0)) / (1.0 + exp(-fabs(x)));
+}
+
 // One token by one wave, in 64 bits: lane l holds logits l, l + 64, ...
 // `cs` is E doubles of LDS that belong to this wave.
 template <int BF16, int EPL>
@@ -182,7 +192,7 @@ __device__ void route_token(const RouteArgs& a, int64_t t, int lane, double* cs)
   }
   // k rounds: the best of what is left, the lowest index of equals
   uint32_t taken = 0u;
-  double w_mine = 0.0, total = 0.0;
+  double w_mine = 0.0;
   int id_mine = 0;
   for (int j = 0; j < a.k; ++j) {
     double best = -INFINITY, pb = 0.0;
@@ -211,12 +221,15 @@ __device__ void route_token(const RouteArgs& a, int64_t t, int lane, double* cs)
       id_mine = at;
       w_mine = pb;
     }
-    total += pb;
+  }
+  if (a.renorm) {
+    const double x = lane < a.k ? double(logit_at<BF16>(a.logits, t * E + id_mine)) : -INFINITY;
+    const double s = share(a.sigmoid, x, wave_max(x)), total = wave_sum(s);
+    w_mine = total == 0.0 ? 0.0 : s / total;
   }
   if (lane < a.k) {
     a.ids[t * a.k + lane] = id_mine;
-    const double w = a.renorm ? (total == 0.0 ? 0.0 : w_mine / total) : w_mine;
-    a.weights[t * a.k + lane] = float(w * double(a.scale));
+    a.weights[t * a.k + lane] = float(w_mine * double(a.scale));
   }
 }
 
@@ -368,6 +381,12 @@ __device__ __forceinline__ void merge8(double* v) {
 }
 
 constexpr double kNever = -1.7e308;  // key of an expert that has no score to be chosen by
+// Below kTiny a key has no room for the expert's number beside what orders it
+// (and sigmoid_near is 0 for scores that are not): such choices are settled by
+// the general path if a logit is kFar to 760 below (from 746 on scores are 0 in
+// 64 bits).  Below kSmall the chosen scores' sum is no divisor for what may be
+// left of a score.
+constexpr double kTiny = 1e-290, kSmall = 1e-250;
 
 // The general path as a call, so that its registers are not this path's.
 template <int BF16, int EPL>
@@ -456,7 +475,7 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
     c[i] = __builtin_fmin(__builtin_fmax(c[i], kNever), -kNever);
     if (o >= per) c[i] = -INFINITY;
   }
-  bool in = true, close = false;  // close: for the general path to settle
+  bool in = true, close = false, tiny = false;  // close: for the general path to settle
   if (G > 1) {
     double b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
@@ -474,6 +493,7 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
       }
     });
     const double worth = a.group_top == 2 ? b1 + b2 : b1;
+    tiny = fabs(worth) < kTiny;
     int before = 0;  // groups that come before this lane's
     for (int h = 1; h < G; ++h) {
       const int og = (g + h) & (G - 1);
@@ -532,7 +552,16 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
   const float x_next = __shfl_down(xm, 1);
   close |= l + 1 < a.k && next > kNever * 0.999 &&
                fabs(mine.d - next) <= (fabs(mine.d) + p + p_next) * 0x1p-38 && !(xm == x_next && bm == b_next);
-  close |= SIGMOID && on && xm < -kFar && xm > -760.f;  // a weight of what sigmoid_near leaves out
+  close |= a.renorm && on && xm != -INFINITY && total < kSmall;
+  tiny |= on && fabs(mine.d) < kTiny;
+  if (__ballot(tiny)) {
+    const float from = SIGMOID ? 0.f : float(top);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const float d = at(i) < per ? logit_at<BF16>(a.logits, row + g * per + at(i)) - from : 0.f;
+      close |= d < float(-kFar) && d > -760.f;
+    }
+  }
   if (last > kNever * 0.999) {
     const int from = (lane & ~(L - 1)) + a.k - 1;
     const double lim = last - (fabs(last) + (a.bias != nullptr ? 1.0 : 0.0)) * 0x1p-38;

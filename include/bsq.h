@@ -352,7 +352,9 @@ typedef enum bsq_score {
  *   bias    float32 [E] or NULL
  *   ids     int32 [T, k] (out);  weights float32 [T, k] (out)
  *   scores  float32 [T, E], all p (out), or NULL
- * A logit of -inf has score 0; a row of them has scores and weights 0.  NaN
+ * A logit of -inf has score 0; a row of them has scores and weights 0.
+ * Renormalised weights are those of the formula however small the chosen
+ * scores are (a bias may steer the choice to scores that round to 0).  NaN
  * and +inf give unspecified values, but ids are k different experts always.
  * Rules: E % groups == 0, 1 <= top_groups <= groups, k <= the experts of
  * top_groups groups, group_top <= E / groups (else SHAPE); E <= 1024,

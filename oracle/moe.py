@@ -54,8 +54,7 @@ def route(x, k, bias=None, groups=1, top_groups=1, group_top=1, sigmoid=False, r
         ids[t] = sorted(range(E), key=lambda e: (-left[e], e))[:k]
     w = np.take_along_axis(p, ids.astype(np.int64), 1)
     if renorm:
-        total = w.sum(1, keepdims=True)
-        w = np.where(total > 0, w / np.where(total > 0, total, 1.0), 0.0)
+        w = shares(np.take_along_axis(np.asarray(x, np.float64), ids.astype(np.int64), 1), True, sigmoid)
     return ids, w * scale, p
 
 

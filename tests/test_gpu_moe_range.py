@@ -117,3 +117,89 @@ def test_route_gradient_beside_masked_logits_and_ids_that_are_none(T, sigmoid):
     ids[1::5, 1] = E
     for ds in (None, (rng.standard_normal((T, E)) * 0.1).astype(np.float32)):
         _check_backward(x, False, ids, ds, sigmoid, seed=1)
+
+
+def _check_forward(x, bf16, k, bias=None, full=True, **kw):
+    torch = _torch()
+    dx, xv = _logits(x, bf16)
+    T, E = xv.shape
+    sigmoid = kw.pop("sigmoid", False)
+    ids, w = filled((T, k), torch.int32, -7), filled((T, k), torch.float32, float("nan"))
+    scores = filled((T, E), torch.float32, float("nan")) if full else None
+    bsq.bsq_moe_route(dx, ids, w, bias=None if bias is None else to_dev(np.asarray(bias, np.float32)), scores=scores,
+                      score=int(sigmoid), **kw)
+    rid, rw, rp = OE.route(xv, k, bias=None if bias is None else np.asarray(bias, np.float32), sigmoid=sigmoid, **kw)
+    assert np.array_equal(host(ids), rid), np.argwhere(host(ids) != rid)[:4].tolist()
+    half = 2.0 ** -24 * (1 + 2.0 ** -10)
+    _within(_values(w), rw, half * np.abs(rw) + LEAST * kw.get("scale", 1.0), "weights")
+    if full:
+        _within(_values(scores), rp, half * rp + LEAST, "scores")
+    return rid, rw
+
+
+FORWARD = [(256, 8, True, dict(groups=8, top_groups=4, group_top=2, scale=2.5)), (256, 8, False, {}),
+           (128, 6, False, dict(groups=4, top_groups=2)), (40, 5, False, dict(renorm=False)), (20, 1, False, {}),
+           (320, 8, False, {}), (60, 9, False, {}), (96, 4, False, dict(groups=3, top_groups=2))]
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k,bf16,opts", FORWARD)
+def test_route_is_rounded_once(T, sigmoid, E, k, bf16, opts):
+    """Scores and weights to half a step of 32 bits, also where a few logits
+    are far from the rest."""
+    say("route rounded once", T, sigmoid, E, k, bf16, opts)
+    rng = np.random.default_rng(E + k)
+    x = rng.standard_normal((T, E)) * 1.5
+    x[0::5, ::3] = -1e9
+    x[1::5, 0] = -3e38
+    x[2::5, :E // 2] -= 60.0
+    x[3::5, 1::2] -= 690.0
+    _check_forward(x, bf16, k, (rng.standard_normal(E) * 0.1).astype(np.float32), sigmoid=sigmoid, **opts)
+    _check_forward(x, bf16, k, sigmoid=sigmoid, **opts)
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("far", [90, 200, 690, 705, 720, 735, 760, 3000])
+@pytest.mark.parametrize("E,k,bf16,opts", FORWARD)
+def test_route_weights_of_chosen_scores_that_are_nothing(T, sigmoid, far, E, k, bf16, opts):
+    """A bias steers the choice to half of the experts, whose logits lie `far`
+    below the row's largest (softmax) or zero (sigmoid): p / sum is ordinary
+    where p itself is less than 64 bits hold."""
+    say("route weights far", T, sigmoid, far, E, k, bf16, opts)
+    rng = np.random.default_rng(E + far)
+    x = rng.standard_normal((T, E)) - far
+    bias = np.zeros(E, np.float32)
+    bias[E // 2:] = 4.0
+    if not sigmoid:
+        x[:, :E // 2] += far
+    rid, rw = _check_forward(x, bf16, k, bias, sigmoid=sigmoid, **opts)
+    assert np.all(rid >= E // 2)
+    if opts.get("renorm", True):
+        assert np.allclose(rw.sum(1), opts.get("scale", 1.0))
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,groups", [(24, 1), (256, 1), (256, 8), (300, 3), (512, 4)])
+@pytest.mark.parametrize("k", [4, 8, 12])
+def test_route_choice_between_scores_that_are_nearly_nothing(T, sigmoid, E, groups, k):
+    """Fewer ordinary logits than choices; the rest -inf (score 0), and some far
+    below (scores of 1e-295 and less, the least numbers of 64 bits among them),
+    which come before the -inf ones in the order of their size."""
+    say("route nearly nothing", T, sigmoid, E, groups, k)
+    rng = np.random.default_rng(E + groups)
+    x = np.full((T, E), -np.inf)
+    far = -(np.array([691.0, 693, 695, 697, 699, 701, 703, 705]) if sigmoid else
+            np.array([691.0, 703, 716, 730, 738, 740, 742, 744]))
+    for t in range(T):
+        at = rng.permutation(E)
+        x[t, at[:8]] = far[rng.permutation(8)]
+        if not sigmoid or t % 2:
+            x[t, at[8]] = 0.0
+        x[t, at[9:11]] = (-800.0, -1e9)
+    for g in (1, 2) if groups > 1 else (1,):
+        opts = dict(groups=groups, top_groups=max(1, groups // 2), group_top=g) if groups > 1 else {}
+        _check_forward(x, False, k, sigmoid=sigmoid, full=False, **opts)
+        _check_forward(x, False, k, np.zeros(E, np.float32), sigmoid=sigmoid, renorm=False, **opts)
