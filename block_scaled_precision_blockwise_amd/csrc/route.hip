@@ -139,7 +139,7 @@ __device__ void route_token(const RouteArgs& a, int64_t t, int lane, double* cs)
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       // a row of -inf alone has scores of zero
-      p[i] = top == -INFINITY ? 0.0 : exp(p[i] - top);
+      p[i] = p[i] == -INFINITY ? 0.0 : exp(p[i] - top);
       sum += p[i];
     }
     sum = wave_sum(sum);
@@ -225,7 +225,8 @@ __device__ void route_token(const RouteArgs& a, int64_t t, int lane, double* cs)
   if (a.renorm) {
     const double x = lane < a.k ? double(logit_at<BF16>(a.logits, t * E + id_mine)) : -INFINITY;
     const double s = share(a.sigmoid, x, wave_max(x)), total = wave_sum(s);
-    w_mine = total == 0.0 ? 0.0 : s / total;
+    // a row with NaN or +inf has softmax scores of NaN, also where none of them is chosen
+    w_mine = w_mine == w_mine ? (total == 0.0 ? 0.0 : s / total) : w_mine;
   }
   if (lane < a.k) {
     a.ids[t * a.k + lane] = id_mine;
@@ -418,6 +419,9 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
 #pragma unroll
   for (int q = 0; q < S / V; ++q)
     load4<BF16>(a.logits, row + g * per, at(q * V), per, whole, -INFINITY, x + 4 * q);
+  float largest = x[0];  // NaN if there is one
+#pragma unroll
+  for (int i = 1; i < S; ++i) largest = __builtin_elementwise_maximum(largest, x[i]);
   // ---- scores
   double c[S];
   double top = 0.0, inv = 0.0;
@@ -425,10 +429,7 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < S; ++i) c[i] = sigmoid_near(exp_near, double(x[i]));
   } else {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < S; ++i) m = fmaxf(m, x[i]);
-    top = lanes_max<L>(double(m));
+    top = lanes_max<L>(double(largest));
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -475,7 +476,9 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
     c[i] = __builtin_fmin(__builtin_fmax(c[i], kNever), -kNever);
     if (o >= per) c[i] = -INFINITY;
   }
-  bool in = true, close = false, tiny = false;  // close: for the general path to settle
+  bool in = true, tiny = false;
+  // for the general path to settle, which shows NaN where it is
+  bool close = SIGMOID ? largest != largest : !(largest < INFINITY);
   if (G > 1) {
     double b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
@@ -586,9 +589,11 @@ __global__ void __launch_bounds__(256) k_route_top(RouteArgs a) {
     const double v = a.renorm ? (total == 0.0 ? 0.0 : p / total) : p;
     a.weights[t_mine * a.k + l] = float(v * double(a.scale));
   }
-  if (again)
+  if (again) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the scores above, which it writes anew
     for (int r = 0; r < TPW; ++r)
       if ((again >> (L * r)) & whose) route_token_apart<BF16, kSlow>(a, t0 + r, lane, cs[w]);
+  }
 }
 
 // ------------------------------------------------------------- gradient --
@@ -645,7 +650,7 @@ __device__ void route_backward_token(const RouteBwdArgs& a, int64_t t, int lane,
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      p[i] = top == -INFINITY ? 0.f : expf(p[i] - top);
+      p[i] = p[i] == -INFINITY ? 0.f : expf(p[i] - top);
       sum += p[i];
     }
     sum = wave_sum(sum);
@@ -736,7 +741,7 @@ __global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      p[i] = top == -INFINITY ? 0.f : expf(p[i] - top);
+      p[i] = p[i] == -INFINITY ? 0.f : expf(p[i] - top);
       sum += p[i];
     }
     sum = row_sum(sum);

@@ -354,8 +354,10 @@ typedef enum bsq_score {
  *   scores  float32 [T, E], all p (out), or NULL
  * A logit of -inf has score 0; a row of them has scores and weights 0.
  * Renormalised weights are those of the formula however small the chosen
- * scores are (a bias may steer the choice to scores that round to 0).  NaN
- * and +inf give unspecified values, but ids are k different experts always.
+ * scores are (a bias may steer the choice to scores that round to 0).
+ * NaN shows: a softmax row with NaN or +inf has NaN scores and weights (and
+ * gradients), a sigmoid's NaN logit a NaN score, which is chosen last.  ids are
+ * k different experts always.
  * Rules: E % groups == 0, 1 <= top_groups <= groups, k <= the experts of
  * top_groups groups, group_top <= E / groups (else SHAPE); E <= 1024,
  * k <= 64, groups <= 64, group_top <= 2, T <= 2^31 - 1 (else UNSUPPORTED). */

@@ -203,3 +203,46 @@ def test_route_choice_between_scores_that_are_nearly_nothing(T, sigmoid, E, grou
         opts = dict(groups=groups, top_groups=max(1, groups // 2), group_top=g) if groups > 1 else {}
         _check_forward(x, False, k, sigmoid=sigmoid, full=False, **opts)
         _check_forward(x, False, k, np.zeros(E, np.float32), sigmoid=sigmoid, renorm=False, **opts)
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("E,groups,k", [(40, 1, 4), (40, 1, 9), (256, 8, 8), (256, 8, 12), (300, 1, 8), (24, 3, 3), (1000, 1, 2)])
+def test_route_shows_nan(T, E, groups, k):
+    """Softmax: a row with NaN or +inf has NaN scores, weights and gradients.
+    Sigmoid: a NaN logit has a NaN score and comes last; +inf has the score 1.
+    By whichever kernel; the rows beside them are as without."""
+    torch = _torch()
+    say("route NaN", T, E, groups, k)
+    rng = np.random.default_rng(E + k)
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    x[1::7, 3] = np.nan
+    x[2::7, 5] = np.inf
+    x[3::7, 1:] = -np.inf
+    x[3::7, 0] = np.nan
+    x[4::7] = np.nan
+    bad = np.zeros(T, bool)
+    for r in range(1, 5):
+        bad[r::7] = True
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    for sigmoid in (False, True):
+        ids, w, p = filled((T, k), torch.int32, -7), filled((T, k), torch.float32, 7.0), filled((T, E), torch.float32, 7.0)
+        kw = dict(groups=groups, top_groups=max(1, groups // 2)) if groups > 1 else {}
+        bsq.bsq_moe_route(to_dev(x), ids, w, scores=p, score=int(sigmoid), **kw)
+        dl = filled((T, E), torch.float32, 7.0)
+        bsq.bsq_moe_route_backward(to_dev(x), ids, to_dev(dw), dl, score=int(sigmoid))
+        i, w, p, dl = host(ids), host(w), host(p), host(dl)
+        assert i.min() >= 0 and i.max() < E and all(len(set(r)) == k for r in i.tolist())
+        if not sigmoid:
+            assert np.all(np.isnan(p[bad])) and np.all(np.isnan(w[bad])) and np.all(np.isnan(dl[bad]))
+            assert np.all(np.isfinite(p[~bad])) and np.all(np.isfinite(w[~bad])) and np.all(np.isfinite(dl[~bad]))
+            continue
+        assert np.array_equal(np.isnan(p), np.isnan(x)) and np.array_equal(np.isnan(dl), np.isnan(x) | (
+            np.isnan(np.take_along_axis(x, i.astype(np.int64), 1)).any(1)[:, None] & _asked(i, E)))
+        assert np.all(p[2::7, 5] == 1.0) and np.all(np.isfinite(w[1::7])) and np.all(np.isfinite(w[2::7]))
+        assert not np.any(i[1::7] == 3) and np.all(np.isnan(w[4::7]))
+
+
+def _asked(ids, E):
+    m = np.zeros((len(ids), E), bool)
+    np.put_along_axis(m, ids.astype(np.int64), True, 1)
+    return m
