@@ -97,13 +97,22 @@ __device__ __forceinline__ void load8(const void* base, int64_t elem, float (&x)
   }
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two values as bfloat16, to nearest even; NaN of any payload stays NaN
+// (encode_bf16 carries some of them into the sign).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
 // Stores 8 consecutive values (as f32, or as bf16 rounded to nearest even).
 template <int BF16>
 __device__ __forceinline__ void store8(void* p, int64_t elem, const float (&v)[8]) {
   if (BF16) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = encode_bf16(v[2 * i]) | (encode_bf16(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) u[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + elem) = make_uint4(u[0], u[1], u[2], u[3]);
   } else {
     float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + elem);
@@ -123,7 +132,6 @@ constexpr int kTile = 128;
 
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
@@ -187,7 +195,7 @@ __device__ __forceinline__ void store8nt(void* p, int64_t elem, const float (&v)
   if (BF16) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = encode_bf16(v[2 * i]) | (encode_bf16(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) u[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     stnt(static_cast<uint16_t*>(p) + elem, u[0], u[1], u[2], u[3]);
   } else {
 #pragma unroll

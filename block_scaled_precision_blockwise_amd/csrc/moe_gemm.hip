@@ -452,9 +452,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_moe_gemm(MoeArgs p) {
         const int64_t o = view.out0(t) + (int64_t(t.m0) + tr) * view.rows_b() + n;
         if (OUT_BF16) {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-          const uint32_t lo = encode_bf16(v[0]) | (encode_bf16(v[1]) << 16);
-          const uint32_t hi = encode_bf16(v[2]) | (encode_bf16(v[3]) << 16);
-          __builtin_nontemporal_store(u32x2{lo, hi}, reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + o));
+          __builtin_nontemporal_store(__builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4)),
+                                      reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + o));
         } else {
           __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(static_cast<float*>(p.out) + o));
         }

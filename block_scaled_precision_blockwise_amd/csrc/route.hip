@@ -692,7 +692,7 @@ __device__ void route_backward_token(const RouteBwdArgs& a, int64_t t, int lane,
     if (e < E) {
       const float dx = c[i] + (a.sigmoid ? dp[i] * p[i] * q[i] : p[i] * (dp[i] - dot));
       if (BF16)
-        static_cast<uint16_t*>(a.dlogits)[t * E + e] = uint16_t(encode_bf16(dx));
+        static_cast<uint16_t*>(a.dlogits)[t * E + e] = uint16_t(bf16_pair(dx, 0.f));
       else
         static_cast<float*>(a.dlogits)[t * E + e] = dx;
     }
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
       if (o < E) {
         if (BF16)
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + row + o) =
-              make_uint2(encode_bf16(dx[0]) | (encode_bf16(dx[1]) << 16), encode_bf16(dx[2]) | (encode_bf16(dx[3]) << 16));
+              make_uint2(bf16_pair(dx[0], dx[1]), bf16_pair(dx[2], dx[3]));
         else
           *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + row + o) =
               make_float4(dx[0], dx[1], dx[2], dx[3]);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(256) k_route_backward_rows(RouteBwdArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (o + i < E) {
-          if (BF16) static_cast<uint16_t*>(a.dlogits)[row + o + i] = uint16_t(encode_bf16(dx[i]));
+          if (BF16) static_cast<uint16_t*>(a.dlogits)[row + o + i] = uint16_t(bf16_pair(dx[i], 0.f));
           else static_cast<float*>(a.dlogits)[row + o + i] = dx[i];
         }
     }

@@ -334,7 +334,10 @@ bsq_status bsq_scaled_matmul_nvfp4(int64_t B, int64_t M, int64_t N, int64_t K, c
  * there is none.  What these index arrays hold is read on the device only:
  * numbers out of range are taken as "none" or cut to the arrays, and never
  * make an access out of range.  Codes are blocked by 32 with E8M0 scales, as
- * bsq_quant_mx writes them.  Every call gives the same bytes on every run. */
+ * bsq_quant_mx writes them of finite values; here infinities become the largest
+ * code of their block and NaN a NaN code (what else its block holds is
+ * unspecified), and NaN stays NaN in every float output that it goes into.
+ * Every call gives the same bytes on every run. */
 
 typedef enum bsq_score {
   BSQ_SOFTMAX = 0, /* p = softmax of a token's logits */

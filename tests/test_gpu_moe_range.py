@@ -246,3 +246,101 @@ def _asked(ids, E):
     m = np.zeros((len(ids), E), bool)
     np.put_along_axis(m, ids.astype(np.int64), True, 1)
     return m
+
+
+PAYLOADS = [0x7FC00000, 0x7FFFFFFF, 0xFFFFFFFF, 0xFFC00001, 0x7FFF8000]
+
+
+@pytest.mark.parametrize("bits", PAYLOADS)
+def test_nan_stays_nan_in_bfloat16(bits):
+    """A NaN of any payload, on its way to a bfloat16 output."""
+    torch = _torch()
+    say("NaN in bfloat16", hex(bits))
+    nan = np.array([bits], np.uint32).view(np.float32)
+    w = np.ones((5, 2), np.float32)
+    w[2, 1:] = nan
+    y = torch.randn(10, 64, device="cuda").bfloat16()
+    pos = torch.arange(10, dtype=torch.int32, device="cuda").view(5, 2)
+    out = torch.zeros(5, 64, dtype=torch.bfloat16, device="cuda")
+    bsq.bsq_moe_combine(y, pos, out, weights=to_dev(w))
+    want = np.zeros((5, 64), bool)
+    want[2] = True
+    assert np.array_equal(torch.isnan(out).cpu().numpy(), want)
+    for T in (5, MANY):
+        x = torch.randn(T, 16, device="cuda").bfloat16()
+        dw = np.ones((T, 2), np.float32)
+        dw[2, 1:] = nan
+        ids = torch.arange(2, dtype=torch.int32, device="cuda").repeat(T, 1)
+        dl = torch.zeros(T, 16, dtype=torch.bfloat16, device="cuda")
+        bsq.bsq_moe_route_backward(x, ids, to_dev(dw), dl, renorm=False)
+        assert torch.isnan(dl[2]).all() and not torch.isnan(dl[3:]).any() and not torch.isnan(dl[:2]).any()
+
+
+@pytest.mark.parametrize("e5m2", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("bits", PAYLOADS)
+def test_nan_stays_nan_in_codes_and_products(bits, bf16, e5m2):
+    """NaN in a token or in the gate's input is a NaN code (of both operands
+    and of the checkpoint), NaN in the product's row and in the gradient; blocks
+    and rows without one are as they were."""
+    torch = _torch()
+    say("NaN codes", hex(bits), bf16, e5m2)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    fp8 = torch.float8_e5m2 if e5m2 else torch.float8_e4m3fn
+    cd = bsq.BSQ_E5M2 if e5m2 else bsq.BSQ_E4M3
+    raw = np.array([bits >> 16], np.uint16).view(np.int16) if bf16 else np.array([bits], np.uint32).view(np.int32)
+    R, C = 128, 256
+    x = torch.randn(R, C, device="cuda").to(dt)
+
+    def put(t, r, c):
+        t.view(torch.int16 if bf16 else torch.int32)[r, c] = int(raw[0])
+
+    def codes(t, T, H, k=1, weights=None):
+        o = [filled(s, torch.uint8, 0x55) for s in ((T, H), (T, H // 32), (H, T), (H, T // 32))]
+        rows = torch.arange(T, dtype=torch.int32, device="cuda")
+        bsq.bsq_moe_gather_mx(t, rows, k, *o, weights=weights, code_dtype=cd)
+        return o
+
+    nan = lambda c: torch.isnan(c.view(fp8).float())  # noqa: E731
+    plain = codes(x, R, C)
+    put(x, 70, 100)
+    for weights in (None, torch.ones(R, 1, device="cuda")):
+        got = codes(x, R, C, weights=weights)
+        m = torch.zeros(R, C, dtype=torch.bool, device="cuda")
+        m[70, 100] = True
+        assert torch.equal(nan(got[0]), m) and torch.equal(nan(got[2]).t(), m)
+        m[70, 96:128] = True
+        assert torch.equal(got[0][~m], plain[0][~m])
+        m[70] = False
+        m[64:96, 100] = True
+        assert torch.equal(got[2].t()[~m], plain[2].t()[~m])
+    if not e5m2:
+        for out_dt in (torch.float32, torch.bfloat16):
+            b, sb = torch.full((1, 32, C), 0x38, dtype=torch.uint8, device="cuda"), filled((1, 32, C // 32), torch.uint8, 127)
+            out = torch.zeros(R, 32, dtype=out_dt, device="cuda")
+            bsq.bsq_moe_matmul(got[0], got[1], b, sb, torch.tensor([0, R], dtype=torch.int32, device="cuda"), out)
+            m = torch.zeros(R, 32, dtype=torch.bool, device="cuda")
+            m[70] = True
+            assert torch.equal(torch.isnan(out), m)
+    # the gate: g at (9, 5), u at (90, 40)
+    gu = torch.randn(R, C, device="cuda").to(dt)
+    put(gu, 9, 5)
+    put(gu, 90, 128 + 40)
+    u8 = lambda *s: filled(s, torch.uint8, 0x55)  # noqa: E731
+    h, hs, ht, hts, kept, ks = u8(R, 128), u8(R, 4), u8(128, R), u8(128, R // 32), u8(R, C), u8(R, C // 32)
+    bsq.bsq_swiglu_mx(gu, h, hs, ht, hts, kept, ks, code_dtype=cd)
+    m = torch.zeros(R, 128, dtype=torch.bool, device="cuda")
+    m[9, 5] = m[90, 40] = True
+    assert torch.equal(nan(h), m) and torch.equal(nan(ht).t(), m) and torch.equal(nan(kept), torch.isnan(gu))
+    h2, hs2 = u8(R, 128), u8(R, 4)
+    bsq.bsq_swiglu_mx(gu, h2, hs2, code_dtype=cd)
+    assert torch.equal(h2, h) and torch.equal(hs2, hs)
+    dh = torch.randn(R, 128, device="cuda").to(dt)
+    put(dh, 50, 7)
+    dgu = torch.zeros(R, C, dtype=dt, device="cuda")
+    bsq.bsq_swiglu_mx_backward(kept, ks, dh, dgu, code_dtype=cd)
+    m[50, 7] = True
+    bad = torch.isnan(dgu)
+    assert torch.equal(bad[:, :128], m)          # dg: from g, u or dh
+    m[90, 40] = False
+    assert torch.equal(bad[:, 128:], m)          # du: from g or dh
