@@ -48,7 +48,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int BK = 128;
-constexpr int64_t kCUs = 256;
 
 struct MoeArgs {
   const uint8_t *A, *B, *SA, *SB;
@@ -218,11 +217,6 @@ struct Deal {
   int total;
   uint32_t before, mine;
 };
-// Chunks that are mostly full, experts that fit the lanes.
-__host__ __device__ inline bool dealt(int per, int E) {
-  const int chunks = (per + 31) / 32;
-  return E <= 64 && 8 * per >= 7 * 32 * chunks;
-}
 template <int TM, int TN, int WGRAD>
 __device__ __forceinline__ Deal deal_tiles(const MoeArgs& p, int lane) {
   Deal d{0, 0, 0};
@@ -817,8 +811,6 @@ MoeArgs args_of(const MoeGemmLaunch& L) {
   return MoeArgs{L.A, L.B, L.SA, L.SB, L.out, L.offsets, L.rows, L.T, L.cap, L.E, int(L.N), int(L.K), L.k, 0};
 }
 
-int64_t up_to(int64_t v, int64_t m) { return (v + m - 1) / m; }
-
 }  // namespace
 
 bsq_status launch_moe_product(const MoeGemmLaunch& L, hipStream_t st) {
@@ -826,68 +818,26 @@ bsq_status launch_moe_product(const MoeGemmLaunch& L, hipStream_t st) {
   // a segment's last tile may be part full: at most one such tile for each
   // expert and for the rows past the last segment
   auto grid = [&](int tm, int tn) { return (L.cap / tm + L.E + 1) * up_to(L.N, tn); };
-  // rows that hold a choice, as far as the host knows, and per expert
-  const int64_t n = L.rows != nullptr && L.T < L.cap / L.k ? L.T * L.k : L.cap, rows = n / L.E;
-  // us at (rows per expert, experts, N, K), 256 x 256 tiles against the next:
-  // (256, 16, 2048, 2048) 32 / 41, (192, 64, 2048, 1024) 65 / 78; with fewer
-  // tiles than most CUs (255, 8, 1792, 1024) 18.5 / 12.1.  The big tiles
-  // address rows with 32 bits.
-  if (rows >= 160 && (n / 256 + L.E / 2) * up_to(L.N, 256) >= 160 && L.T * L.K < (int64_t(1) << 32))
-    return launch_big<0, 0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
-  // Few tiles leave CUs idle: the smallest tiles of which no CU gets two (half
-  // a part-full tile to an expert on average; rows that a plan's alignment
-  // leaves empty count, as their workgroups start too).  us so / with 64 x 128
-  // and two stages at (rows per expert, experts, N, K): 32 x 64 tiles (250, 4,
-  // 256, 4096) 13 / 26, 64 x 64 (256, 4, 512, 4096) 16 / 26, 64 x 128 (250, 4,
-  // 1536, 2048) 13 / 16; with more tiles than that, (325, 4, 1536, 2048), 64 x
-  // 64 takes 19, 64 x 128 with three stages 18, with two 17
-  auto few = [&](int tm, int tn) { return (L.cap / tm + (L.E + 1) / 2) * up_to(L.N, tn) <= kCUs; };
-  if (few(32, 64)) return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
-  if (rows >= 32) {
-    if (few(64, 64)) return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
-    if (few(64, 128)) return launch<2, 2, 2, 4, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
-    // 64 x 128 against 128 x 128: (255, 8, 1792, 1024) 12.1 / 14.8, (192, 64,
-    // 2048, 1024) 79 / 78; against 64 x 64: (37, 32, 2048, 1024, segments
-    // aligned to 128) 26 / 32
-    return launch<2, 2, 2, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
+  switch (product_tile(L.T, L.cap, L.E, L.N, L.K, L.k, L.rows != nullptr)) {
+    case MoeTile::t256x256: return launch_big<0, 0>(a, L.a_e5m2, L.out_bf16, grid(256, 256), st);
+    case MoeTile::t32x64: return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
+    case MoeTile::t64x64: return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
+    case MoeTile::t64x128s3: return launch<2, 2, 2, 4, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
+    default: return launch<2, 2, 2, 4, 2, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 128), st);
   }
-  // few rows, where the weights' bytes are most of the work: three stages
-  // against two (1, 32, 4096, 2048) 33 / 42; 32 rows against 64 (8, 32, 2048,
-  // 1024) 13.8 / 16.4, (25, 32, 4096, 2048) 74 / 70
-  if (rows > 16) return launch<2, 2, 2, 2, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(64, 64), st);
-  return launch<1, 4, 2, 1, 3, 0>(a, L.a_e5m2, L.out_bf16, grid(32, 64), st);
 }
 
 bsq_status launch_moe_wgrad(const MoeGemmLaunch& L, hipStream_t st) {
   const MoeArgs a = args_of(L);
-  // us with 256 x 256 tiles against 128 x 128 at (big tiles, rows per expert):
-  // (128, 512) 20 / 17, (64, 8192) 85 / 60
-  const int64_t big = up_to(L.N, 256) * up_to(L.K, 256) * L.E;
-  if (big >= 256 && L.cap * 256 < (int64_t(1) << 32)) {
-    // Where an XCD's chunk of 32 tiles (deal_tiles) reads more than its 4 MB of
-    // L2, one operand is better off leaving it first.  us so / kept, (N, K,
-    // experts, rows per expert): (2048, 2048, 16, 2048) 152 / 163, (2048, 2048,
-    // 8, 4096) 136 / 147, (4096, 2048, 8, 4096) 248 / 270, (2048, 4096, 8, 4096)
-    // 280 / 280, (2048, 1024, 16, 2048) 80 / 88; where it fits, (2048, 2048, 16,
-    // 1125) 100 / 93, and where tiles are dealt by eighths, (1280, 2048, 12,
-    // 2048) 117 / 107.  The products lose by it: 627 / 537.
-    const int64_t across = up_to(L.K, 256), cols = across < 32 ? across : 32, rows = up_to(32, cols);
-    if (dealt(int(big / L.E), L.E) && (rows + cols) * 256 * (L.cap / L.E) > (int64_t(4) << 20))
-      return launch_big<1, 1>(a, L.a_e5m2, L.out_bf16, big, st);
-    return launch_big<1, 0>(a, L.a_e5m2, L.out_bf16, big, st);
-  }
-  // Few tiles leave CUs idle: the smallest tiles of which no CU gets two.  us
-  // with 64 x 64 / 64 x 128 / 128 x 128 at (N, K, experts, rows per expert):
-  // (512, 512, 4, 8192) 25 / 33 / 44, (1024, 512, 4, 8192) 45 / 36 / 44, (1024,
-  // 768, 4, 4096) 48 / 43 / 34, (640, 640, 8, 4096) 64 / 46 / 36
   auto tiles = [&](int tn, int tk) { return up_to(L.N, tn) * up_to(L.K, tk) * L.E; };
-  if (tiles(64, 64) <= kCUs) return launch<2, 2, 2, 2, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(64, 64), st);
-  if (tiles(64, 128) <= kCUs) return launch<2, 2, 2, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(64, 128), st);
-  // a workgroup to a CU: three stages for it; more: two, so that two fit.  us
-  // with three / two at (tiles, rows per expert): (256, 2048) 27 / 33, (256,
-  // 8192) 48 / 60, (512, 512) 21 / 17
-  if (tiles(128, 128) <= kCUs) return launch<2, 2, 4, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(128, 128), st);
-  return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, tiles(128, 128), st);
+  switch (wgrad_tile(L.cap, L.E, L.N, L.K)) {
+    case MoeTile::t256x256_stream: return launch_big<1, 1>(a, L.a_e5m2, L.out_bf16, tiles(256, 256), st);
+    case MoeTile::t256x256: return launch_big<1, 0>(a, L.a_e5m2, L.out_bf16, tiles(256, 256), st);
+    case MoeTile::t64x64: return launch<2, 2, 2, 2, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(64, 64), st);
+    case MoeTile::t64x128s3: return launch<2, 2, 2, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(64, 128), st);
+    case MoeTile::t128x128s3: return launch<2, 2, 4, 4, 3, 1>(a, L.a_e5m2, L.out_bf16, tiles(128, 128), st);
+    default: return launch<2, 2, 4, 4, 2, 1>(a, L.a_e5m2, L.out_bf16, tiles(128, 128), st);
+  }
 }
 
 }  // namespace bsq

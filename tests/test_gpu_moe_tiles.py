@@ -84,3 +84,111 @@ def test_wgrad_keeps_inside_its_arrays(E, cap, N, K):
     got = whole[1:-1].clone()
     bsq.bsq_moe_wgrad(dy, sd, x, sx, to_dev(off // 128 * 128), whole[1:-1])
     assert torch.equal(got.view(torch.int16), whole[1:-1].contiguous().view(torch.int16)) and torch.any(got != 0)
+
+
+# ------------------------------------------------ every tile, type and length --
+
+def _wide(codes, scales, fp8):
+    """float64 values of codes with a scale to each 32 along the last axis."""
+    torch = _torch()
+    v = codes.view(fp8).double().view(*scales.shape, 32)
+    return (v * torch.exp2(scales.double() - 127.0)[..., None]).view(codes.shape)
+
+
+def _close(got, a, b, bf16, what):
+    """got [m, n] against a [m, k] b [n, k]^T in 64 bits: 1e-4 of the sum of
+    |products|, what the matrix core cuts off a group of 8, a rounding to bfloat16."""
+    torch = _torch()
+
+    def groups(v):
+        return v.abs().view(*v.shape[:-1], v.shape[-1] // 8, 8).amax(-1)
+
+    want = a @ b.t()
+    bound = 1e-4 * (a.abs() @ b.abs().t()) + 2.0 ** -9 * (groups(a) @ groups(b).t()) + 1e-37
+    if bf16:
+        bound += 2.0 ** -8 * want.abs()
+    off = (got.double() - want).abs()
+    assert torch.isfinite(got).all(), what
+    bad = (off > bound).nonzero()
+    assert len(bad) == 0, f"{what}: {len(bad)} of {got.numel()} outside; first {bad[0].tolist()}"
+
+
+def _random_codes(g, shape, fp8):
+    """Codes of normal values of unlike size, a block exponent to each 32."""
+    torch = _torch()
+    top = 448.0 if fp8 == torch.float8_e4m3fn else 57344.0
+    c = (torch.randn(shape, generator=g, device="cuda") * (top / 6)).clamp(-top, top).to(fp8).view(torch.uint8)
+    e = torch.randint(112, 122, (*shape[:-1], shape[-1] // 32), generator=g, device="cuda", dtype=torch.int32)
+    return c, e.to(torch.uint8)
+
+
+# lengths, N, by the tile that they take with any K of these tests
+PRODUCT_TILES = {
+    "t32x64": ([3, 0, 33, 1], 144), "t64x64": ([300, 0, 500, 3], 784), "t64x128s3": ([300, 0, 500, 3], 1296),
+    "t64x128": ([300, 0, 500, 3], 2576), "t256x256": ([700, 0, 1301], 9232)}
+TYPES = [(False, False), (False, True), (True, False), (True, True)]  # A in e5m2, output in bfloat16
+
+
+@pytest.mark.parametrize("steps", range(1, 10))
+@pytest.mark.parametrize("tile", PRODUCT_TILES)
+def test_matmul_of_each_tile_type_and_length(tile, steps):
+    torch = _torch()
+    lengths, N = PRODUCT_TILES[tile]
+    K, E, k = 128 * steps, len(lengths), 2
+    cap = sum(lengths) + 5
+    T = cap  # more choices than rows: all rows may hold one
+    g = torch.Generator(device="cuda").manual_seed(steps)
+    off = torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+    rows = torch.randint(-T // 4, T * k, (cap,), generator=g, device="cuda").clamp(min=-1).to(torch.int32)
+    b, sb = _random_codes(g, (E, N, K), torch.float8_e4m3fn)
+    bv = _wide(b, sb, torch.float8_e4m3fn)
+    for e5m2, bf16 in TYPES:
+        say("matmul of tile", tile, K, e5m2, bf16)
+        fp8 = torch.float8_e5m2 if e5m2 else torch.float8_e4m3fn
+        a, sa = _random_codes(g, (T, K), fp8)
+        av = _wide(a, sa, fp8)
+        outs = [filled((cap, N), torch.bfloat16 if bf16 else torch.float32, float("nan")) for _ in range(2)]
+        for out in outs:
+            bsq.bsq_moe_matmul(a, sa, b, sb, off, out, rows=rows, k=k,
+                               a_dtype=bsq.BSQ_E5M2 if e5m2 else bsq.BSQ_E4M3)
+        src = torch.where((rows >= 0)[:, None], av[(rows.clamp(min=0) // k).long()], 0.0)
+        at = 0
+        for e, n in enumerate(lengths):
+            _close(outs[0][at:at + n], src[at:at + n], bv[e], bf16, f"expert {e}")
+            at += n
+        assert torch.all(outs[0][at:] == 0)
+        assert torch.equal(outs[0].view(torch.uint8), outs[1].view(torch.uint8)), "two runs differ"
+
+
+# blocks of 128 rows of the experts' segments, blocks of cap, N, K
+WGRAD_TILES = {
+    "t64x64": ([9, 7, 0, 1, 3], 21, 400, 272), "t64x128s3": ([5, 0, 6, 8, 2, 4, 1, 9], 36, 400, 400),
+    "t128x128s3": ([5, 0, 6, 8, 2, 4, 1, 9], 35, 656, 528), "t128x128": ([5, 0, 6, 8, 2, 4, 1, 9], 35, 784, 784),
+    "t256x256": ([9, 7, 6, 8, 0, 4, 1, 3], 40, 1296, 2032), "t256x256 dealt": ([9, 5, 4, 3, 8], 40, 2032, 2000),
+    "t256x256_stream": ([9, 7, 20, 0, 2], 64, 2032, 2000), "t256x256_stream one": ([1, 3, 6, 8], 56, 2048, 1936)}
+
+
+@pytest.mark.parametrize("e5m2,bf16", TYPES)
+@pytest.mark.parametrize("tile", WGRAD_TILES)
+def test_wgrad_of_each_tile_type_and_length(tile, e5m2, bf16):
+    torch = _torch()
+    blocks, all_blocks, N, K = WGRAD_TILES[tile]
+    E, cap = len(blocks), 128 * all_blocks
+    say("wgrad of tile", tile, E, cap, N, K, e5m2, bf16)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    fp8 = torch.float8_e5m2 if e5m2 else torch.float8_e4m3fn
+    dy, sd = _random_codes(g, (N, cap), fp8)
+    x, sx = _random_codes(g, (K, cap), torch.float8_e4m3fn)
+    off = (torch.tensor([0] + blocks, device="cuda").cumsum(0) * 128).to(torch.int32)
+    outs = [filled((E, N, K), torch.bfloat16 if bf16 else torch.float32, float("nan")) for _ in range(2)]
+    for out in outs:
+        bsq.bsq_moe_wgrad(dy, sd, x, sx, off, out, dyt_dtype=bsq.BSQ_E5M2 if e5m2 else bsq.BSQ_E4M3)
+    dv, xv = _wide(dy, sd, fp8), _wide(x, sx, torch.float8_e4m3fn)
+    at = 0
+    for e, n in enumerate(blocks):
+        if n:
+            _close(outs[0][e], dv[:, at:at + 128 * n].contiguous(), xv[:, at:at + 128 * n].contiguous(), bf16, f"expert {e}")
+        else:
+            assert torch.all(outs[0][e] == 0)
+        at += 128 * n
+    assert torch.equal(outs[0].view(torch.uint8), outs[1].view(torch.uint8)), "two runs differ"

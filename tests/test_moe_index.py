@@ -181,3 +181,35 @@ def test_launches_are_cut_below_the_threads_that_one_has(tmp_path):
         int calls = 0;
         EXPECT(in_parts(100, 10, [&](int64_t, int64_t) { return ++calls == 3 ? 7 : 0; }) == 7 && calls == 3, "status");
     """)
+
+
+def test_the_gpu_tests_reach_every_tile(tmp_path):
+    """The sizes of tests/test_gpu_moe_tiles.py take the tiles that they are
+    named for, and these are all that a product or a weight gradient can take."""
+    import test_gpu_moe_tiles as G
+
+    lines, seen = [], (set(), set())
+    for name, (lengths, N) in G.PRODUCT_TILES.items():
+        cap, seen_in = sum(lengths) + 5, seen[0]
+        seen_in.add(name)
+        for steps in range(1, 10):
+            lines.append(f"EXPECT(product_tile({cap}, {cap}, {len(lengths)}, {N}, {128 * steps}, 2, true) == MoeTile::{name}, "
+                         f"\"{name} {steps}\");")
+    for name, (blocks, all_blocks, N, K) in G.WGRAD_TILES.items():
+        assert sum(blocks) <= all_blocks
+        tile, *kind = name.split()
+        seen[1].add(tile)
+        big = -(-N // 256) * -(-K // 256)
+        lines.append(f"EXPECT(wgrad_tile({128 * all_blocks}, {len(blocks)}, {N}, {K}) == MoeTile::{tile}, \"{name}\");")
+        if tile.startswith("t256"):
+            want = "false" if not kind and tile == "t256x256" else "true"
+            lines.append(f"EXPECT(dealt({big}, {len(blocks)}) == {want}, \"{name}\");")
+            if kind != ["one"] and kind != ["dealt"]:
+                assert big * len(blocks) > 256  # workgroups that go through more than one tile
+    assert seen[0] == {"t32x64", "t64x64", "t64x128s3", "t64x128", "t256x256"}
+    assert seen[1] == {"t64x64", "t64x128s3", "t128x128s3", "t128x128", "t256x256", "t256x256_stream"}
+    wild = [p.values for p in G.WILD]
+    for (E, cap, N, K), name in zip(wild, ("t32x64", "t64x64", "t64x128s3", "t64x128", "t64x64", "t256x256", "t32x64")):
+        lines.append(f"EXPECT(product_tile({cap}, {cap}, {E}, {N}, {K}, 2, true) == MoeTile::{name}, \"wild {N}\");")
+        lines.append(f"EXPECT(product_tile({cap}, {cap}, {E}, {N}, {K}, 1, false) == MoeTile::{name}, \"wild {N}\");")
+    _run(tmp_path, "\n".join(lines))
