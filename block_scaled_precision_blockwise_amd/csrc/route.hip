@@ -249,13 +249,18 @@ __global__ void __launch_bounds__(256) k_route(RouteArgs a) {
 // and breaks ties by the lowest index; every lane sorts its keys and keeps
 // 8, and log2(L) exchanges merge the lists (the larger of A[i] and B[7 - i]
 // are the 8 largest of two sorted lists).  Scores that are closer than the
-// lost bits and this path's own exponential (2^-42) allow are told apart by
-// the general path above, unless their logits and biases are the same.
+// lost bits and this path's own exponential allow are told apart by the general
+// path above, unless their logits and biases are the same.  A score is off by
+// at most 2^-40.5 of itself (the exponential's 2^-41.5, and as much by the sum),
+// a key by 2^-42 more of its value c, so the difference of two by less than
+// (p + p' + |c|) 2^-40; what lies within (p + p' + |c|) 2^-38 is settled there,
+// and groups within (|worth| + 2) 2^-38, four scores of at most 1 each.
 constexpr int kTop = 8;
 
-// e^x to a relative 2^-42 for x <= 0 or so: x = n ln 2 + r (ln 2 in two
+// e^x to a relative 2^-41.5 for x <= 0 or so: x = n ln 2 + r (ln 2 in two
 // pieces, the first of 36 bits, so that n times it is exact), the power series of
-// e^r to r^10 (|r| <= ln 2 / 2: the next term is below 2.3e-13).
+// e^r to r^10 (|r| <= ln 2 / 2: what it leaves out is below 2.2e-13, at r = -ln 2
+// / 2 1.31 2^-42 of e^r).
 struct ExpSeries {
   double c[8];  // 1 / 10!, ..., 1 / 3!
   __device__ ExpSeries()

@@ -14,7 +14,7 @@ namespace {
 // ------------------------------------------------------------------- plan --
 // A stable counting sort.  Workgroup b owns a contiguous run of choices; the
 // row of a choice is its expert's first row, plus the expert's choices in
-// earlier workgroups, plus those before it in its own.  Up to kPlanOne
+// earlier workgroups, plus those before it in its own.  Up to kPlanChunk
 // choices one workgroup does it all; beyond, a first launch leaves each
 // workgroup's counts in `space` and every workgroup of the second sums them
 // itself (nothing waits for another workgroup).  No atomic orders anything:
