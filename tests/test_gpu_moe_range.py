@@ -344,3 +344,40 @@ def test_nan_stays_nan_in_codes_and_products(bits, bf16, e5m2):
     assert torch.equal(bad[:, :128], m)          # dg: from g, u or dh
     m[90, 40] = False
     assert torch.equal(bad[:, 128:], m)          # du: from g or dh
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("E", [60, 100, 250, 500, 1000])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_by_every_kernel(T, E, bf16, sigmoid):
+    """Widths up to 64, 128, 256, 512 and 1024, few tokens and many, few
+    choices (up to 8) and more (past 16 in the gradient)."""
+    say("route every kernel", T, E, bf16, sigmoid)
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((T, E)) * 1.5
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    ds = (rng.standard_normal((T, E)) * 0.1).astype(np.float32)
+    for k in (5, 12, 17):
+        ids, _ = _check_forward(x, bf16, k, bias, full=k != 12, sigmoid=sigmoid, scale=2.5)
+        _check_backward(x, bf16, ids, ds if k != 12 else None, sigmoid, seed=k)
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,groups,k", [(16, 4, 3), (64, 8, 8), (256, 8, 8), (256, 16, 4), (24, 3, 5), (64, 8, 12)])
+def test_route_of_groups_whose_experts_a_bias_rules_out(T, sigmoid, E, groups, k):
+    """A group's worth is the sum of its two largest: -inf with fewer than two
+    experts left, equal to that of a group with none, so the lowest index."""
+    say("route groups ruled out", T, sigmoid, E, groups, k)
+    rng = np.random.default_rng(E + k)
+    x = rng.standard_normal((T, E)) * 1.5
+    per = E // groups
+    for left in range(3):  # experts left in each group but the last
+        bias = np.full(E, -np.inf, np.float32)
+        bias[(groups - 1) * per:] = 0.0
+        for g in range(1, groups - 1):
+            bias[g * per + rng.permutation(per)[:left]] = 0.25
+        for top in sorted({1, 2, groups // 2, groups - 1}):
+            if k <= top * per:
+                _check_forward(x, False, k, bias, sigmoid=sigmoid, groups=groups, top_groups=top, group_top=2)

@@ -192,3 +192,17 @@ def test_wgrad_of_each_tile_type_and_length(tile, e5m2, bf16):
             assert torch.all(outs[0][e] == 0)
         at += 128 * n
     assert torch.equal(outs[0].view(torch.uint8), outs[1].view(torch.uint8)), "two runs differ"
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_big_tiles_without_tokens_or_contraction_write_zeros(bf16):
+    torch = _torch()
+    E, N = 3, 9232
+    off = torch.tensor([0, 700, 700, 2001], dtype=torch.int32, device="cuda")
+    out = filled((2006, N), torch.bfloat16 if bf16 else torch.float32, float("nan"))
+    u8 = lambda *s: filled(s, torch.uint8, 0x7F)  # noqa: E731
+    for T, K in ((0, 128), (2006, 0)):
+        say("big tiles empty", T, K, bf16)
+        out.fill_(float("nan"))
+        bsq.bsq_moe_matmul(u8(T, K), u8(T, K // 32), u8(E, N, K), u8(E, N, K // 32), off, out)
+        assert torch.all(out == 0)
