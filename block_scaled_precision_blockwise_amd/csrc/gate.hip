@@ -4,8 +4,8 @@
 // gradient's operand), and g and u themselves in 8 bits, from which the
 // backward pass takes its gradient instead of from 16-bit copies.
 //
-// A stream: 32768 x 2048 reads 268 MB and writes 277 (forward, 110 us) and
-// reads 272 and writes 268 (backward, 84 us); the two calls take 199 us, 5.4
+// A stream: 32768 x 2048 reads 268 MB and writes 277 (forward, 114 us) and
+// reads 272 and writes 268 (backward, 84 us); the two calls take 198 us, 5.4
 // TB/s, the rate of a large copy.  What it took: g and u as pairs of 16 bits
 // to the conversion that scales, tiles of 128 columns so that codes are
 // written in whole lines both ways, non-temporal stores, and a sigmoid of 10

@@ -25,14 +25,16 @@
 // stay under way.  The MFMA's first operand is the B fragment, so that a
 // lane's four results are four neighbours of one output row.
 //
-// Measured (MI355X): 65536 rows over 32 experts, N 4096, K 2048: 539 us, 2.04
+// Measured (MI355X): 65536 rows over 32 experts, N 4096, K 2048: 545 us, 2.02
 // PFLOP/s; the weight gradients of 32768 rows over 16 experts, N = K = 2048:
-// 152 us, 1.81 PFLOP/s.  A big tile's 16 steps take 45 k cycles, 2800 a step
-// where its 256 MFMAs take 2048; with every load a hit in the L2 2700, without
-// loads 2500; the rest of a tile (search, first loads, output) 10 k.  The
-// clock is held to 1.9 - 2.0 GHz by power: pure MFMAs on such operands run at
-// 16 - 19 ns per 16 x 16 x 128, not the 13.3 of 2.4 GHz.  8 tokens over 32
-// experts (N 4096, K 2048): 33 us, 5.3 TB/s of weights.
+// 148 us, 1.86 PFLOP/s; 65536 own rows in e5m2, N 2048, K 4096: 535 us.  A big
+// tile's 16 steps take 47 k cycles, 2950 a step where its 256 MFMAs take 2048
+// (with every load a hit in the L2 2700, without loads 2500); the rest of a
+// tile 10.6 k: search 1.4, addresses 1.0, waits 0.4, output with the next
+// tile's first loads 7.8.  The clock is at 1.8 GHz meanwhile (cycles over time);
+// pure MFMAs on such operands run at 16 - 19 ns per 16 x 16 x 128, not the 13.3
+// of 2.4 GHz.  8 tokens over 32 experts (N 4096, K 2048): 30 - 34 us, 5.1 - 5.8
+// TB/s of weights.
 #include "moe.h"
 #include "moe_index.h"
 

@@ -350,7 +350,8 @@ typedef enum bsq_score {
  * the largest c are chosen, largest first, the lowest index of equals.
  * Their weights are p (without the bias), divided by their sum if renorm is
  * not 0, times scale.
- * The choice is the one that scores in 64 bits give.
+ * The choice is the one that scores in 64 bits give; scores and weights are
+ * good to 2^-38 before their one rounding to float32.
  *   logits  [T, E] of logits_dtype (BSQ_F32 or BSQ_BF16)
  *   bias    float32 [E] or NULL
  *   ids     int32 [T, k] (out);  weights float32 [T, k] (out)
@@ -462,6 +463,7 @@ bsq_status bsq_moe_wgrad(int64_t cap, int64_t E, int64_t N, int64_t K, const uin
  *   kept [R, 2 F] codes, kept_scales [R, 2 F / 32]: gu itself in 8 bits, the
  *        checkpoint that the backward pass reads, or both NULL
  * code_dtype (E4M3 or E5M2) is that of all codes.
+ * Float32 arithmetic, 1 / (1 + e^-g) within 4 steps of 2^-23.
  * bsq_swiglu_mx_backward, from the checkpoint's values of g and u, with
  * s = 1 / (1 + e^-g): dgu = [dh u s (1 + g (1 - s)) | dh g s], dh [R, F] and
  * dgu [R, 2 F] of dh_dtype.
