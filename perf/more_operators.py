@@ -214,7 +214,8 @@ def _quantize4(x, factor):
         E = _exponent(b.abs().amax(-1), 6.0)
         return _e2m1((b * _power(-E)[..., None]).view(x.shape)), (E + 127).to(torch.uint8).view(E8M0)
     b = (x.float() * factor).reshape(*x.shape[:-1], -1, 16)
-    scale = (b.abs().amax(-1) / 6.0).clamp(2.0 ** -9, 448.0).to(E4M3)
+    # a sixth in 64 bits: torch divides by a number through its reciprocal
+    scale = (b.abs().amax(-1).double() / 6.0).float().clamp(2.0 ** -9, 448.0).to(E4M3)
     return _e2m1((b / scale.float()[..., None]).view(x.shape)), scale
 
 
