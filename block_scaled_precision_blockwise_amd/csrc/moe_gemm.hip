@@ -35,19 +35,15 @@
 // pure MFMAs on such operands run at 16 - 19 ns per 16 x 16 x 128, not the 13.3
 // of 2.4 GHz.  8 tokens over 32 experts (N 4096, K 2048): 30 - 34 us, 5.1 - 5.8
 // TB/s of weights.
+#include "lds.h"
 #include "moe.h"
-#include "moe_index.h"
+#include "tiles.h"
 
 #include <type_traits>
 
 namespace bsq {
 
 namespace {
-
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int BK = 128;
 
@@ -59,133 +55,6 @@ struct MoeArgs {
   int E, N, K, k;
   int first;  // workgroup of this launch (k_moe_gemm)
 };
-
-// Buffer resource of `records` bytes (in range 0 .. 2^32 - 1) from `base`;
-// reads past it give zeros.
-__device__ __forceinline__ i32x4 rsrc(const uint8_t* base, int64_t records) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint32_t n = uint32_t(records < 0 ? 0 : (records > int64_t(0xFFFFFFFF) ? int64_t(0xFFFFFFFF) : records));
-  return i32x4{__builtin_amdgcn_readfirstlane(int(uint32_t(b))),
-               __builtin_amdgcn_readfirstlane(int(uint32_t(b >> 32) & 0xFFFFu)),
-               __builtin_amdgcn_readfirstlane(int(n)), 0x00020000};
-}
-
-// A value that is the same in every lane, in a scalar register.
-__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t scalar(int64_t v) {
-  return int64_t(uint64_t(uint32_t(scalar(int(v)))) | (uint64_t(uint32_t(scalar(int(v >> 32)))) << 32));
-}
-__device__ __forceinline__ const uint8_t* scalar(const uint8_t* v) {
-  return reinterpret_cast<const uint8_t*>(scalar(reinterpret_cast<int64_t>(v)));
-}
-
-// 16 bytes per lane straight into LDS: lane i fills [lds + 16 i, + 16).  In
-// inline asm, so that the compiler does not order it against the reads of
-// the other stage; the caller waits with vmcnt before the barrier that
-// publishes the stage.  No register is written.  The compiler does not know
-// what these are, so the waits that the hardware leaves to software are in
-// them: one state from m0 to its use, five from a descriptor that a vector
-// instruction may have written.
-__device__ __forceinline__ void dma16(const uint8_t* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "memory");
-}
-__device__ __forceinline__ void dma16(i32x4 r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(scalar(int(lds))), "v"(voff), "s"(r)
-               : "memory");
-}
-// 4 bytes per lane: lane i fills [lds + 4 i, + 4).
-__device__ __forceinline__ void dma4(i32x4 r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :
-               : "s"(scalar(int(lds))), "v"(voff), "s"(r)
-               : "memory");
-}
-// From a 32-bit offset to a base in scalar registers, to `at` (a constant
-// where it is inlined) past lds.
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds, int at) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"(lds), "v"(off), "s"(base), "i"(at)
-               : "memory", "scc");
-}
-
-// The same, to be dropped from the L2 first.
-__device__ __forceinline__ void dma16_stream(const uint8_t* base, uint32_t off, uint32_t lds, int at) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
-               :
-               : "s"(lds), "v"(off), "s"(base), "i"(at)
-               : "memory", "scc");
-}
-
-// s_waitcnt's operand: at most n vector memory operations under way.
-constexpr int vmcnt(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
-// A barrier that no access of the compiler's moves across.
-__device__ __forceinline__ void barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t lds_of(const uint8_t* p) {
-  return __builtin_amdgcn_readfirstlane(
-      uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)(p))));
-}
-
-__device__ __forceinline__ v8i frag(const uint8_t* tile, int off0, int off1) {
-  const uint4 lo = *reinterpret_cast<const uint4*>(tile + off0);
-  const uint4 hi = *reinterpret_cast<const uint4*>(tile + off1);
-  return v8i{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
-}
-
-// The tiles of all segments (`total`), and the segment of the mt-th.  Every
-// wave computes it alone: lane l sums the tiles of its share of the segments,
-// a scan over the lanes finds the lane, and that lane's segments are walked.
-template <int TM>
-__device__ __forceinline__ Segments<TM> segments(const MoeArgs& a) {
-  return Segments<TM>{a.offsets, a.E, a.cap};
-}
-template <int TM>
-__device__ __forceinline__ int tiles_total(const MoeArgs& a, int lane, uint32_t& mine_before, uint32_t& mine) {
-  mine = segments<TM>(a).lane_tiles(lane);
-  uint32_t s = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(s, d);
-    if (lane >= d) s += o;
-  }
-  mine_before = s - mine;
-  const uint32_t total = uint32_t(__builtin_amdgcn_readlane(int(s), 63)), limit = uint32_t(segments<TM>(a).limit());
-  return scalar(int(total < limit ? total : limit));
-}
-template <int TM>
-__device__ __forceinline__ Segment find_tile(const MoeArgs& a, int mt, uint32_t mine_before, uint32_t mine) {
-  const uint64_t here = __ballot(Segments<TM>::has(mine_before, mine, mt));
-  const int l = here ? __ffsll((unsigned long long)here) - 1 : 63;
-  Segment s = segments<TM>(a).at(l, mt - __builtin_amdgcn_readlane(int(mine_before), l));
-  s.e = __builtin_amdgcn_readfirstlane(s.e);
-  s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
-  s.end = __builtin_amdgcn_readfirstlane(s.end);
-  return s;
-}
-
-// Tile order: workgroups are dealt to the 8 XCDs round-robin by linear id,
-// and each XCD has its own L2, so XCD x takes the x-th contiguous eighth of
-// an order that walks bands of kBand tile rows column by column.  65536 rows
-// over 32 experts, N 4096, K 2048: bands of 2, 4, 6, 8, 16 rows 662, 628, 610,
-// 649, 673 us with an earlier output, of 4, 5, 6 rows 543, 531, 533 us with the
-// present one; bands that end with the segments are no faster.
-__device__ __forceinline__ void tile_order(int L, int tiles_m, int tiles_n, int& tm, int& tn) {
-  constexpr int kBand = 5;
-  const int T = tiles_m * tiles_n, per = T / 8;
-  const int t = L < 8 * per ? (L % 8) * per + L / 8 : L;
-  const int band = t / (kBand * tiles_n);
-  const int rows = min(kBand, tiles_m - band * kBand);
-  const int in = t - band * kBand * tiles_n;
-  tm = band * kBand + in % rows;
-  tn = in / rows;
-}
 
 // What a workgroup computes: output rows [m0, m_end) and columns from n0 of
 // expert e, over nk steps of the contraction from byte k0 on.
@@ -223,7 +92,7 @@ template <int TM, int TN, int WGRAD>
 __device__ __forceinline__ Deal deal_tiles(const MoeArgs& p, int lane) {
   Deal d{0, 0, 0};
   if (!WGRAD) {
-    d.total = tiles_total<TM>(p, lane, d.before, d.mine);
+    d.total = tiles_total(Segments<TM>{p.offsets, p.E, p.cap}, lane, d.before, d.mine);
     return d;
   }
   // 16 experts of 2048 x 2048 over 32768 rows, segments of 0.5 to 2 times the
@@ -274,7 +143,7 @@ __device__ __forceinline__ bool find_place(const MoeArgs& p, int lane, const Dea
     if (unsigned(L) >= unsigned(d.total) * unsigned(tiles_n)) return false;
     int tm, tn;
     tile_order(L, d.total, tiles_n, tm, tn);
-    const Segment s = find_tile<TM>(p, tm, d.before, d.mine);
+    const Segment s = find_tile(Segments<TM>{p.offsets, p.E, p.cap}, tm, d.before, d.mine);
     t.e = s.e < p.E ? s.e : 0;
     t.m0 = s.row0;
     t.m_end = s.end;
