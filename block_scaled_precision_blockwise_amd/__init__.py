@@ -23,7 +23,7 @@ import os
 from typing import Optional
 
 __all__ = [
-    "BSQ_F32", "BSQ_BF16", "BSQ_E4M3", "BSQ_E5M2", "BSQ_E8M0", "BSQ_I8", "BSQ_I32",
+    "BSQ_F32", "BSQ_BF16", "BSQ_E4M3", "BSQ_E5M2", "BSQ_E8M0", "BSQ_I8", "BSQ_I32", "BSQ_E2M1",
     "lib", "lib_path", "is_built",
     "bsq_version", "bsq_device_check", "bsq_time_next_gemm",
     "bsq_quant_fp8_rowblock", "bsq_quant_fp8_tile", "bsq_quant_mx",
@@ -38,11 +38,13 @@ __all__ = [
     "bsq_moe_capacity", "bsq_moe_plan_workspace_bytes", "bsq_moe_plan", "bsq_moe_gather_mx",
     "bsq_moe_combine", "bsq_moe_combine_backward", "bsq_moe_matmul", "bsq_moe_wgrad",
     "bsq_swiglu_mx", "bsq_swiglu_mx_backward",
+    "BSQ_MXFP4", "BSQ_NVFP4", "bsq_quant_fp4", "bsq_scaled_matmul_mxfp4", "bsq_moe_matmul_mxfp4",
     "BsqError",
 ]
 
-BSQ_F32, BSQ_BF16, BSQ_E4M3, BSQ_E5M2, BSQ_E8M0, BSQ_I8, BSQ_I32 = range(7)
+BSQ_F32, BSQ_BF16, BSQ_E4M3, BSQ_E5M2, BSQ_E8M0, BSQ_I8, BSQ_I32, BSQ_E2M1 = range(8)
 BSQ_SOFTMAX, BSQ_SIGMOID = range(2)
+BSQ_MXFP4, BSQ_NVFP4 = range(2)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbsq.so")
@@ -95,6 +97,9 @@ _SIGNATURES = {
     "bsq_moe_wgrad": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _INT, _P]),
     "bsq_swiglu_mx": (_INT, [_I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _P, _P, _P]),
     "bsq_swiglu_mx_backward": (_INT, [_I64, _I64, _P, _INT, _P, _P, _INT, _P, _P]),
+    "bsq_quant_fp4": (_INT, [_I64, _I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _P, _P]),
+    "bsq_scaled_matmul_mxfp4": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _INT, _P]),
+    "bsq_moe_matmul_mxfp4": (_INT, [_I64, _I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _P, _INT, _P]),
 }
 
 
@@ -811,3 +816,129 @@ def bsq_swiglu_mx_backward(kept, kept_scales, dh, dgu, code_dtype: Optional[int]
     _expect(dgu, dh.dtype, (R, 2 * F), "dgu")
     _raise(lib().bsq_swiglu_mx_backward(R, F, _ptr(kept), _one_code(code_dtype, kept), _ptr(kept_scales), _ptr(dh),
                                         dd, _ptr(dgu), _stream(stream)), "bsq_swiglu_mx_backward")
+
+
+# ----------------------------------------------------- 4-bit operands ----
+
+_codes_of = None
+
+
+def _here(*ts):
+    """The tensors are on the current device, whose stream and memory the call uses."""
+    _dev(*ts)
+    now = _torch()._C._cuda_getDevice()
+    for t in ts:
+        if t is not None and t.get_device() != now:
+            raise ValueError(f"tensors must be on the current device ({now}), got one on {t.get_device()}")
+
+
+def _code(t, code_dtype, name):
+    """The format of codes: `code_dtype`, or what the dtype says (bytes: E2M1)."""
+    global _codes_of
+    if _codes_of is None:
+        torch = _torch()
+        _codes_of = {torch.uint8: BSQ_E2M1, torch.float8_e4m3fn: BSQ_E4M3, torch.float8_e5m2: BSQ_E5M2}
+        if hasattr(torch, "float4_e2m1fn_x2"):
+            _codes_of[torch.float4_e2m1fn_x2] = BSQ_E2M1
+    said = _codes_of.get(t.dtype)
+    if said is None:
+        raise TypeError(f"{name} must be bytes of codes, got {t.dtype}")
+    if code_dtype is None:
+        return said
+    if t.dtype != _torch().uint8 and said != code_dtype:
+        raise TypeError(f"{name} of {t.dtype} cannot hold codes of format {code_dtype}")
+    return code_dtype
+
+
+def _packed(codes, scales, shape, block, name, optional=False):
+    """Checks e2m1 codes of `shape` values, two to a byte, and their scales, one per `block` along the last axis."""
+    if codes is None and scales is None and optional:
+        return
+    if codes is None or scales is None:
+        raise ValueError(f"{name} needs both codes and scales")
+    if shape[-1] % block:
+        raise ValueError(f"{name}: {shape[-1]} values are no multiple of the block ({block})")
+    if _code(codes, None, name) != BSQ_E2M1:
+        raise TypeError(f"{name} must hold packed e2m1 codes, got {codes.dtype}")
+    _bytes1(scales, name + " scales")
+    _expect(codes, codes.dtype, (*shape[:-1], shape[-1] // 2), name)
+    _expect(scales, scales.dtype, (*shape[:-1], shape[-1] // block), name + " scales")
+
+
+def bsq_quant_fp4(src, codes=None, scales=None, codes_t=None, scales_t=None, format: int = BSQ_MXFP4, factor=None,
+                  stream=None):
+    """src [rows, cols] or [B, rows, cols] (f32 or bf16) as packed e2m1 codes
+    [.., rows, cols/2] + scales [.., rows, cols/block] and / or transposed
+    codes_t [.., cols, rows/2] + scales_t [.., cols, rows/block]; block 32 with
+    E8M0 scales (BSQ_MXFP4) or 16 with E4M3 scales (BSQ_NVFP4, of src times
+    factor f32 [1])."""
+    _here(src, codes, scales, codes_t, scales_t, factor)
+    if src.dim() not in (2, 3):
+        raise ValueError(f"src must have 2 or 3 dimensions, got shape {tuple(src.shape)}")
+    lead = tuple(src.shape[:-2])
+    rows, cols = src.shape[-2:]
+    sd = _wide(src, "src")
+    if format not in (BSQ_MXFP4, BSQ_NVFP4):
+        raise ValueError("format must be BSQ_MXFP4 or BSQ_NVFP4")
+    block = 16 if format == BSQ_NVFP4 else 32
+    _packed(codes, scales, (*lead, rows, cols), block, "codes", optional=True)
+    _packed(codes_t, scales_t, (*lead, cols, rows), block, "codes_t", optional=True)
+    if factor is not None:
+        _expect(factor, _torch().float32, (1,), "factor")
+    _raise(lib().bsq_quant_fp4(lead[0] if lead else 1, rows, cols, _ptr(src), sd, format, _ptr(factor), _ptr(codes),
+                               _ptr(scales), _ptr(codes_t), _ptr(scales_t), _stream(stream)), "bsq_quant_fp4")
+
+
+def _left(a, a_scales, rank, K, a_dtype, name):
+    """Checks the left operand of a product with 4-bit weights; its format."""
+    code = _code(a, a_dtype, name)
+    shape = (*a.shape[:-1], K)
+    _rank(a, rank, name)
+    if code == BSQ_E2M1:
+        _packed(a, a_scales, shape, 32, name)
+    else:
+        _blocks(a, a_scales, shape, name)
+    return code
+
+
+def bsq_scaled_matmul_mxfp4(lhs, rhs, lhs_scales, rhs_scales, out, lhs_dtype: Optional[int] = None, stream=None):
+    """out [B, M, N] (f32 or bf16) = lhs rhs^T with 4-bit weights: rhs [B, N,
+    K/2] packed e2m1; lhs [B, M, K/2] packed e2m1 (uint8) or [B, M, K] fp8
+    codes; E8M0 scales [B, M, K/32] and [B, N, K/32]."""
+    _here(lhs, rhs, lhs_scales, rhs_scales, out)
+    _rank(rhs, 3, "rhs")
+    _rank(out, 3, "out")
+    B, N = rhs.shape[:2]
+    K = 2 * rhs.shape[2]
+    ld = _left(lhs, lhs_scales, 3, K, lhs_dtype, "lhs")
+    _packed(rhs, rhs_scales, (B, N, K), 32, "rhs")
+    M = lhs.shape[1]
+    if lhs.shape[0] != B:
+        raise ValueError("lhs and rhs must share B")
+    _expect(out, out.dtype, (B, M, N), "out")
+    _raise(lib().bsq_scaled_matmul_mxfp4(B, M, N, K, _ptr(lhs), ld, _ptr(rhs), _ptr(lhs_scales), _ptr(rhs_scales),
+                                         _ptr(out), _wide(out, "out"), _stream(stream)), "bsq_scaled_matmul_mxfp4")
+
+
+def bsq_moe_matmul_mxfp4(a, a_scales, b, b_scales, offsets, out, rows=None, k: int = 1,
+                         a_dtype: Optional[int] = None, stream=None):
+    """The experts' products with 4-bit weights: out [cap, N] (f32 or bf16),
+    row r of expert e's segment = a[rows[r] // k] (or a[r]) times b[e]^T; a
+    [T, K/2] packed e2m1 (uint8) or [T, K] fp8 codes, b [E, N, K/2] packed
+    e2m1, E8M0 scales [.., K/32], offsets i32 [E + 1]."""
+    torch = _torch()
+    _here(a, a_scales, b, b_scales, offsets, out, rows)
+    _rank(b, 3, "b")
+    _rank(out, 2, "out")
+    E, N = b.shape[:2]
+    K = 2 * b.shape[2]
+    ad = _left(a, a_scales, 2, K, a_dtype, "a")
+    _packed(b, b_scales, (E, N, K), 32, "b")
+    T, cap = a.shape[0], out.shape[0]
+    _expect(offsets, torch.int32, (E + 1,), "offsets")
+    _expect(out, out.dtype, (cap, N), "out")
+    if rows is not None:
+        _expect(rows, torch.int32, (cap,), "rows")
+    _raise(lib().bsq_moe_matmul_mxfp4(T, cap, E, N, K, k, _ptr(a), ad, _ptr(a_scales), _ptr(b), _ptr(b_scales),
+                                      _ptr(offsets), _ptr(rows), _ptr(out), _wide(out, "out"), _stream(stream)),
+           "bsq_moe_matmul_mxfp4")

@@ -71,7 +71,7 @@ namespace {
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 bool is_fp8(int d) { return d == BSQ_E4M3 || d == BSQ_E5M2; }
-bool known_dtype(int d) { return d >= BSQ_F32 && d <= BSQ_I32; }
+bool known_dtype(int d) { return d >= BSQ_F32 && d <= BSQ_E2M1; }
 
 // Shared tail of every call: the device check comes after the host-side
 // argument checks, so argument errors are reported without a GPU.

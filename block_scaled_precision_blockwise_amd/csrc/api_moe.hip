@@ -22,7 +22,7 @@ bool elems_fit(int64_t a, int64_t b, int64_t c = 1) {
 }
 bool is_fp8(int d) { return d == BSQ_E4M3 || d == BSQ_E5M2; }
 bool is_wide(int d) { return d == BSQ_F32 || d == BSQ_BF16; }
-bool known_dtype(int d) { return d >= BSQ_F32 && d <= BSQ_I32; }
+bool known_dtype(int d) { return d >= BSQ_F32 && d <= BSQ_E2M1; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 

@@ -28,7 +28,8 @@
  *   - Non-finite inputs give unspecified results (the pages state all
  *     values are finite).
  *   - Format names: E4M3 = OCP float8_e4m3fn, E5M2 = OCP float8_e5m2,
- *     E8M0 = OCP float8_e8m0fnu (scale 2^(b-127)), BF16 = bfloat16.
+ *     E8M0 = OCP float8_e8m0fnu (scale 2^(b-127)), BF16 = bfloat16, E2M1 =
+ *     OCP float4_e2m1fn, two to a byte, the lower index in the low nibble.
  *
  * Citations name the web page and the part of it that defines the
  * operation: "scaled_matmul" = jax.nn.scaled_matmul documentation;
@@ -64,7 +65,8 @@ typedef enum bsq_dtype {
   BSQ_E5M2 = 3,
   BSQ_E8M0 = 4,
   BSQ_I8 = 5,
-  BSQ_I32 = 6
+  BSQ_I32 = 6,
+  BSQ_E2M1 = 7
 } bsq_dtype;
 
 /* ---------------------------------------------------------------- misc -- */
@@ -474,6 +476,69 @@ bsq_status bsq_swiglu_mx(int64_t R, int64_t F, const void* gu, int gu_dtype, int
 bsq_status bsq_swiglu_mx_backward(int64_t R, int64_t F, const uint8_t* kept, int code_dtype,
                                   const uint8_t* kept_scales, const void* dh, int dh_dtype, void* dgu,
                                   void* stream);
+
+/* --------------------------------------------------------- 4-bit operands -- */
+
+typedef enum bsq_fp4 {
+  BSQ_MXFP4 = 0, /* E2M1 codes, E8M0 scales per 32 */
+  BSQ_NVFP4 = 1  /* E2M1 codes, E4M3 scales per 16 */
+} bsq_fp4;
+
+/* Quantizer to 4 bits, along rows and / or transposed from one read (the
+ * operands of scaled_matmul's Notes; the page states no scale rule).
+ *   BSQ_MXFP4  as bsq_quant_mx with fmax 6: E = the smallest integer with
+ *              max(amax, 1e-10) <= 6 * 2^E, codes = e2m1(x * 2^-E).
+ *   BSQ_NVFP4  y = x * factor[0] in float32 (factor NULL: y = x), s =
+ *              e4m3(max(amax / 6, 2^-9)) and at most 448, codes = e2m1(y / s),
+ *              a true division.  The tensor's own factor, typically 6 * 448 /
+ *              max|x|, keeps the scales off E4M3's subnormals; the product is
+ *              then too large by both operands' factors.
+ * Rounded to nearest even; values beyond 6 scales (NVFP4 past 6 * 448, or a
+ * scale that was rounded down) become 6.
+ *   src     [B, rows, cols] of src_dtype (BSQ_F32 or BSQ_BF16)
+ *   codes   [B, rows, cols / 2],  scales   [B, rows, cols / block], or both NULL
+ *   codes_t [B, cols, rows / 2],  scales_t [B, cols, rows / block], or both
+ *           NULL: blocks down the columns, written transposed
+ * An infinity becomes the largest code of its block; a block with NaN has the
+ * NaN scale, so that a product with it is NaN (its codes are unspecified).
+ * Rules: cols is a multiple of the block (32, NVFP4 16), with codes_t rows
+ * too; factor only with BSQ_NVFP4 (else UNSUPPORTED). */
+bsq_status bsq_quant_fp4(int64_t B, int64_t rows, int64_t cols, const void* src, int src_dtype, int format,
+                         const float* factor, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                         uint8_t* scales_t, void* stream);
+
+/* scaled_matmul with 4-bit weights: out[b, m, n] = sum_k lhs[b,m,k]
+ * 2^lhs_scales[b,m,k/32] rhs[b,n,k] 2^rhs_scales[b,n,k/32], float32 sums on
+ * the matrix core.
+ *   lhs [B, M, K / 2] (lhs_dtype BSQ_E2M1) or [B, M, K] (BSQ_E4M3, BSQ_E5M2)
+ *   rhs [B, N, K / 2], BSQ_E2M1
+ *   lhs_scales [B, M, K / 32], rhs_scales [B, N, K / 32], E8M0; read in whole
+ *       aligned words, so that up to 3 bytes behind the last are looked at
+ *   out [B, M, N] of out_dtype (BSQ_F32 or BSQ_BF16)
+ * The gradients are the same call with the transposed operands that
+ * bsq_quant_fp4 writes: dX = dY W with rhs = W's codes_t, dW = dY^T X with lhs
+ * = dY's codes_t and rhs = X's.  A scale byte 0xFF (NaN) gives NaN.
+ * Rules: K % 32 == 0 (else SHAPE); N % 16 == 0, M K / 32 and N K / 32 below
+ * 2^32 - 16, at most 2^31 - 1 tiles of 16 x 16 (else UNSUPPORTED). */
+bsq_status bsq_scaled_matmul_mxfp4(int64_t B, int64_t M, int64_t N, int64_t K, const uint8_t* lhs, int lhs_dtype,
+                                   const uint8_t* rhs, const uint8_t* lhs_scales, const uint8_t* rhs_scales,
+                                   void* out, int out_dtype, void* stream);
+
+/* bsq_moe_matmul with 4-bit weights: out[r] = a[src(r)] B_e^T for the rows r of
+ * expert e's segment, src(r) = rows[r] / k, or r where rows is NULL.  Rows
+ * without a choice, and rows from offsets[E] on, are written as zeros.
+ *   a [T, K / 2] (a_dtype BSQ_E2M1) or [T, K] (BSQ_E4M3, BSQ_E5M2), a_scales
+ *       [T, K / 32]
+ *   b [E, N, K / 2], BSQ_E2M1, b_scales [E, N, K / 32]
+ *   offsets int32 [E + 1] (any row numbers, also unaligned), rows int32 [cap]
+ *   out [cap, N] of out_dtype (BSQ_F32 or BSQ_BF16)
+ * Rules: K % 32 == 0 (else SHAPE); N % 16 == 0, T <= 2^30, T K / 32 and N K /
+ * 32 below 2^32 - 16, cap at most 2^31 - 2^16, at most 2^31 - 1 tiles of 16 x
+ * 16 (else UNSUPPORTED). */
+bsq_status bsq_moe_matmul_mxfp4(int64_t T, int64_t cap, int64_t E, int64_t N, int64_t K, int64_t k,
+                                const uint8_t* a, int a_dtype, const uint8_t* a_scales, const uint8_t* b,
+                                const uint8_t* b_scales, const int32_t* offsets, const int32_t* rows, void* out,
+                                int out_dtype, void* stream);
 
 #ifdef __cplusplus
 }
