@@ -39,12 +39,14 @@ __all__ = [
     "bsq_moe_combine", "bsq_moe_combine_backward", "bsq_moe_matmul", "bsq_moe_wgrad",
     "bsq_swiglu_mx", "bsq_swiglu_mx_backward",
     "BSQ_MXFP4", "BSQ_NVFP4", "bsq_quant_fp4", "bsq_scaled_matmul_mxfp4", "bsq_moe_matmul_mxfp4",
+    "BSQ_LAYER_NORM", "BSQ_RMS_NORM", "bsq_norm_mx", "bsq_norm_backward_workspace_bytes", "bsq_norm_backward",
     "BsqError",
 ]
 
 BSQ_F32, BSQ_BF16, BSQ_E4M3, BSQ_E5M2, BSQ_E8M0, BSQ_I8, BSQ_I32, BSQ_E2M1 = range(8)
 BSQ_SOFTMAX, BSQ_SIGMOID = range(2)
 BSQ_MXFP4, BSQ_NVFP4 = range(2)
+BSQ_LAYER_NORM, BSQ_RMS_NORM = range(2)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbsq.so")
@@ -99,6 +101,9 @@ _SIGNATURES = {
     "bsq_swiglu_mx_backward": (_INT, [_I64, _I64, _P, _INT, _P, _P, _INT, _P, _P]),
     "bsq_quant_fp4": (_INT, [_I64, _I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _P, _P]),
     "bsq_scaled_matmul_mxfp4": (_INT, [_I64, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _INT, _P]),
+    "bsq_norm_mx": (_INT, [_I64, _I64, _P, _INT, _INT, _F32, _P, _P, _P, _INT, _P, _P, _P, _P, _P]),
+    "bsq_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "bsq_norm_backward": (_INT, [_I64, _I64, _P, _P, _INT, _INT, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "bsq_moe_matmul_mxfp4": (_INT, [_I64, _I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _P, _INT, _P]),
 }
 
@@ -942,3 +947,59 @@ def bsq_moe_matmul_mxfp4(a, a_scales, b, b_scales, offsets, out, rows=None, k: i
     _raise(lib().bsq_moe_matmul_mxfp4(T, cap, E, N, K, k, _ptr(a), ad, _ptr(a_scales), _ptr(b), _ptr(b_scales),
                                       _ptr(offsets), _ptr(rows), _ptr(out), _wide(out, "out"), _stream(stream)),
            "bsq_moe_matmul_mxfp4")
+
+
+def _vectors(C, **ts):
+    for name, t in ts.items():
+        if t is not None:
+            _expect(t, _torch().float32, (C,), name)
+
+
+def bsq_norm_mx(x, y=None, codes=None, scales=None, gamma=None, beta=None, mean=None, rstd=None, eps: float = 1e-5,
+                kind: int = BSQ_LAYER_NORM, code_dtype: Optional[int] = None, stream=None):
+    """Layer or rms norm of the rows of x [R, C] (f32 or bf16): y [R, C] of x's
+    dtype and / or y as a product's operand, fp8 codes [R, C] or packed e2m1
+    [R, C/2] (uint8) with E8M0 scales [R, C/32]; gamma, beta f32 [C]; mean,
+    rstd f32 [R] for the gradient."""
+    _here(x, y, codes, scales, gamma, beta, mean, rstd)
+    _rank(x, 2, "x")
+    R, C = x.shape
+    xd = _wide(x, "x")
+    if y is not None:
+        _expect(y, x.dtype, (R, C), "y")
+    cd = BSQ_E4M3
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes needs both codes and scales")
+        cd = _code(codes, code_dtype, "codes")
+        if cd == BSQ_E2M1:
+            _packed(codes, scales, (R, C), 32, "codes")
+        else:
+            _blocks(codes, scales, (R, C), "codes")
+    _vectors(C, gamma=gamma, beta=beta)
+    _vectors(R, mean=mean, rstd=rstd)
+    _raise(lib().bsq_norm_mx(R, C, _ptr(x), xd, kind, eps, _ptr(gamma), _ptr(beta), _ptr(y), cd, _ptr(codes),
+                             _ptr(scales), _ptr(mean), _ptr(rstd), _stream(stream)), "bsq_norm_mx")
+
+
+def bsq_norm_backward_workspace_bytes(R: int, C: int) -> int:
+    return int(lib().bsq_norm_backward_workspace_bytes(R, C))
+
+
+def bsq_norm_backward(x, dy, rstd, dx, mean=None, gamma=None, dgamma=None, dbeta=None, workspace=None,
+                      kind: int = BSQ_LAYER_NORM, stream=None):
+    """Gradients of bsq_norm_mx: dx [R, C] from x and dy of one dtype (f32 or
+    bf16), mean (layer norm) and rstd f32 [R] as the norm gave them, gamma f32
+    [C]; dgamma, dbeta f32 [C] (with a workspace) where given."""
+    _here(x, dy, rstd, dx, mean, gamma, dgamma, dbeta, workspace)
+    _rank(x, 2, "x")
+    R, C = x.shape
+    xd = _wide(x, "x")
+    _expect(dy, x.dtype, (R, C), "dy")
+    _expect(dx, x.dtype, (R, C), "dx")
+    _vectors(C, gamma=gamma, dgamma=dgamma, dbeta=dbeta)
+    _vectors(R, mean=mean, rstd=rstd)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _raise(lib().bsq_norm_backward(R, C, _ptr(x), _ptr(dy), xd, kind, _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+                                   _ptr(dgamma), _ptr(dbeta), _ptr(workspace), nbytes, _stream(stream)),
+           "bsq_norm_backward")

@@ -2,6 +2,7 @@
 // argument validation on the host, then kernel launches on the caller's stream.
 #include "common.h"
 #include "gemm4.h"
+#include "norm.h"
 #include "quant4.h"
 
 using namespace bsq;
@@ -13,6 +14,7 @@ constexpr int64_t kMaxInt = 0x7FFFFFFF;
 constexpr int64_t kMaxContraction = int64_t(1) << 24;
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxNorm = int64_t(1) << 24;  // values of a row
 
 bool elems_fit(int64_t a, int64_t b, int64_t c = 1) {
   int64_t n = 0;
@@ -131,6 +133,76 @@ bsq_status bsq_moe_matmul_mxfp4(int64_t T, int64_t cap, int64_t E, int64_t N, in
   return launch_mx4_product(Mx4Launch{T, cap, E, int(k), N, K, a, a_scales, b, b_scales, offsets, rows, out,
                                       code_of(a_dtype), out_dtype == BSQ_BF16},
                             as_stream(stream));
+}
+
+// -------------------------------------------------------------------- norm --
+
+static bsq_status norm_check(int64_t R, int64_t C, int dtype, int kind) {
+  BSQ_CHECK(R >= 0 && C >= 0, BSQ_ERR_SHAPE, "negative size");
+  BSQ_CHECK(elems_fit(R, C), BSQ_ERR_UNSUPPORTED, "more than 2^60 elements");
+  BSQ_CHECK(known_dtype(dtype), BSQ_ERR_DTYPE, "unknown dtype");
+  BSQ_CHECK(kind == BSQ_LAYER_NORM || kind == BSQ_RMS_NORM, BSQ_ERR_DTYPE, "unknown kind of norm");
+  BSQ_CHECK(is_wide(dtype), BSQ_ERR_UNSUPPORTED, "x must be F32 or BF16");
+  BSQ_CHECK(C <= kMaxNorm, BSQ_ERR_UNSUPPORTED, "rows of more than 2^24 values");
+  return BSQ_OK;
+}
+
+bsq_status bsq_norm_mx(int64_t R, int64_t C, const void* x, int x_dtype, int kind, float eps, const float* gamma,
+                       const float* beta, void* y, int code_dtype, uint8_t* codes, uint8_t* scales, float* mean,
+                       float* rstd, void* stream) {
+  const bsq_status s = norm_check(R, C, x_dtype, kind);
+  if (s != BSQ_OK) return s;
+  BSQ_CHECK((codes == nullptr) == (scales == nullptr), BSQ_ERR_NULL, "codes and their scales come together");
+  if (codes != nullptr) {
+    BSQ_CHECK(known_dtype(code_dtype), BSQ_ERR_DTYPE, "unknown dtype");
+    BSQ_CHECK(is_code(code_dtype), BSQ_ERR_UNSUPPORTED, "code_dtype must be E4M3, E5M2 or E2M1");
+    BSQ_CHECK(C % 32 == 0, BSQ_ERR_SHAPE, "C must be a multiple of the block (32) for codes");
+  }
+  BSQ_CHECK(eps >= 0.0f, BSQ_ERR_UNSUPPORTED, "eps must not be negative");
+  if (R == 0 || C == 0) return ok();
+  BSQ_CHECK_PTR(x);
+  BSQ_CHECK(aligned16(y) && aligned16(codes) && aligned16(gamma) && aligned16(beta), BSQ_ERR_ALIGN,
+            "y, codes, gamma or beta not 16-byte aligned");
+  BSQ_CHECK(word(mean) && word(rstd), BSQ_ERR_ALIGN, "mean or rstd not 4-byte aligned");
+  BSQ_DEVICE();
+  const NormCode code = codes == nullptr         ? NormCode::none
+                        : code_dtype == BSQ_E4M3 ? NormCode::e4m3
+                        : code_dtype == BSQ_E5M2 ? NormCode::e5m2
+                                                 : NormCode::e2m1;
+  return launch_norm(NormLaunch{R, C, x, x_dtype == BSQ_BF16, kind == BSQ_RMS_NORM, eps, gamma, beta, y, code, codes,
+                                scales, mean, rstd},
+                     as_stream(stream));
+}
+
+size_t bsq_norm_backward_workspace_bytes(int64_t R, int64_t C) {
+  if (R < 0 || C < 0) return 0;
+  if (C > kMaxNorm) return SIZE_MAX;
+  const size_t b = size_t(8) * size_t(C) * size_t(R < kNormGroups ? R : kNormGroups);
+  return b < 16 ? 16 : b;
+}
+
+bsq_status bsq_norm_backward(int64_t R, int64_t C, const void* x, const void* dy, int x_dtype, int kind,
+                             const float* gamma, const float* mean, const float* rstd, void* dx, float* dgamma,
+                             float* dbeta, void* workspace, size_t workspace_bytes, void* stream) {
+  const bsq_status s = norm_check(R, C, x_dtype, kind);
+  if (s != BSQ_OK) return s;
+  const bool weights = dgamma != nullptr || dbeta != nullptr;
+  BSQ_CHECK(!weights || workspace_bytes >= bsq_norm_backward_workspace_bytes(R, C), BSQ_ERR_SHAPE,
+            "workspace too small");
+  if (C == 0 || (R == 0 && !weights)) return ok();
+  if (R > 0) {
+    BSQ_CHECK_PTR(x);
+    BSQ_CHECK_PTR(dy);
+    BSQ_CHECK_PTR(dx);
+    BSQ_CHECK(rstd != nullptr && (mean != nullptr || kind == BSQ_RMS_NORM), BSQ_ERR_NULL, "mean or rstd is NULL");
+    BSQ_CHECK(word(mean) && word(rstd), BSQ_ERR_ALIGN, "mean or rstd not 4-byte aligned");
+    if (weights) BSQ_CHECK_PTR(workspace);
+  }
+  BSQ_CHECK(aligned16(gamma) && word(dgamma) && word(dbeta), BSQ_ERR_ALIGN, "gamma, dgamma or dbeta not aligned");
+  BSQ_DEVICE();
+  return launch_norm_backward(NormBackwardLaunch{R, C, x, dy, x_dtype == BSQ_BF16, kind == BSQ_RMS_NORM, gamma, mean,
+                                                 rstd, dx, dgamma, dbeta, static_cast<float*>(workspace)},
+                              as_stream(stream));
 }
 
 }  // extern "C"

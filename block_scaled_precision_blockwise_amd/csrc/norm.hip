@@ -1,0 +1,458 @@
+// Layer and rms norm, whose output may leave as the next product's operand,
+// and their gradients.
+//
+//   mean = sum x / C (rms: 0), rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),
+//   xn = (x - mean) rstd, y = xn gamma + beta
+//   d = dy gamma, dx = rstd (d - xn (sum d xn) / C - (sum d) / C), the last
+//   term for layer norm only; dgamma = sum over rows of dy xn, dbeta of dy
+//
+// in float32.  The variance is summed from x - mean in a second pass over the
+// registers, so that rows far from zero lose nothing.  Codes are of the
+// float32 y, before y's own rounding.
+//
+// Bound by memory.  A row stays in the registers of NT threads, P times eight
+// values each; rows too long for that are read again instead.  The weights'
+// gradients are summed by groups of rows in registers, a group's sums go to the
+// workspace, and a second kernel adds the groups in their order, so that every
+// run gives the same bytes.
+#include "fp4.h"
+#include "moe_index.h"
+#include "norm.h"
+
+#include <type_traits>
+
+namespace bsq {
+
+namespace {
+
+// Sum over NT threads (64: a wave of its own), left in each; `red` is one of
+// two or more places used in turn.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ float sum_over(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) v += red[i];
+  }
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ void sum_over(float& a, float& b, float* red) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (NT > 64) {
+    constexpr int W = NT / 64;
+    if ((threadIdx.x & 63) == 0) {
+      red[threadIdx.x >> 6] = a;
+      red[W + (threadIdx.x >> 6)] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      a += red[i];
+      b += red[W + i];
+    }
+  }
+}
+
+template <int BF16>
+__device__ __forceinline__ float load1(const void* p, int64_t at) {
+  return BF16 ? decode_bf16(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
+}
+template <int BF16>
+__device__ __forceinline__ void store1(void* p, int64_t at, float v) {
+  if (BF16) static_cast<uint16_t*>(p)[at] = uint16_t(bf16_pair(v, v) & 0xFFFFu);
+  else static_cast<float*>(p)[at] = v;
+}
+
+// The columns that a thread of a row's NT holds: VEC eight neighbours P times,
+// else 8 P single ones NT apart.
+template <int NT, int VEC>
+__device__ __forceinline__ int col(int t, int p, int i) {
+  return VEC ? 8 * (t + NT * p) + i : t + NT * (8 * p + i);
+}
+template <int BF16, int NT, int VEC>
+__device__ __forceinline__ void load_row(const void* base, int64_t row0, int t, int p, int C, float (&v)[8]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    if (8 * (t + NT * p) < C) load8<BF16>(base, row0 + 8 * (t + NT * p), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = col<NT, 0>(t, p, i) < C ? load1<BF16>(base, row0 + col<NT, 0>(t, p, i)) : 0.f;
+  }
+}
+template <int BF16, int NT, int VEC>
+__device__ __forceinline__ void store_row(void* base, int64_t row0, int t, int p, int C, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (8 * (t + NT * p) < C) store8<BF16>(base, row0 + 8 * (t + NT * p), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col<NT, 0>(t, p, i) < C) store1<BF16>(base, row0 + col<NT, 0>(t, p, i), v[i]);
+  }
+}
+// gamma or beta of the thread's columns; `none` where it is null.
+template <int NT, int VEC>
+__device__ __forceinline__ void load_weight(const float* w, int t, int p, int C, float none, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = none;
+  if (w == nullptr) return;
+  if constexpr (VEC) {
+    if (8 * (t + NT * p) < C) {
+      const float4* f = reinterpret_cast<const float4*>(w + 8 * (t + NT * p));
+      const float4 a = f[0], b = f[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col<NT, 0>(t, p, i) < C) v[i] = w[col<NT, 0>(t, p, i)];
+  }
+}
+
+// Eight neighbours of a row as codes, four lanes to a block; every lane of the
+// wave takes part, `in` guards the stores.
+__device__ __forceinline__ void put_codes(NormCode code, uint8_t* codes, uint8_t* scales, int64_t at, bool in,
+                                          bool words, const float (&v)[8]) {
+  if (code == NormCode::e2m1) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    const uint32_t e = mx4_byte(group_max_bits<4>(m));
+    put_scale4<4>(scales, at / 32, in, words, e);
+    if (in) *reinterpret_cast<uint32_t*>(codes + at / 2) = encode8_fp4(v, mx_scale(e));
+  } else if (code == NormCode::e4m3) {
+    put_row<0>(codes, scales, at / 8, in, words, v);
+  } else {
+    put_row<1>(codes, scales, at / 8, in, words, v);
+  }
+}
+
+// ---------------------------------------------------------------- forward --
+template <int BF16, int VEC, int NT, int P>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a, int64_t first) {
+  constexpr int kRows = NT < 256 ? 256 / NT : 1;  // of a workgroup
+  __shared__ float red[2][NT > 64 ? NT / 64 : 1];
+  const int t = threadIdx.x % NT, C = int(a.C);
+  const int64_t r = (first + blockIdx.x) * kRows + threadIdx.x / NT;
+  const bool in = r < a.R;
+  const int64_t row0 = (in ? r : a.R - 1) * a.C;
+  saturate_fp8();
+  float x[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) load_row<BF16, NT, VEC>(a.x, row0, t, p, C, x[p]);
+  float mean = 0.f, s = 0.f;
+  if (!a.rms) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[p][i];
+    mean = sum_over<NT>(s, red[0]) / float(C);
+    s = 0.f;
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[p][i] = col<NT, VEC>(t, p, i) < C ? x[p][i] - mean : 0.f;
+      s += x[p][i] * x[p][i];
+    }
+  const float rstd = 1.0f / sqrtf(sum_over<NT>(s, red[1]) / float(C) + a.eps);
+  if (t == 0 && in) {
+    if (a.mean != nullptr) a.mean[r] = mean;
+    if (a.rstd != nullptr) a.rstd[r] = rstd;
+  }
+  const bool words = VEC && C % 128 == 0 && aligned4(a.scales);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    float g[8], b[8];
+    load_weight<NT, VEC>(a.gamma, t, p, C, 1.f, g);
+    load_weight<NT, VEC>(a.beta, t, p, C, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[p][i] = x[p][i] * rstd * g[i] + b[i];
+    if (in && a.y != nullptr) store_row<BF16, NT, VEC>(a.y, row0, t, p, C, x[p]);
+    if (VEC && a.codes != nullptr)
+      put_codes(a.code, a.codes, a.scales, row0 + 8 * (t + NT * p), in && 8 * (t + NT * p) < C, words, x[p]);
+  }
+}
+
+// Any length: a workgroup reads its row three times.
+constexpr int kLong = 1024;
+template <int BF16>
+__global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first) {
+  __shared__ float red[2][kLong / 64];
+  const int64_t r = first + blockIdx.x, row0 = r * a.C;
+  saturate_fp8();
+  float mean = 0.f, s = 0.f;
+  if (!a.rms) {
+    for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += load1<BF16>(a.x, row0 + c);
+    mean = sum_over<kLong>(s, red[0]) / float(a.C);
+    s = 0.f;
+  }
+  for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
+    const float d = load1<BF16>(a.x, row0 + c) - mean;
+    s += d * d;
+  }
+  const float rstd = 1.0f / sqrtf(sum_over<kLong>(s, red[1]) / float(a.C) + a.eps);
+  if (threadIdx.x == 0) {
+    if (a.mean != nullptr) a.mean[r] = mean;
+    if (a.rstd != nullptr) a.rstd[r] = rstd;
+  }
+  auto value = [&](int64_t c) {
+    const float xn = (load1<BF16>(a.x, row0 + c) - mean) * rstd;
+    return xn * (a.gamma != nullptr ? a.gamma[c] : 1.f) + (a.beta != nullptr ? a.beta[c] : 0.f);
+  };
+  if (a.codes == nullptr) {
+    if (a.y == nullptr) return;
+    for (int64_t c = threadIdx.x; c < a.C; c += kLong) store1<BF16>(a.y, row0 + c, value(c));
+    return;
+  }
+  // blocks of 32, four lanes of eight neighbours each; a wave's lanes go on
+  // together, since the maximum of a block is taken across them
+  for (int64_t c0 = 0; c0 < a.C; c0 += 8 * kLong) {
+    const int64_t c = c0 + 8 * threadIdx.x;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c < a.C ? value(c + i) : 0.f;
+    if (c < a.C && a.y != nullptr) store8<BF16>(a.y, row0 + c, v);
+    put_codes(a.code, a.codes, a.scales, row0 + c, c < a.C, false, v);
+  }
+}
+
+// --------------------------------------------------------------- backward --
+// Workgroups go through the rows blockIdx.x + gridDim.x i.
+template <int BF16, int VEC, int NT, int P>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm_dx(NormBackwardLaunch a) {
+  constexpr int kRows = NT < 256 ? 256 / NT : 1;
+  __shared__ float red[2][2 * (NT > 64 ? NT / 64 : 1)];
+  __shared__ float join[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? 2 * 8 * P * NT : 1];
+  const int t = threadIdx.x % NT, sub = threadIdx.x / NT, C = int(a.C);
+  const float inv = 1.0f / float(C);
+  float g[P][8], sg[P][8], sb[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    load_weight<NT, VEC>(a.gamma, t, p, C, 1.f, g[p]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sg[p][i] = sb[p][i] = 0.f;
+  }
+  const int64_t step = int64_t(gridDim.x) * kRows;
+  float x[P][8], dy[P][8], mean = 0.f, rstd = 0.f;
+  auto load = [&](int64_t r) {
+    const int64_t rr = r < a.R ? r : a.R - 1;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      load_row<BF16, NT, VEC>(a.x, rr * a.C, t, p, C, x[p]);
+      load_row<BF16, NT, VEC>(a.dy, rr * a.C, t, p, C, dy[p]);
+    }
+    mean = a.rms ? 0.f : a.mean[rr];
+    rstd = a.rstd[rr];
+  };
+  int buf = 0;
+  for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < a.R; r0 += step, buf ^= 1) {
+    const int64_t r = r0 + sub;
+    load(r);
+    const bool in = r < a.R;
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // columns and rows that are not there have dy 0
+        const float d = in ? dy[p][i] : 0.f, xn = in ? (x[p][i] - mean) * rstd : 0.f;
+        x[p][i] = xn;
+        sg[p][i] += d * xn;
+        sb[p][i] += d;
+        dy[p][i] = d * g[p][i];
+        s1 += dy[p][i] * (col<NT, VEC>(t, p, i) < C ? xn : 0.f);
+        s2 += dy[p][i];
+      }
+    sum_over<NT>(s1, s2, red[buf]);
+    s1 *= inv;
+    s2 = a.rms ? 0.f : s2 * inv;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[p][i] = rstd * (dy[p][i] - x[p][i] * s1 - s2);
+      if (in) store_row<BF16, NT, VEC>(a.dx, r * a.C, t, p, C, x[p]);
+    }
+  }
+  if (a.dgamma == nullptr && a.dbeta == nullptr) return;
+  if constexpr (kRows > 1) {  // the rows of the workgroup, in their order
+    if (sub > 0) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          join[sub - 1][(8 * p + i) * NT + t] = sg[p][i];
+          join[sub - 1][(8 * (P + p) + i) * NT + t] = sb[p][i];
+        }
+    }
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int o = 0; o < kRows - 1; ++o)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sg[p][i] += join[o][(8 * p + i) * NT + t];
+          sb[p][i] += join[o][(8 * (P + p) + i) * NT + t];
+        }
+  }
+  float* const to = a.space + int64_t(blockIdx.x) * C;
+  float* const to_b = to + int64_t(gridDim.x) * C;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    store_row<0, NT, VEC>(to, 0, t, p, C, sg[p]);
+    store_row<0, NT, VEC>(to_b, 0, t, p, C, sb[p]);
+  }
+}
+
+// Any length: a row's sums, then its gradient, from two reads.
+template <int BF16>
+__global__ void __launch_bounds__(kLong) k_norm_dx_long(NormBackwardLaunch a, int64_t first) {
+  __shared__ float red[2 * kLong / 64];
+  const int64_t r = first + blockIdx.x, row0 = r * a.C;
+  const float mean = a.rms ? 0.f : a.mean[r], rstd = a.rstd[r];
+  float s1 = 0.f, s2 = 0.f;
+  for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
+    const float d = load1<BF16>(a.dy, row0 + c) * (a.gamma != nullptr ? a.gamma[c] : 1.f);
+    s1 += d * ((load1<BF16>(a.x, row0 + c) - mean) * rstd);
+    s2 += d;
+  }
+  sum_over<kLong>(s1, s2, red);
+  s1 /= float(a.C);
+  s2 = a.rms ? 0.f : s2 / float(a.C);
+  for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
+    const float d = load1<BF16>(a.dy, row0 + c) * (a.gamma != nullptr ? a.gamma[c] : 1.f);
+    const float xn = (load1<BF16>(a.x, row0 + c) - mean) * rstd;
+    store1<BF16>(a.dx, row0 + c, rstd * (d - xn * s1 - s2));
+  }
+}
+// The weights' gradients of long rows: a thread to a column, groups of rows.
+template <int BF16>
+__global__ void __launch_bounds__(256) k_norm_dw_long(NormBackwardLaunch a, int groups) {
+  const int64_t chunks = up_to(a.C, 256), c = (int64_t(blockIdx.x) % chunks) * 256 + threadIdx.x;
+  const int64_t gr = int64_t(blockIdx.x) / chunks;
+  if (c >= a.C) return;
+  float sg = 0.f, sb = 0.f;
+  for (int64_t r = gr; r < a.R; r += groups) {
+    const float d = load1<BF16>(a.dy, r * a.C + c);
+    sg += d * ((load1<BF16>(a.x, r * a.C + c) - (a.rms ? 0.f : a.mean[r])) * a.rstd[r]);
+    sb += d;
+  }
+  a.space[gr * a.C + c] = sg;
+  a.space[(groups + gr) * a.C + c] = sb;
+}
+
+// Sums over the groups in their order: 32 columns x 8 shares of the groups,
+// the shares added through LDS.
+__global__ void __launch_bounds__(256) k_norm_sum(const float* __restrict__ space, int groups, int64_t C, float* dgamma,
+                                                  float* dbeta) {
+  __shared__ float part[8][32];
+  const int64_t chunks = up_to(C, 32);
+  const int which = int(blockIdx.x / chunks);  // 0: dgamma, 1: dbeta
+  float* const out = which ? dbeta : dgamma;
+  if (out == nullptr) return;
+  const int x = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int64_t c = blockIdx.x % chunks * 32 + x;
+  const int per = (groups + 7) / 8, end = min(groups, (share + 1) * per);
+  float s = 0.f;
+  if (c < C) {
+#pragma unroll 8
+    for (int i = share * per; i < end; ++i) s += space[(int64_t(which) * groups + i) * C + c];
+  }
+  part[share][x] = s;
+  __syncthreads();
+  if (share > 0 || c >= C) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += part[i][x];
+  out[c] = s;
+}
+
+// Threads of a row and how many times eight values each holds: f(NT, P).
+template <typename F>
+bsq_status with_shape(int64_t C, F&& f) {
+#define BSQ_NORM(NT, P) f(std::integral_constant<int, NT>{}, std::integral_constant<int, P>{})
+  if (C <= 512) return BSQ_NORM(64, 1);
+  if (C <= 1024) return BSQ_NORM(64, 2);
+  if (C <= 2048) return BSQ_NORM(256, 1);
+  if (C <= 4096) return BSQ_NORM(256, 2);
+  if (C <= 8192) return BSQ_NORM(512, 2);
+  return BSQ_NORM(1024, 2);
+#undef BSQ_NORM
+}
+constexpr int64_t kInRegisters = 16384;
+
+}  // namespace
+
+bsq_status launch_norm(const NormLaunch& L, hipStream_t st) {
+  if (L.C > kInRegisters)
+    return in_parts(L.R, kLaunchGroups / 2, [&](int64_t first, int64_t n) {
+      if (L.bf16) hipLaunchKernelGGL((k_norm_long<1>), dim3(unsigned(n)), kLong, 0, st, L, first);
+      else hipLaunchKernelGGL((k_norm_long<0>), dim3(unsigned(n)), kLong, 0, st, L, first);
+      return launch_status("norm");
+    });
+  return with_shape(L.C, [&](auto nt, auto p) {
+    constexpr int NT = decltype(nt)::value, P = decltype(p)::value, kRows = NT < 256 ? 256 / NT : 1;
+    return in_parts(up_to(L.R, kRows), kLaunchGroups / 2, [&](int64_t first, int64_t n) {
+      const dim3 g = dim3(unsigned(n)), b = dim3(NT < 256 ? 256 : NT);
+      switch ((L.bf16 ? 1 : 0) | (L.C % 8 == 0 ? 2 : 0)) {
+        case 0: hipLaunchKernelGGL((k_norm<0, 0, NT, P>), g, b, 0, st, L, first); break;
+        case 1: hipLaunchKernelGGL((k_norm<1, 0, NT, P>), g, b, 0, st, L, first); break;
+        case 2: hipLaunchKernelGGL((k_norm<0, 1, NT, P>), g, b, 0, st, L, first); break;
+        default: hipLaunchKernelGGL((k_norm<1, 1, NT, P>), g, b, 0, st, L, first);
+      }
+      return launch_status("norm");
+    });
+  });
+}
+
+bsq_status launch_norm_backward(const NormBackwardLaunch& L, hipStream_t st) {
+  const bool weights = L.dgamma != nullptr || L.dbeta != nullptr;
+  int groups = 0;
+  bsq_status s = BSQ_OK;
+  if (L.R > 0 && L.C > kInRegisters) {
+    s = in_parts(L.R, kLaunchGroups / 2, [&](int64_t first, int64_t n) {
+      if (L.bf16) hipLaunchKernelGGL((k_norm_dx_long<1>), dim3(unsigned(n)), kLong, 0, st, L, first);
+      else hipLaunchKernelGGL((k_norm_dx_long<0>), dim3(unsigned(n)), kLong, 0, st, L, first);
+      return launch_status("norm_backward");
+    });
+    if (s != BSQ_OK || !weights) return s;
+    groups = int(L.R < 32 ? L.R : 32);
+    const dim3 g = dim3(unsigned(up_to(L.C, 256) * groups));
+    if (L.bf16) hipLaunchKernelGGL((k_norm_dw_long<1>), g, 256, 0, st, L, groups);
+    else hipLaunchKernelGGL((k_norm_dw_long<0>), g, 256, 0, st, L, groups);
+    s = launch_status("norm_backward");
+  } else if (L.R > 0) {
+    s = with_shape(L.C, [&](auto nt, auto p) {
+      constexpr int NT = decltype(nt)::value, P = decltype(p)::value, kRows = NT < 256 ? 256 / NT : 1;
+      const int64_t most = 512, all = up_to(L.R, kRows);
+      groups = int(all < most ? all : most);
+      const dim3 g = dim3(unsigned(groups)), b = dim3(NT < 256 ? 256 : NT);
+      switch ((L.bf16 ? 1 : 0) | (L.C % 8 == 0 ? 2 : 0)) {
+        case 0: hipLaunchKernelGGL((k_norm_dx<0, 0, NT, P>), g, b, 0, st, L); break;
+        case 1: hipLaunchKernelGGL((k_norm_dx<1, 0, NT, P>), g, b, 0, st, L); break;
+        case 2: hipLaunchKernelGGL((k_norm_dx<0, 1, NT, P>), g, b, 0, st, L); break;
+        default: hipLaunchKernelGGL((k_norm_dx<1, 1, NT, P>), g, b, 0, st, L);
+      }
+      return launch_status("norm_backward");
+    });
+  }
+  if (s != BSQ_OK || !weights) return s;
+  hipLaunchKernelGGL(k_norm_sum, dim3(unsigned(2 * up_to(L.C, 32))), 256, 0, st, L.space, groups, L.C, L.dgamma, L.dbeta);
+  return launch_status("norm_backward (weights)");
+}
+
+}  // namespace bsq

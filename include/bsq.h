@@ -540,6 +540,46 @@ bsq_status bsq_moe_matmul_mxfp4(int64_t T, int64_t cap, int64_t E, int64_t N, in
                                 const uint8_t* b_scales, const int32_t* offsets, const int32_t* rows, void* out,
                                 int out_dtype, void* stream);
 
+typedef enum bsq_norm {
+  BSQ_LAYER_NORM = 0, /* the mean is taken off */
+  BSQ_RMS_NORM = 1
+} bsq_norm;
+
+/* Norm of each row, whose output may leave as the next product's operand:
+ * mean = sum x / C (BSQ_RMS_NORM: 0), rstd = 1 / sqrt(sum (x - mean)^2 / C +
+ * eps), y = (x - mean) rstd gamma + beta, in float32.
+ *   x      [R, C] of x_dtype (BSQ_F32 or BSQ_BF16)
+ *   gamma, beta  float32 [C], or NULL (1 and 0)
+ *   y      [R, C] of x_dtype (out), or NULL
+ *   codes, scales  y (before its rounding to x_dtype) quantized along rows, or
+ *          both NULL: code_dtype BSQ_E4M3 or BSQ_E5M2, codes [R, C], as
+ *          bsq_quant_mx; or BSQ_E2M1, codes [R, C / 2], as bsq_quant_fp4
+ *          (BSQ_MXFP4); scales E8M0 [R, C / 32]
+ *   mean, rstd   float32 [R] (out), or NULL; the gradient reads them
+ * Infinities and NaN in a row make it NaN: in y, in e4m3 and e5m2 codes, and as
+ * the NaN scale of e2m1 codes.
+ * Rules: with codes C % 32 == 0 (else SHAPE); C <= 2^24, eps >= 0 (else
+ * UNSUPPORTED).  Rows of up to 16384 are held in registers, longer ones are
+ * read three times. */
+bsq_status bsq_norm_mx(int64_t R, int64_t C, const void* x, int x_dtype, int kind, float eps, const float* gamma,
+                       const float* beta, void* y, int code_dtype, uint8_t* codes, uint8_t* scales, float* mean,
+                       float* rstd, void* stream);
+
+/* Gradients of bsq_norm_mx: with xn = (x - mean) rstd and d = dy gamma,
+ * dx = rstd (d - xn sum(d xn) / C - sum(d) / C), without the last term for
+ * BSQ_RMS_NORM; dgamma = sum over rows of dy xn, dbeta = sum over rows of dy.
+ *   x, dy, dx  [R, C] of x_dtype;  gamma float32 [C] or NULL (1)
+ *   mean (NULL with BSQ_RMS_NORM), rstd  float32 [R], as bsq_norm_mx gave them
+ *   dgamma, dbeta  float32 [C] (out), or NULL; zeros where R is 0
+ *   workspace  at least bsq_norm_backward_workspace_bytes(R, C) bytes, for
+ *              dgamma and dbeta (NULL and 0 where both are NULL)
+ * Every run gives the same bytes.  Rules: C <= 2^24 (else UNSUPPORTED); a
+ * smaller workspace -> SHAPE. */
+size_t bsq_norm_backward_workspace_bytes(int64_t R, int64_t C);
+bsq_status bsq_norm_backward(int64_t R, int64_t C, const void* x, const void* dy, int x_dtype, int kind,
+                             const float* gamma, const float* mean, const float* rstd, void* dx, float* dgamma,
+                             float* dbeta, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
