@@ -432,6 +432,425 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
   }
 }
 
+// -------------------------------------------------------------- big tiles --
+// 256 x 256 by four waves of 128 x 128, one wave per SIMD: a step's LDS reads
+// are 128 KiB for 1024 4-bit MFMAs of 16 cycles on four SIMDs, and the
+// accumulators of a wave fill the 256 accumulation registers.  With nothing
+// else to run on its SIMD a wave may never wait, so it goes through a step in
+// four phases, one for each pairing of the halves of its A and B fragments (A0
+// B0, A0 B1, A1 B1, A1 B0), and reads beside each the half that a later phase
+// needs: B1 and A1 of this step, then A0 and B0 of the next (B0 fragment by
+// fragment, as its last MFMAs pass).  The reads of a stage end in its second
+// phase: the step's one barrier is there, the loads of the step after next
+// follow it, and have until the next barrier to land.
+//
+// Scales of 16 blocks of a row (a group of 2 steps of 4 bits, 4 of 8) go
+// through registers, so that they may start at any byte: what the contraction
+// has not got becomes 1, and the 4 x 4 bytes are transposed, so that a lane's
+// one word holds its block of each of four MFMAs.
+//
+// A workgroup goes through the tiles blockIdx.x + gridDim.x i.  Between two of
+// them the output of the last one goes from the accumulators to memory without
+// LDS (lanes exchange halves until each holds 16 neighbouring bytes of a row),
+// the loads of the next one's first two steps beside it; the search for the
+// one after follows while they land.
+
+// 16 bytes from any address before `end`, which has 16 in front of it: the last
+// 16 where fewer are left.
+__device__ __forceinline__ uint4 scales16(const uint8_t* p, const uint8_t* end) {
+  uint4 v;
+  __builtin_memcpy(&v, p + 16 <= end ? p : end - 16, 16);
+  return v;
+}
+// The 4 x 4 bytes transposed.  Where a row ends (n < 16), the bytes that are
+// there are brought to the front by `skip` and the rest becomes 0x7F.
+__device__ __forceinline__ uint4 turned(uint4 v, int n, int skip) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (n < 16) {
+    uint32_t x[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      uint32_t lo = 0u, hi = 0u;  // the words that word d of the shifted bytes spans
+#pragma unroll
+      for (int i = d; i < 4; ++i) {
+        if (i == d + (skip >> 2)) lo = w[i];
+        if (i == d + (skip >> 2) + 1) hi = w[i];
+      }
+      x[d] = __builtin_amdgcn_alignbyte(hi, lo, uint32_t(skip & 3));
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int have = min(max(n - 4 * d, 0), 4);
+      const uint32_t keep = uint32_t((uint64_t(1) << (8 * have)) - 1);
+      w[d] = (x[d] & keep) | (0x7F7F7F7Fu & ~keep);
+    }
+  }
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  return make_uint4(__builtin_amdgcn_perm(c, a, 0x05040100u), __builtin_amdgcn_perm(c, a, 0x07060302u),
+                    __builtin_amdgcn_perm(d, b, 0x05040100u), __builtin_amdgcn_perm(d, b, 0x07060302u));
+}
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// acc += b x a in inline asm, for its place among the loads and reads (the
+// compiler moves the builtin past all of them) and for accumulation registers;
+// two wait states first, which an operand that a vector instruction wrote
+// needs.  HH: the byte (0 or 1) of both scale words.
+template <int FA, int HH>
+__device__ __forceinline__ void mfma_at(v4f& acc, v4i b, const v8i& a, int sb, int sa) {
+  const v4i lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+#define BSQ_MFMA(SEL, FMT, A)                                                                          \
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4" FMT \
+               : "+a"(acc)                                                                             \
+               : "v"(b), "v"(A), "v"(sb), "v"(sa))
+#define BSQ_MFMA_HH(FMT, A)                                                              \
+  do {                                                                                   \
+    if constexpr (HH == 0) BSQ_MFMA("op_sel_hi:[0,0,0]", FMT, A);                        \
+    else BSQ_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]", FMT, A);                           \
+  } while (0)
+  if constexpr (FA == 4) BSQ_MFMA_HH(" blgp:4", lo);
+  else if constexpr (FA == 1) BSQ_MFMA_HH(" blgp:1", a);
+  else BSQ_MFMA_HH("", a);
+#undef BSQ_MFMA_HH
+#undef BSQ_MFMA
+}
+
+template <int FA, int OUT_BF16>
+__global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
+  constexpr int TM = 256, TN = 256, NW = 4;
+  constexpr int kStep = FA == 4 ? 256 : 128, kHalves = kStep / 128, kGroup = 512 / kStep;  // steps of 16 blocks
+  constexpr int BA = 128, BB = kStep / 2, RB = 1024 / BB, LB = TN / RB / NW;  // loads of B per wave and step
+  constexpr int kStage = TM * BA + TN * BB;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_s[2 * (TM + TN) * 16];
+  __shared__ int src[2][TM];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = scalar(tid >> 6);
+  const View4<FA> view{p};
+  const int nb = p.K / 32, all = (p.K + kStep - 1) / kStep;
+  const bool part = p.K % kStep != 0;
+
+  // ---- loads: 8 slices of 8 rows of A per wave (and of B, or 4 of 16 rows of
+  // 64 bytes); lane i fills the i-th 16 bytes of a slice with the chunk that
+  // the swizzle keeps there (see k_mx4_tile).  32-bit offsets from a base that
+  // moves on by a step (the launcher sends what they do not reach elsewhere).
+  const int lrow = lane >> 3, ca = 16 * ((lane & 7) ^ (4 * (w & 1) + (lrow >> 1)));
+  const int brow = BB == 128 ? lrow : 2 * lrow + ((lane >> 2) & 1);
+  const int cb = BB == 128 ? ca : 16 * ((lane & 3) ^ ((lrow >> 1) & 3));
+  // whether the last step has not got the lane's chunk: it loads the row's
+  // first of that step instead, and puts zeros over it
+  const bool past_a = part && int64_t(all - 1) * BA + ca >= view.pitch_a();
+  const bool past_b = part && int64_t(all - 1) * BB + cb >= view.pitch_b();
+  const uint8_t *pa, *pb;
+  uint32_t off[8 + LB];
+  uint32_t back_a = 0, back_b = 0;  // of the step that is loaded
+  const uint32_t lbase = lds_of(lds + 1024 * w);
+  uint32_t to = lbase;  // stage that is loaded
+  auto last_step = [&](bool yes) {
+    back_a = yes && past_a ? uint32_t(ca) : 0u;
+    back_b = yes && past_b ? uint32_t(cb) : 0u;
+  };
+  auto load = [&](int s, uint32_t to) {
+    const int at = s < 8 ? 1024 * NW * s : TM * BA + 1024 * NW * (s - 8);
+    dma16(s < 8 ? pa : pb, off[s] - (s < 8 ? back_a : back_b), to, at);
+  };
+  auto loaded = [&] {  // a whole step
+    pa += BA;
+    pb += BB;
+    to = 2 * lbase + kStage - to;
+  };
+  // Zeros over the chunks that the last step, in the stage from `stage` bytes
+  // on, has not got; its loads have landed.
+  auto blank = [&](int stage) {
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t* const at = lds + stage + 1024 * w + 16 * lane;
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (past_a) *reinterpret_cast<uint4*>(at + 1024 * NW * s) = zero;
+#pragma unroll
+    for (int s = 0; s < LB; ++s)
+      if (past_b) *reinterpret_cast<uint4*>(at + TM * BA + 1024 * NW * s) = zero;
+  };
+  // scales: thread t has row t of A and of B, 16 blocks at a time
+  const uint8_t *sa_row, *sb_row, *sa_end, *sb_end;
+  uint4 va, vb;
+  auto load_scales = [&](int q) {
+    va = scales16(sa_row + 16 * q, sa_end);
+    vb = scales16(sb_row + 16 * q, sb_end);
+  };
+  auto put_scales = [&](int q) {
+    uint8_t* const at = lds_s + (q & 1) * (TM + TN) * 16 + 16 * tid;
+    auto skip = [&](const uint8_t* row, const uint8_t* end) { return max(int(row + 16 * q + 16 - end), 0); };
+    *reinterpret_cast<uint4*>(at) = turned(va, nb - 16 * q, skip(sa_row, sa_end));
+    *reinterpret_cast<uint4*>(at + TM * 16) = turned(vb, nb - 16 * q, skip(sb_row, sb_end));
+  };
+  // Addresses of tile t, whose rows of A are in src[buf], and its first scales.
+  auto begin = [&](const Place4& t, int buf) {
+    if (t.none || all == 0) return;
+    // rows of their own are near the tile's first; gathered ones anywhere
+    const int near = p.rows != nullptr ? 0 : min(t.m0, int(p.T) - 1);
+    auto a_row = [&](int r) { return max(src[buf][r], near) - near; };
+    pa = scalar(view.a(t.e) + near * view.pitch_a());
+    pb = scalar(view.b(t.e) + int64_t(t.n0) * view.pitch_b());
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      off[s] = uint32_t(a_row(8 * (w + NW * s) + lrow)) * uint32_t(view.pitch_a()) + uint32_t(ca);
+#pragma unroll
+    for (int s = 0; s < LB; ++s)
+      off[8 + s] = uint32_t(min(RB * (w + NW * s) + brow, p.N - 1 - t.n0)) * uint32_t(view.pitch_b()) + uint32_t(cb);
+    const int64_t sp = view.pitch_s();
+    sa_row = view.sa(t.e) + (int64_t(a_row(tid)) + near) * sp;
+    sb_row = view.sb(t.e) + int64_t(min(t.n0 + tid, p.N - 1)) * sp;
+    sa_end = view.sa(t.e) + p.T * sp;
+    sb_end = view.sb(t.e) + p.N * sp;
+    to = lbase;
+    load_scales(0);
+  };
+  // Quarter q of the loads of a tile's first two steps.
+  auto preload = [&](int nk, int q) {
+    if (nk <= q / 2) return;
+    const uint32_t stage = uint32_t(scalar(int(lbase + (q < 2 ? 0 : kStage))));
+    last_step(part && q / 2 == nk - 1);
+    if (q & 1) {
+#pragma unroll
+      for (int s = 0; s < LB; ++s) load(8 + s, stage);
+      loaded();
+    } else {
+#pragma unroll
+      for (int s = 0; s < 8; ++s) load(s, stage);
+    }
+  };
+
+  const int wm = w & 1, wn = w >> 1, g = lane >> 4, r16 = lane & 15;
+  const int ra = (128 * wm + r16) * BA, rb = TM * BA + (128 * wn + r16) * BB;
+  const int x8 = r16 >> 1;
+  // of the stage that is read: where a row's two chunks are
+  const int oa0 = ra + 16 * (g ^ x8), oa1 = ra + 16 * ((4 + g) ^ x8);
+  const int ob0 = BB == 128 ? rb + 16 * (g ^ x8)
+                            : TM * BA + (64 * wn + x8) * 128 + 64 * (r16 & 1) + 16 * (g ^ ((r16 >> 2) & 3));
+  const int ob1 = rb + 16 * ((4 + g) ^ x8);
+  const int ssa = (128 * wm + r16) * 16 + 4 * g, ssb = (TM + 128 * wn + r16) * 16 + 4 * g;
+  v4f acc[8][8];  // [column block][row block]
+  v8i fa[8];
+  v4i fb[8][kHalves];
+  int qa[8], qb[8];
+  int o = 0;  // stage that is read
+  auto a_part = [&](int f, int h) {  // 16 bytes of a fragment
+    const uint4 v = *reinterpret_cast<const uint4*>(lds + o + (h ? oa1 : oa0) + 16 * f * BA);
+    fa[f][4 * h] = int(v.x);
+    fa[f][4 * h + 1] = int(v.y);
+    fa[f][4 * h + 2] = int(v.z);
+    fa[f][4 * h + 3] = int(v.w);
+  };
+  auto b_part = [&](int f, int h) {
+    const uint4 v = *reinterpret_cast<const uint4*>(lds + o + (h ? ob1 : ob0) + 16 * f * BB);
+    fb[f][h] = v4i{int(v.x), int(v.y), int(v.z), int(v.w)};
+  };
+  auto scale_a = [&](int q, int f) -> int {
+    return *reinterpret_cast<const int*>(lds_s + (q & 1) * (TM + TN) * 16 + ssa + 16 * 16 * f);
+  };
+  auto scale_b = [&](int q, int f) -> int {
+    return *reinterpret_cast<const int*>(lds_s + (q & 1) * (TM + TN) * 16 + ssb + 16 * 16 * f);
+  };
+  // Nothing, but no use of an accumulator moves past it.
+  auto settle = [&] {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) asm volatile("" : "+a"(acc[j][i]));
+  };
+  auto clear = [&] {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  // The MFMAs of the halves j0 of B and i0 of A, column by column, two blocks
+  // at a time; `beside(x)` comes between the first of them.
+  auto phase = [&](int j0, int i0, auto&& beside) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int j = j0 + x / 2, i = i0 + 2 * (x & 1);
+      mfma_at<FA, 0>(acc[j][i], fb[j][0], fa[i], qb[j], qa[i]);
+      beside(x);
+      mfma_at<FA, 0>(acc[j][i + 1], fb[j][0], fa[i + 1], qb[j], qa[i + 1]);
+      if constexpr (kHalves == 2) {
+        v8i a0 = __builtin_shufflevector(fa[i], fa[i], 4, 5, 6, 7, 4, 5, 6, 7);
+        v8i a1 = __builtin_shufflevector(fa[i + 1], fa[i + 1], 4, 5, 6, 7, 4, 5, 6, 7);
+        mfma_at<FA, 1>(acc[j][i], fb[j][kHalves - 1], a0, qb[j], qa[i]);
+        mfma_at<FA, 1>(acc[j][i + 1], fb[j][kHalves - 1], a1, qb[j], qa[i + 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Step ks; LOADS: the step after next follows it, and is loaded.
+  auto step = [&](int ks, int nk, auto loads) {
+    constexpr bool LOADS = decltype(loads)::value;
+    const int q = (ks + 1) / kGroup, at = (ks + 1) % kGroup;  // of the next step
+    phase(0, 0, [&](int x) {
+      if (x % 2 < kHalves) b_part(4 + x / 2, x & 1);
+    });
+    phase(4, 0, [&](int x) { a_part(4 + x / 2, x & 1); });
+    __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    if (part && ks + 1 == nk - 1) blank(o ^ kStage);
+    if (at == 0 && ks + 1 < nk) put_scales(q);
+    barrier();
+    if (LOADS && at == kGroup - 1) load_scales(q + 1);
+    o ^= kStage;
+    const uint32_t fill = uint32_t(scalar(int(to)));
+    if (LOADS) last_step(part && ks + 2 == nk - 1);
+    int next[16];  // scales of the next step
+    phase(4, 4, [&](int x) {
+      a_part(x / 2, x & 1);
+      next[x] = scale_a(q, x);
+      if (LOADS) load(x, fill);
+    });
+    // fragment f of B0 is free after its last MFMA
+    phase(0, 4, [&](int x) {
+      if (x >= 2 && x % 2 < kHalves) b_part(x / 2 - 1, x & 1);
+      next[8 + x] = scale_b(q, x);
+      if (LOADS && x < LB) load(8 + x, fill);
+    });
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) b_part(3, h);
+    // in inline asm, so that they stay behind the MFMAs
+    const int bits = 8 * kHalves * at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      asm volatile("v_lshrrev_b32 %0, %2, %1" : "=v"(qa[i]) : "v"(next[i]), "s"(bits));
+      asm volatile("v_lshrrev_b32 %0, %2, %1" : "=v"(qb[i]) : "v"(next[8 + i]), "s"(bits));
+    }
+    if (LOADS) loaded();
+  };
+  // ---- out: lane (g, r16) has columns 4 g .. 4 g + 3 of row r16 of each
+  // block.  bfloat16: of two blocks' eight, halves of the wave and then rows
+  // of 16 lanes change places until it has columns 8 g .. 8 g + 7 of the 32;
+  // then neighbouring rows trade one pair of blocks each, so that a store
+  // writes whole 128-byte lines.
+  auto output = [&](const Place4& t, int buf, auto&& beside) {
+    constexpr int kElem = OUT_BF16 ? 2 : 4;
+    const int64_t pitch = int64_t(p.N) * kElem;
+    const int n0 = t.n0 + 128 * wn, left = p.N - n0;  // columns of the wave
+    uint8_t* at = static_cast<uint8_t*>(p.out) + view.row0(t.e) * pitch + byte_at(t.m0, 128 * wm, pitch, n0, kElem);
+    const bool odd = r16 & 1;
+    uint8_t* const pair = at + (r16 & 14) * pitch + (odd ? 64 : 0) + 16 * g;
+    at += r16 * pitch + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      beside(i);
+      const int tr = 128 * wm + 16 * i + r16;
+      const bool none = src[buf][tr] < 0, in = row_in(t.m0, tr, t.m_end);
+      if constexpr (OUT_BF16) {
+        const bool even_in = row_in(t.m0, tr & ~1, t.m_end), odd_in = row_in(t.m0, tr | 1, t.m_end);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {  // 64 columns
+          uint32_t v[2][4];            // 8 columns of 32, twice
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = 4 * q + 2 * h;
+            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_convertvector(acc[j][i], bf16x4));  // to nearest even
+            const u32x2 y = __builtin_bit_cast(u32x2, __builtin_convertvector(acc[j + 1][i], bf16x4));
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const auto a = __builtin_amdgcn_permlane32_swap(x[d], y[d], false, false);
+              const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+              v[h][d] = none ? 0u : uint32_t(b[0]);
+              v[h][2 + d] = none ? 0u : uint32_t(b[1]);
+            }
+          }
+          u32x4_t even_row, odd_row;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t got = uint32_t(__builtin_amdgcn_mov_dpp(int(odd ? v[0][d] : v[1][d]), 0xB1, 0xF, 0xF, true));
+            even_row[d] = odd ? got : v[0][d];
+            odd_row[d] = odd ? v[1][d] : got;
+          }
+          if (64 * q + (odd ? 32 : 0) + 8 * g < left) {
+            uint8_t* const to = pair + 16 * i * pitch + 128 * q;
+            if (even_in) __builtin_nontemporal_store(even_row, reinterpret_cast<u32x4_t*>(to));
+            if (odd_in) __builtin_nontemporal_store(odd_row, reinterpret_cast<u32x4_t*>(to + pitch));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v4f v;  // one at a time out of the accumulation registers
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            float x;
+            asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(acc[j][i][d]));
+            v[d] = none ? 0.f : x;
+          }
+          if (in && 16 * j + 4 * g < left)
+            __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(at + 16 * i * pitch + 64 * j));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  Place4 cur, next{};
+  int L = blockIdx.x, buf = 0;
+  if (!find_place4<TM, TN>(p, lane, L, false, cur)) return;
+  src[0][tid] = source4(p, cur, tid);
+  __syncthreads();
+  begin(cur, 0);
+  int nk = cur.none ? 0 : all;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) preload(nk, q);
+  clear();
+  for (;;) {
+    L += gridDim.x;
+    const bool more = find_place4<TM, TN>(p, lane, L, false, next);
+    const int row = more ? source4(p, next, tid) : -1;
+    if (nk > 0) put_scales(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    if (part && nk == 1) blank(0);
+    __syncthreads();
+    if (nk > 0) {
+      o = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a_part(i, h);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) b_part(i, h);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        qa[i] = scale_a(0, i);
+        qb[i] = scale_b(0, i);
+      }
+      settle();  // the zeros, before an MFMA adds to them
+      asm volatile("s_nop 15");
+      int ks = 0;
+      for (; ks < nk - 2; ++ks) step(ks, nk, std::true_type{});
+      for (; ks < nk; ++ks) step(ks, nk, std::false_type{});
+      asm volatile("s_nop 15\n\ts_nop 15");  // the last MFMAs, before their results are read
+      settle();
+    }
+    // the last step's barrier is past the last reads of both stages that count
+    const Place4 done = cur;
+    cur = next;
+    const int done_buf = buf;
+    nk = more && !cur.none ? all : 0;
+    if (more) {
+      buf ^= 1;
+      src[buf][tid] = row;
+      __syncthreads();
+      begin(cur, buf);
+    }
+    output(done, done_buf, [&](int i) {
+      if (i < 4) preload(nk, i);
+    });
+    if (!more) return;
+    clear();
+  }
+}
+
 template <typename F>
 bsq_status with_code(Code4 a, F&& f) {
   switch (a) {
@@ -469,6 +888,18 @@ bsq_status launch_tile(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   });
 }
 
+bsq_status launch_big(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
+  // one workgroup to a CU, each going through its share of the tiles
+  const int64_t grid = tile_rows(L, 256) * up_to(L.N, 256);
+  const dim3 g = dim3(unsigned(grid < kCUs ? grid : kCUs)), b = dim3(256);
+  return with_code(L.a, [&](auto fa) {
+    constexpr int FA = decltype(fa)::value;
+    if (L.out_bf16) hipLaunchKernelGGL((k_mx4_big<FA, 1>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((k_mx4_big<FA, 0>), g, b, 0, st, a);
+    return launch_status("mx4 product (big tiles)");
+  });
+}
+
 }  // namespace
 
 bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
@@ -476,6 +907,10 @@ bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
                   L.out_bf16 ? 1 : 0, 0};
   const int64_t rows = L.offsets ? (L.rows && L.T < L.cap / L.k ? L.T * L.k : L.cap) / L.E : L.T;
   if (rows <= 16 && L.cap <= (1 << 20)) return launch_few<1, 2, 8>(L, a, st);
+  const int64_t n = L.offsets ? rows * L.E : L.T * L.E, half = L.offsets ? L.E / 2 : 0;
+  const int64_t pitch_a = L.a == Code4::e2m1 ? L.K / 2 : L.K;
+  const int64_t tiles = (L.offsets ? n / 256 + half : up_to(L.T, 256) * L.E) * up_to(L.N, 256);
+  if (rows >= 160 && tiles >= 160 && (L.rows == nullptr || L.T * pitch_a < (int64_t(1) << 32))) return launch_big(L, a, st);
   return launch_tile<2, 2, 2, 4, 2>(L, a, st);
 }
 

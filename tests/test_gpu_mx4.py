@@ -162,8 +162,46 @@ def test_dense_exact(B, M, N, K, kind):
         assert torch.equal(bf[i], y.float().bfloat16())
 
 
+# tiles of 256 x 256: one step of the contraction or less, two, more than a
+# group of scales, ends inside a step; rows and columns past the last tile
+BIG = [(1, 2817, 3600, K) for K in (32, 96, 128, 256, 288, 384, 512, 544, 800, 1024, 1056, 1408)] + [(3, 1030, 2576, 672)]
+
+
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B, M, N, K", [(1, 1, 272, 4096), (2, 33, 144, 288), (1, 200, 272, 1056), (1, 257, 528, 1312)])
+@pytest.mark.parametrize("B, M, N, K", BIG)
+def test_dense_exact_big(B, M, N, K, kind):
+    test_dense_exact(B, M, N, K, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("K", [128, 288, 1056])
+def test_ragged_exact_big(K, own, kind):
+    """Many rows to an expert: segments that start anywhere, an empty one, holes, rows behind the last."""
+    counts, T, N, k = [600, 0, 1033, 257, 900, 1, 640], 1100, 2576, 3
+    say("mxfp4 ragged, big tiles", K, own, kind)
+    b, sb = exact_operand((len(counts), N, K), "e2m1", 6)
+    offsets, rows = ragged(counts, T, k, 8, 7)
+    cap = rows.numel()
+    T = cap - 30 if own else T  # own rows past A's are zeros
+    a, sa = exact_operand((T, K), kind, 5)
+    out, bf = empty(cap, N, dtype=torch.float32), empty(cap, N, dtype=torch.bfloat16)
+    for o in (out, bf):
+        bsq.bsq_moe_matmul_mxfp4(a, sa, b, sb, offsets, o, rows=None if own else rows, k=k)
+    want = torch.zeros(cap, N, dtype=torch.float64, device="cuda")
+    ends, x = offsets.tolist(), decode(a, sa)
+    at = torch.arange(cap, device="cuda") if own else torch.where(rows >= 0, rows // k, -1).long()
+    at = torch.where(at < T, at, -1)
+    for e in range(len(counts)):
+        r = at[ends[e]:ends[e + 1]]
+        want[ends[e]:ends[e + 1]] = torch.where((r >= 0)[:, None], x[r.clamp_min(0)], 0.0) @ decode(b[e], sb[e]).t()
+    assert torch.equal(out.double(), want), int((out.double() != want).sum())
+    assert torch.equal(bf, want.float().bfloat16())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B, M, N, K", [(1, 1, 272, 4096), (2, 33, 144, 288), (1, 200, 272, 1056), (1, 257, 528, 1312),
+                                        (1, 2817, 3600, 1056)])
 def test_dense_any_codes(B, M, N, K, kind):
     say("mxfp4 dense, any codes", B, M, N, K, kind)
     a, sa = full_operand((B, M, K), kind, 3)
