@@ -63,30 +63,40 @@ struct View4 {  // FA: 0 e4m3, 1 e5m2, 4 e2m1
   __device__ __forceinline__ int64_t row0(int e) const { return ragged() ? 0 : int64_t(e) * p.T; }  // of out
 };
 
-// The workgroup's tile `L` in the order of tiles `rows_first`: along the
-// columns first (few rows) or by tile_order.
+// What a lane knows of the tiles of all experts (or of the batch: `total` only).
+struct Deal4 {
+  int total;
+  uint32_t before, mine;
+};
+template <int TM>
+__device__ __forceinline__ Deal4 deal4(const Mx4Args& p, const int32_t* offsets, int lane) {
+  Deal4 d{int((p.T + TM - 1) / TM) * p.E, 0, 0};
+  if (p.offsets != nullptr) d.total = tiles_total(Segments<TM>{offsets, p.E, p.cap}, lane, d.before, d.mine);
+  return d;
+}
+
+// The workgroup's tile `L`: along the columns first (few rows) or by
+// tile_order.  `offsets`: the experts', or a copy of them.
 template <int TM, int TN>
-__device__ __forceinline__ bool find_place4(const Mx4Args& p, int lane, int L, bool along, Place4& t) {
+__device__ __forceinline__ bool find_place4(const Mx4Args& p, const int32_t* offsets, const Deal4& d, int L, bool along,
+                                            Place4& t) {
   const int tiles_n = (p.N + TN - 1) / TN;
-  int tm, tn, total;
-  uint32_t before = 0, mine = 0;
-  const int per = int((p.T + TM - 1) / TM);
-  if (p.offsets != nullptr) total = tiles_total(Segments<TM>{p.offsets, p.E, p.cap}, lane, before, mine);
-  else total = per * p.E;
-  if (unsigned(L) >= unsigned(total) * unsigned(tiles_n)) return false;
+  int tm, tn;
+  if (unsigned(L) >= unsigned(d.total) * unsigned(tiles_n)) return false;
   if (along) {
     tm = L / tiles_n;
     tn = L - tm * tiles_n;
   } else {
-    tile_order(L, total, tiles_n, tm, tn);
+    tile_order(L, d.total, tiles_n, tm, tn);
   }
   if (p.offsets != nullptr) {
-    const Segment s = find_tile(Segments<TM>{p.offsets, p.E, p.cap}, tm, before, mine);
+    const Segment s = find_tile(Segments<TM>{offsets, p.E, p.cap}, tm, d.before, d.mine);
     t.none = s.e >= p.E || p.T == 0;
     t.e = s.e < p.E ? s.e : 0;
     t.m0 = s.row0;
     t.m_end = s.end;
   } else {
+    const int per = int((p.T + TM - 1) / TM);
     t.none = false;
     t.e = tm / per;
     t.m0 = (tm - t.e * per) * TM;
@@ -100,14 +110,14 @@ __device__ __forceinline__ bool find_place4(const Mx4Args& p, int lane, int L, b
   return true;
 }
 
-// The row of A of a tile's row r, -1 for none.
-__device__ __forceinline__ int source4(const Mx4Args& p, const Place4& t, int r) {
+// The row of A of a tile's row r, -1 for none: the choice at the row, and the
+// row of it.
+__device__ __forceinline__ int choice4(const Mx4Args& p, const Place4& t, int r) {
   if (!row_in(t.m0, r, t.m_end) || t.none) return -1;
-  int f = t.m0 + r;
-  if (p.rows != nullptr) {
-    f = p.rows[f];
-    if (f >= 0) f /= p.k;
-  }
+  return p.rows != nullptr ? p.rows[t.m0 + r] : t.m0 + r;
+}
+__device__ __forceinline__ int source4(const Mx4Args& p, int choice) {
+  const int f = p.rows != nullptr && choice >= 0 ? choice / p.k : choice;
   return f >= p.T ? -1 : f;
 }
 
@@ -145,13 +155,13 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
   const int w = scalar(tid >> 6);
   const View4<FA> view{p};
   Place4 t;
-  if (!find_place4<TM, TN>(p, lane, p.first + int(blockIdx.x), true, t)) return;
+  if (!find_place4<TM, TN>(p, p.offsets, deal4<TM>(p, p.offsets, lane), p.first + int(blockIdx.x), true, t)) return;
   const int g = lane >> 4, r16 = lane & 15;
   const int nb = t.none ? 0 : p.K / 32;
   const uint8_t *pa[MB], *psa[MB], *pb[NB], *psb[NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    const int s = source4(p, t, 16 * i + r16), row = s < 0 ? 0 : s;
+    const int s = source4(p, choice4(p, t, 16 * i + r16)), row = s < 0 ? 0 : s;
     if (w == 0 && g == 0) src[16 * i + r16] = s;
     pa[i] = view.a(t.e) + row * view.pitch_a();
     psa[i] = view.sa(t.e) + row * view.pitch_s();
@@ -271,8 +281,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
   const int w = scalar(tid >> 6);
   const View4<FA> view{p};
   Place4 t;
-  if (!find_place4<TM, TN>(p, lane, p.first + int(blockIdx.x), false, t)) return;
-  for (int r = tid; r < TM; r += 64 * NW) src[r] = source4(p, t, r);
+  if (!find_place4<TM, TN>(p, p.offsets, deal4<TM>(p, p.offsets, lane), p.first + int(blockIdx.x), false, t)) return;
+  for (int r = tid; r < TM; r += 64 * NW) src[r] = source4(p, choice4(p, t, r));
   __syncthreads();
   const int nk = t.none ? 0 : (p.K + kStep - 1) / kStep;
 
@@ -493,28 +503,52 @@ __device__ __forceinline__ uint4 turned(uint4 v, int n, int skip) {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 
+constexpr int kMaxEnds = 1025;  // of the experts' segments
+
 // acc += b x a in inline asm, for its place among the loads and reads (the
-// compiler moves the builtin past all of them) and for accumulation registers;
-// two wait states first, which an operand that a vector instruction wrote
-// needs.  HH: the byte (0 or 1) of both scale words.
+// compiler moves the builtin past all of them) and for accumulation registers.
+// HH: the byte of both scale words.  Its operands come from LDS reads, which
+// the compiler waits for; the scale words may come from vector instructions,
+// two wait states after which are the caller's.  Back to back on one
+// accumulator needs none.
+#define BSQ_MFMA4(SEL, FMT) "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4" FMT
+#define BSQ_MFMA4_FA(SEL, ...)                                   \
+  do {                                                           \
+    if constexpr (FA == 4) __VA_ARGS__(BSQ_MFMA4(SEL, " blgp:4"), a_lo); \
+    else if constexpr (FA == 1) __VA_ARGS__(BSQ_MFMA4(SEL, " blgp:1"), a); \
+    else __VA_ARGS__(BSQ_MFMA4(SEL, ""), a);                     \
+  } while (0)
+#define BSQ_MFMA4_HH(...)                                                                  \
+  do {                                                                                     \
+    if constexpr (HH == 0) BSQ_MFMA4_FA("op_sel_hi:[0,0,0]", __VA_ARGS__);                 \
+    else if constexpr (HH == 1) BSQ_MFMA4_FA("op_sel:[1,1,0] op_sel_hi:[0,0,0]", __VA_ARGS__); \
+    else if constexpr (HH == 2) BSQ_MFMA4_FA("op_sel_hi:[1,1,0]", __VA_ARGS__);            \
+    else BSQ_MFMA4_FA("op_sel:[1,1,0] op_sel_hi:[1,1,0]", __VA_ARGS__);                    \
+  } while (0)
 template <int FA, int HH>
 __device__ __forceinline__ void mfma_at(v4f& acc, v4i b, const v8i& a, int sb, int sa) {
-  const v4i lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
-#define BSQ_MFMA(SEL, FMT, A)                                                                          \
-  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4" FMT \
-               : "+a"(acc)                                                                             \
-               : "v"(b), "v"(A), "v"(sb), "v"(sa))
-#define BSQ_MFMA_HH(FMT, A)                                                              \
-  do {                                                                                   \
-    if constexpr (HH == 0) BSQ_MFMA("op_sel_hi:[0,0,0]", FMT, A);                        \
-    else BSQ_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]", FMT, A);                           \
-  } while (0)
-  if constexpr (FA == 4) BSQ_MFMA_HH(" blgp:4", lo);
-  else if constexpr (FA == 1) BSQ_MFMA_HH(" blgp:1", a);
-  else BSQ_MFMA_HH("", a);
-#undef BSQ_MFMA_HH
-#undef BSQ_MFMA
+  const v4i a_lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+#define BSQ_PLAIN(TEXT, A) asm volatile(TEXT : "+a"(acc) : "v"(b), "v"(A), "v"(sb), "v"(sa))
+  BSQ_MFMA4_HH(BSQ_PLAIN);
+#undef BSQ_PLAIN
 }
+// The same, and a load of 16 bytes per lane into LDS behind it (see dma16): the
+// MFMA is the wait state between m0 and the load.
+template <int FA, int HH>
+__device__ __forceinline__ void mfma_at(v4f& acc, v4i b, const v8i& a, int sb, int sa, const uint8_t* base, uint32_t off,
+                                        uint32_t lds, int at) {
+  const v4i a_lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+#define BSQ_LOADS(TEXT, A)                                                                           \
+  asm volatile("s_add_u32 m0, %5, %8\n\t" TEXT "\n\tglobal_load_lds_dwordx4 %6, %7"                 \
+               : "+a"(acc)                                                                           \
+               : "v"(b), "v"(A), "v"(sb), "v"(sa), "s"(lds), "v"(off), "s"(base), "i"(at)            \
+               : "memory", "scc")
+  BSQ_MFMA4_HH(BSQ_LOADS);
+#undef BSQ_LOADS
+}
+#undef BSQ_MFMA4_HH
+#undef BSQ_MFMA4_FA
+#undef BSQ_MFMA4
 
 template <int FA, int OUT_BF16>
 __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
@@ -525,6 +559,9 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t lds_s[2 * (TM + TN) * 16];
   __shared__ int src[2][TM];
+  __shared__ int32_t ends[kMaxEnds];
+  // stores of a whole tile by a wave; what vmcnt can count of them
+  constexpr int kStores = OUT_BF16 ? 32 : 63;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = scalar(tid >> 6);
@@ -545,17 +582,14 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
   const bool past_b = part && int64_t(all - 1) * BB + cb >= view.pitch_b();
   const uint8_t *pa, *pb;
   uint32_t off[8 + LB];
-  uint32_t back_a = 0, back_b = 0;  // of the step that is loaded
   const uint32_t lbase = lds_of(lds + 1024 * w);
   uint32_t to = lbase;  // stage that is loaded
-  auto last_step = [&](bool yes) {
-    back_a = yes && past_a ? uint32_t(ca) : 0u;
-    back_b = yes && past_b ? uint32_t(cb) : 0u;
+  auto last_step = [&] {  // before the loads of a tile's last step
+#pragma unroll
+    for (int s = 0; s < 8 + LB; ++s) off[s] -= s < 8 ? (past_a ? uint32_t(ca) : 0u) : (past_b ? uint32_t(cb) : 0u);
   };
-  auto load = [&](int s, uint32_t to) {
-    const int at = s < 8 ? 1024 * NW * s : TM * BA + 1024 * NW * (s - 8);
-    dma16(s < 8 ? pa : pb, off[s] - (s < 8 ? back_a : back_b), to, at);
-  };
+  auto place = [&](int s) { return s < 8 ? 1024 * NW * s : TM * BA + 1024 * NW * (s - 8); };  // in the stage
+  auto load = [&](int s, uint32_t to) { dma16(s < 8 ? pa : pb, off[s], to, place(s)); };
   auto loaded = [&] {  // a whole step
     pa += BA;
     pb += BB;
@@ -608,18 +642,16 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
     to = lbase;
     load_scales(0);
   };
-  // Quarter q of the loads of a tile's first two steps.
-  auto preload = [&](int nk, int q) {
-    if (nk <= q / 2) return;
-    const uint32_t stage = uint32_t(scalar(int(lbase + (q < 2 ? 0 : kStage))));
-    last_step(part && q / 2 == nk - 1);
-    if (q & 1) {
+  // The loads of a tile's first two steps.
+  auto preload = [&](int nk) {
 #pragma unroll
-      for (int s = 0; s < LB; ++s) load(8 + s, stage);
+    for (int q = 0; q < 2; ++q) {
+      if (nk <= q) return;
+      const uint32_t stage = uint32_t(scalar(int(lbase + (q ? kStage : 0))));
+      if (part && q == nk - 1) last_step();
+#pragma unroll
+      for (int s = 0; s < 8 + LB; ++s) load(s, stage);
       loaded();
-    } else {
-#pragma unroll
-      for (int s = 0; s < 8; ++s) load(s, stage);
     }
   };
 
@@ -668,59 +700,74 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
       for (int i = 0; i < 8; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
   };
   // The MFMAs of the halves j0 of B and i0 of A, column by column, two blocks
-  // at a time; `beside(x)` comes between the first of them.
-  auto phase = [&](int j0, int i0, auto&& beside) {
+  // at a time.  P: which bytes of the scale words; the first MFMA of the x-th
+  // two brings load `first` + x where there is one before `end`; `beside(x)`
+  // comes after it.
+  uint32_t fill = lbase;  // stage that the loads go to
+  auto phase = [&](int j0, int i0, auto at, int first, int end, auto&& beside) {
+    constexpr int H = kHalves * decltype(at)::value;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const int j = j0 + x / 2, i = i0 + 2 * (x & 1);
-      mfma_at<FA, 0>(acc[j][i], fb[j][0], fa[i], qb[j], qa[i]);
+      const int j = j0 + x / 2, i = i0 + 2 * (x & 1), s = first + x;
+      if (s < end)
+        mfma_at<FA, H>(acc[j][i], fb[j][0], fa[i], qb[j], qa[i], s < 8 ? pa : pb, off[s], fill, place(s));
+      else
+        mfma_at<FA, H>(acc[j][i], fb[j][0], fa[i], qb[j], qa[i]);
       beside(x);
-      mfma_at<FA, 0>(acc[j][i + 1], fb[j][0], fa[i + 1], qb[j], qa[i + 1]);
+      mfma_at<FA, H>(acc[j][i + 1], fb[j][0], fa[i + 1], qb[j], qa[i + 1]);
       if constexpr (kHalves == 2) {
-        v8i a0 = __builtin_shufflevector(fa[i], fa[i], 4, 5, 6, 7, 4, 5, 6, 7);
-        v8i a1 = __builtin_shufflevector(fa[i + 1], fa[i + 1], 4, 5, 6, 7, 4, 5, 6, 7);
-        mfma_at<FA, 1>(acc[j][i], fb[j][kHalves - 1], a0, qb[j], qa[i]);
-        mfma_at<FA, 1>(acc[j][i + 1], fb[j][kHalves - 1], a1, qb[j], qa[i + 1]);
+        const v8i a0 = __builtin_shufflevector(fa[i], fa[i], 4, 5, 6, 7, 4, 5, 6, 7);
+        const v8i a1 = __builtin_shufflevector(fa[i + 1], fa[i + 1], 4, 5, 6, 7, 4, 5, 6, 7);
+        mfma_at<FA, H + 1>(acc[j][i], fb[j][kHalves - 1], a0, qb[j], qa[i]);
+        mfma_at<FA, H + 1>(acc[j][i + 1], fb[j][kHalves - 1], a1, qb[j], qa[i + 1]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Step ks; LOADS: the step after next follows it, and is loaded.
-  auto step = [&](int ks, int nk, auto loads) {
+  bool stored = false;  // the last tile's stores may still be under way
+  // Step ks.  LOADS: the step after next follows it, and is loaded.  TURN: what
+  // becomes of the scale words for the next step.  0: they stay, and its bytes
+  // are the next (4 bits: the first step of a group); 1: another group's are
+  // read; 2: its group's are read and shifted.  P: the bytes of this step.
+  auto step = [&](int ks, int nk, auto loads, auto turn, auto at) {
     constexpr bool LOADS = decltype(loads)::value;
-    const int q = (ks + 1) / kGroup, at = (ks + 1) % kGroup;  // of the next step
-    phase(0, 0, [&](int x) {
+    constexpr int TURN = decltype(turn)::value;
+    const int q = (ks + 1) / kGroup, next_at = (ks + 1) % kGroup;  // of the next step
+    constexpr int kEnd = LOADS ? 8 + LB : 0;
+    phase(0, 0, at, 0, 0, [&](int x) {
       if (x % 2 < kHalves) b_part(4 + x / 2, x & 1);
     });
-    phase(4, 0, [&](int x) { a_part(4 + x / 2, x & 1); });
-    __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    phase(4, 0, at, 0, 0, [&](int x) { a_part(4 + x / 2, x & 1); });
+    if (ks == 0 && stored) __builtin_amdgcn_s_waitcnt(vmcnt(kStores));
+    else __builtin_amdgcn_s_waitcnt(vmcnt(0));
     if (part && ks + 1 == nk - 1) blank(o ^ kStage);
-    if (at == 0 && ks + 1 < nk) put_scales(q);
+    if (TURN && next_at == 0 && ks + 1 < nk) put_scales(q);
     barrier();
-    if (LOADS && at == kGroup - 1) load_scales(q + 1);
+    if (LOADS && TURN != 1 && next_at == kGroup - 1) load_scales(q + 1);
     o ^= kStage;
-    const uint32_t fill = uint32_t(scalar(int(to)));
-    if (LOADS) last_step(part && ks + 2 == nk - 1);
+    fill = uint32_t(scalar(int(to)));
+    if (LOADS && part && ks + 2 == nk - 1) last_step();
     int next[16];  // scales of the next step
-    phase(4, 4, [&](int x) {
+    phase(4, 4, at, 0, kEnd < 8 ? kEnd : 8, [&](int x) {
       a_part(x / 2, x & 1);
-      next[x] = scale_a(q, x);
-      if (LOADS) load(x, fill);
+      if (TURN) next[x] = scale_a(q, x);
     });
     // fragment f of B0 is free after its last MFMA
-    phase(0, 4, [&](int x) {
+    phase(0, 4, at, 8, kEnd, [&](int x) {
       if (x >= 2 && x % 2 < kHalves) b_part(x / 2 - 1, x & 1);
-      next[8 + x] = scale_b(q, x);
-      if (LOADS && x < LB) load(8 + x, fill);
+      if (TURN) next[8 + x] = scale_b(q, x);
     });
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) b_part(3, h);
     // in inline asm, so that they stay behind the MFMAs
-    const int bits = 8 * kHalves * at;
+    if constexpr (TURN) {
+      const int bits = TURN == 1 ? 0 : 8 * kHalves * next_at;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      asm volatile("v_lshrrev_b32 %0, %2, %1" : "=v"(qa[i]) : "v"(next[i]), "s"(bits));
-      asm volatile("v_lshrrev_b32 %0, %2, %1" : "=v"(qb[i]) : "v"(next[8 + i]), "s"(bits));
+      for (int i = 0; i < 8; ++i) {
+        asm volatile("v_lshrrev_b32 %0, %2, %1" : "=v"(qa[i]) : "v"(next[i]), "s"(bits));
+        asm volatile("v_lshrrev_b32 %0, %2, %1" : "=v"(qb[i]) : "v"(next[8 + i]), "s"(bits));
+      }
+      asm volatile("s_nop 1");
     }
     if (LOADS) loaded();
   };
@@ -729,7 +776,8 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
   // of 16 lanes change places until it has columns 8 g .. 8 g + 7 of the 32;
   // then neighbouring rows trade one pair of blocks each, so that a store
   // writes whole 128-byte lines.
-  auto output = [&](const Place4& t, int buf, auto&& beside) {
+  auto output = [&](const Place4& t, int buf, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;  // every row and column is there
     constexpr int kElem = OUT_BF16 ? 2 : 4;
     const int64_t pitch = int64_t(p.N) * kElem;
     const int n0 = t.n0 + 128 * wn, left = p.N - n0;  // columns of the wave
@@ -739,7 +787,6 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
     at += r16 * pitch + 16 * g;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      beside(i);
       const int tr = 128 * wm + 16 * i + r16;
       const bool none = src[buf][tr] < 0, in = row_in(t.m0, tr, t.m_end);
       if constexpr (OUT_BF16) {
@@ -767,10 +814,10 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
             even_row[d] = odd ? got : v[0][d];
             odd_row[d] = odd ? v[1][d] : got;
           }
-          if (64 * q + (odd ? 32 : 0) + 8 * g < left) {
+          if (kWhole || 64 * q + (odd ? 32 : 0) + 8 * g < left) {
             uint8_t* const to = pair + 16 * i * pitch + 128 * q;
-            if (even_in) __builtin_nontemporal_store(even_row, reinterpret_cast<u32x4_t*>(to));
-            if (odd_in) __builtin_nontemporal_store(odd_row, reinterpret_cast<u32x4_t*>(to + pitch));
+            if (kWhole || even_in) __builtin_nontemporal_store(even_row, reinterpret_cast<u32x4_t*>(to));
+            if (kWhole || odd_in) __builtin_nontemporal_store(odd_row, reinterpret_cast<u32x4_t*>(to + pitch));
           }
         }
       } else {
@@ -783,7 +830,7 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
             asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(acc[j][i][d]));
             v[d] = none ? 0.f : x;
           }
-          if (in && 16 * j + 4 * g < left)
+          if (kWhole || (in && 16 * j + 4 * g < left))
             __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(at + 16 * i * pitch + 64 * j));
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -792,24 +839,37 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
     }
   };
 
+  // The wait for a tile's first step, whose loads were followed by `kept` stores
+  // at least.
+  auto arrive = [&](int nk, int kept) {
+    if (nk > 0) put_scales(0);
+    if (kept) __builtin_amdgcn_s_waitcnt(vmcnt(kStores));
+    else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    if (part && nk == 1) blank(0);
+  };
+
+  const Deal4 deal = deal4<TM>(p, p.offsets, lane);
+  if (p.offsets != nullptr) {
+    for (int i = tid; i <= p.E; i += 256) ends[i] = p.offsets[i];
+    __syncthreads();
+  }
   Place4 cur, next{};
   int L = blockIdx.x, buf = 0;
-  if (!find_place4<TM, TN>(p, lane, L, false, cur)) return;
-  src[0][tid] = source4(p, cur, tid);
+  if (!find_place4<TM, TN>(p, ends, deal, L, false, cur)) return;
+  src[0][tid] = source4(p, choice4(p, cur, tid));
   __syncthreads();
   begin(cur, 0);
   int nk = cur.none ? 0 : all;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) preload(nk, q);
+  preload(nk);
+  arrive(nk, 0);
   clear();
   for (;;) {
+    // the search for the next tile reads LDS only, and the load of its choices
+    // is not waited for here
     L += gridDim.x;
-    const bool more = find_place4<TM, TN>(p, lane, L, false, next);
-    const int row = more ? source4(p, next, tid) : -1;
-    if (nk > 0) put_scales(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt(0));
-    if (part && nk == 1) blank(0);
-    __syncthreads();
+    const bool more = find_place4<TM, TN>(p, ends, deal, L, false, next);
+    const int choice = more ? choice4(p, next, tid) : -1;
+    barrier();
     if (nk > 0) {
       o = 0;
 #pragma unroll
@@ -826,26 +886,43 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
       }
       settle();  // the zeros, before an MFMA adds to them
       asm volatile("s_nop 15");
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      constexpr std::integral_constant<int, 0> zero{};
+      constexpr std::integral_constant<int, 1> one{};
+      constexpr std::integral_constant<int, 2> two{};
       int ks = 0;
-      for (; ks < nk - 2; ++ks) step(ks, nk, std::true_type{});
-      for (; ks < nk; ++ks) step(ks, nk, std::false_type{});
+      if constexpr (kGroup == 2) {  // two steps to a group, whose words stay for both
+        for (; ks + 3 < nk; ks += 2) {
+          step(ks, nk, yes, zero, zero);
+          step(ks + 1, nk, yes, one, one);
+        }
+      }
+      for (; ks < nk - 2; ++ks) step(ks, nk, yes, two, zero);
+      for (; ks < nk; ++ks) step(ks, nk, no, two, zero);
       asm volatile("s_nop 15\n\ts_nop 15");  // the last MFMAs, before their results are read
       settle();
     }
     // the last step's barrier is past the last reads of both stages that count
     const Place4 done = cur;
-    cur = next;
     const int done_buf = buf;
+    cur = next;
     nk = more && !cur.none ? all : 0;
     if (more) {
       buf ^= 1;
-      src[buf][tid] = row;
-      __syncthreads();
+      src[buf][tid] = source4(p, choice);
+      barrier();
       begin(cur, buf);
+      preload(nk);
     }
-    output(done, done_buf, [&](int i) {
-      if (i < 4) preload(nk, i);
-    });
+    stored = row_in(done.m0, TM - 1, done.m_end) && done.n0 + TN <= p.N;
+    if (stored) {
+      output(done, done_buf, std::true_type{});
+      if (more) arrive(nk, kStores);
+    } else {
+      output(done, done_buf, std::false_type{});
+      if (more) arrive(nk, 0);
+    }
     if (!more) return;
     clear();
   }
