@@ -254,11 +254,18 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
 // of A (256 elements of 4 bits, 128 of 8) through a ring of S LDS stages filled
 // by direct loads.  A row's 16-byte chunks are XORed with half its number, so
 // that the 16 rows of a fragment read fall on all 64 banks; B's rows of 64
-// bytes (beside 8-bit A) lie two to a line.  Scales come as whole words: where
-// K is no multiple of 128 a row's bytes start inside one, and one word more is
-// read (AL 0).  A step waits for its own loads only.
-template <int FA, int WM, int WN, int MB, int NB, int S, int AL>
-__global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
+// bytes (beside 8-bit A) lie two to a line.  A step waits for its own loads only.
+//
+// Scales of a row come 16 blocks, a unit of 2 steps of 4 bits or 4 of 8, at a
+// time: a load of 64 rows' scales touches 64 lines however few bytes it takes
+// of each.  They come as whole words: where K is no multiple of 128 a row's
+// bytes start inside one, and one word more is read (AL 0).
+//
+// Where there are fewer tiles than CUs, KG groups of WM x WN waves share a
+// tile's units (group i has i, i + KG, ..), each with a ring of its own, and
+// their sums are joined through LDS in the groups' order.
+template <int FA, int WM, int WN, int MB, int NB, int S, int KG, int AL>
+__global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   constexpr int NW = WM * WN, TM = 16 * MB * WM, TN = 16 * NB * WN;
   constexpr int kStep = FA == 4 ? 256 : 128, kHalves = kStep / 128;
   constexpr int BA = 128, BB = kStep / 2;  // bytes of a row of a step
@@ -267,24 +274,33 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
   static_assert(TM % (8 * NW) == 0 && TN % (RB * NW) == 0 && NW % 2 == 0, "whole loads of every wave");
   constexpr int SM = (TM + 63) / 64 * 64, SR = SM + TN;  // rows of scales
   static_assert(TN % 64 == 0, "scale rows by the 64");
-  constexpr int D = kHalves + (AL ? 0 : 1);       // words of a row's scales
-  constexpr int LS = (SR / 64 * D + NW - 1) / NW;  // loads of them per wave
+  constexpr int kUnit = 512 / kStep;  // steps of 16 blocks
+  static_assert(SR / 64 <= NW, "a wave has 64 rows of scales or none");
+  static_assert(S <= 3 && S - 1 <= kUnit, "two units of scales, waits by one step ahead");
   constexpr int kStage = TM * BA + TN * BB;
   constexpr int kRowB = NB * 64 + 16;  // bytes of a staged output row of a wave, padded
   constexpr int kOut = NW * 16 * kRowB;
-  constexpr int kAB = S * kStage > kOut ? S * kStage : kOut;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kAB];
-  __shared__ __attribute__((aligned(16))) uint32_t lds_s[S][D][SR];
+  constexpr int kJoin = (KG - 1) * NW * MB * NB * 1024;  // the other groups' accumulators
+  constexpr int kMost = kOut > kJoin ? kOut : kJoin;
+  constexpr int kAB = KG * S * kStage > kMost ? KG * S * kStage : kMost;
+  __shared__ __attribute__((aligned(16))) uint8_t lds_ab[kAB];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_sc[KG][2][SR * (AL ? 16 : 20)];
   __shared__ int src[TM];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int w = scalar(tid >> 6);
+  const int w = scalar(tid >> 6) % NW, kg = scalar(tid >> 6) / NW;
+  uint8_t* const lds = lds_ab + kg * S * kStage;
+  uint8_t(*const lds_s)[SR * (AL ? 16 : 20)] = lds_sc[kg];
   const View4<FA> view{p};
   Place4 t;
   if (!find_place4<TM, TN>(p, p.offsets, deal4<TM>(p, p.offsets, lane), p.first + int(blockIdx.x), false, t)) return;
-  for (int r = tid; r < TM; r += 64 * NW) src[r] = source4(p, choice4(p, t, r));
+  for (int r = tid; r < TM; r += 64 * NW * KG) src[r] = source4(p, choice4(p, t, r));
   __syncthreads();
-  const int nk = t.none ? 0 : (p.K + kStep - 1) / kStep;
+  const int all = t.none ? 0 : (p.K + kStep - 1) / kStep;
+  // units of the tile and of the group, steps of the group
+  const int units = (all + kUnit - 1) / kUnit, mine = (units - kg + KG - 1) / KG;
+  const int nk = mine * kUnit - ((units - 1) % KG == kg ? units * kUnit - all : 0);
+  auto global = [&](int i) { return (KG * (i / kUnit) + kg) * kUnit + i % kUnit; };  // step of the group's i-th
 
   // ---- loads: lane i of a load of A fills row i / 8, chunk place i % 8
   const int lrow = lane >> 3, ca = 16 * ((lane & 7) ^ (4 * (w & 1) + (lrow >> 1)));
@@ -301,33 +317,32 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
     pb[s] = view.b(t.e) + int64_t(min(t.n0 + RB * (w + NW * s) + brow, p.N - 1)) * view.pitch_b() + cb;
   const uint32_t la = lds_of(lds + 1024 * w), lb = lds_of(lds + TM * BA + 1024 * w);
   // whether the last step has not got the lane's chunk
-  const int64_t last = int64_t(nk - 1) * BA, last_b = int64_t(nk - 1) * BB;
+  const int64_t last = int64_t(all - 1) * BA, last_b = int64_t(all - 1) * BB;
   const bool past_a = last + ca >= view.pitch_a(), past_b = last_b + cb >= view.pitch_b();
   const bool part = p.K % kStep != 0;
-  // scales: 64 rows of one word to a load
+  // scales: wave w has rows 64 w .. of A's and then B's
   const int64_t sp = view.pitch_s();
   const uint64_t sa0 = reinterpret_cast<uint64_t>(view.sa(t.e));
   const int bm = int(sa0 & 3);  // a batch's scales need not start a word
-  const i32x4 rsa = rsrc(reinterpret_cast<const uint8_t*>(sa0 - bm), (bm + p.T * sp + 3) & ~int64_t(3));
-  const i32x4 rsb = rsrc(view.sb(t.e), p.N * sp);
   auto a_row = [&](int r) { return max(src[r], 0); };
   auto b_row = [&](int r) { return min(t.n0 + r, p.N - 1); };
-  uint32_t so[LS], ls[LS];
-  bool sA[LS];
-#pragma unroll
-  for (int q = 0; q < LS; ++q) {
-    const int item = (w + NW * q) % (SR / 64 * D), grp = item / D, d = item % D;
-    const int r = 64 * grp + lane;
-    sA[q] = 64 * grp < SM;
-    const uint32_t byte = sA[q] ? uint32_t(bm + a_row(min(r, TM - 1)) * sp) : uint32_t(b_row(r - SM) * sp);
-    so[q] = (byte & ~3u) + 4u * uint32_t(d);
-    ls[q] = lds_of(reinterpret_cast<const uint8_t*>(&lds_s[0][d][64 * grp]));
-  }
-  constexpr int kLoads = LA + LB + LS;
+  const bool has = w < SR / 64;
+  const int srow = 64 * w + lane;
+  const i32x4 rs = w < SM / 64 ? rsrc(reinterpret_cast<const uint8_t*>(sa0 - bm), (bm + p.T * sp + 3) & ~int64_t(3))
+                               : rsrc(view.sb(t.e), p.N * sp);
+  const uint32_t so = (srow < SM ? uint32_t(bm + a_row(min(srow, TM - 1)) * sp) : uint32_t(b_row(srow - SM) * sp)) & ~3u;
+  const uint32_t ls = lds_of(&lds_s[0][64 * w * 16]), ls4 = lds_of(&lds_s[0][SR * 16 + 64 * w * 4]);
+  constexpr int kLoads = LA + LB, kScales = AL ? 1 : 2;  // of a step, of a unit
   const uint8_t* const zeros = kZeros;
-  auto load = [&](int ks, int st) {
+  auto load = [&](int i, int st) {  // the group's i-th step
+    const int ks = global(i);
     const uint32_t at = uint32_t(st * kStage);
-    if (part && ks == nk - 1) {
+    if (has && i % kUnit == 0) {
+      const uint32_t from = so + 16u * uint32_t(ks / kUnit), to = uint32_t((i / kUnit & 1) * SR * (AL ? 16 : 20));
+      dma16(rs, from, ls + to);
+      if (!AL) dma4(rs, from + 16u, ls4 + to);
+    }
+    if (part && ks == all - 1) {
 #pragma unroll
       for (int s = 0; s < LA; ++s) dma16(past_a ? zeros : pa[s] + last, la + at + uint32_t(1024 * NW * s));
 #pragma unroll
@@ -338,59 +353,73 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
 #pragma unroll
       for (int s = 0; s < LB; ++s) dma16(pb[s] + int64_t(ks) * BB, lb + at + uint32_t(1024 * NW * s));
     }
-#pragma unroll
-    for (int q = 0; q < LS; ++q)
-      dma4(sA[q] ? rsa : rsb, so[q] + uint32_t(kStep / 32) * uint32_t(ks), ls[q] + uint32_t(st * D * SR * 4));
   };
 
   const int wm = w % WM, wn = w / WM, g = lane >> 4, r16 = lane & 15;
   const int x8 = r16 >> 1;  // what a row's chunks are XORed with
-  // where a lane's scale bytes start inside the first word of its rows
-  int ma[MB], mb = 0;
+  // the byte of a unit's scales that the lane's block of the first MFMA has
+  int ma[MB], mb = g;
 #pragma unroll
-  for (int i = 0; i < MB; ++i) ma[i] = AL ? 0 : int((unsigned(bm) + unsigned(a_row(16 * MB * wm + 16 * i + r16)) * unsigned(sp)) & 3u);
-  if (!AL) mb = int((unsigned(b_row(16 * NB * wn + r16)) * unsigned(sp)) & 3u);
+  for (int i = 0; i < MB; ++i)
+    ma[i] = g + (AL ? 0 : int((unsigned(bm) + unsigned(a_row(16 * MB * wm + 16 * i + r16)) * unsigned(sp)) & 3u));
+  if (!AL) mb += int((unsigned(b_row(16 * NB * wn + r16)) * unsigned(sp)) & 3u);
   v4f acc[NB][MB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  for (int ks = 0; ks < min(nk, S - 1); ++ks) load(ks, ks);
+  for (int i = 0; i < min(nk, S - 1); ++i) load(i, i);
 
   int st = 0;
-  for (int ks = 0; ks < nk; ++ks) {
-    // S - 2 steps stay under way; near the end, where fewer are, all are waited for
-    if (ks + S - 2 < nk) __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads));
-    else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+  uint32_t qa[4][MB], qb[4][NB];  // scales of the unit's MFMAs, in the low byte
+  // One step, the `at`-th of unit u.
+  auto step = [&](int u, int at) {
+    const int i = u * kUnit + at;
+    // S - 2 steps (and what scales come with them) stay under way; near the end,
+    // where fewer are, all are waited for
+    if (i + S - 2 >= nk) __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    else if (S > 2 && has && at == kUnit - 1) __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads + kScales));
+    else __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads));
     barrier();
+    if (i >= nk) return;  // other groups' steps
     // past the barrier nobody reads the stage before this one
-    if (ks + S - 1 < nk) load(ks + S - 1, st == 0 ? S - 1 : st - 1);
+    if (i + S - 1 < nk) load(i + S - 1, st == 0 ? S - 1 : st - 1);
     const uint8_t* ta = lds + st * kStage;
     const uint8_t* tb = ta + TM * BA;
-    const uint32_t(*ss)[SR] = lds_s[st];
-    auto scale = [&](int row, int mis, int block) -> int {  // byte `block` of a row's scales of the step
-      if (AL) return int((ss[block >> 2][row] >> (8 * (block & 3))) & 0xFFu);
-      const int byte = mis + block;
-      return reinterpret_cast<const uint8_t*>(&ss[byte >> 2][row])[byte & 3];
-    };
-    int qa[kHalves][MB], qb[kHalves][NB];
+    if (at == 0) {
+      const uint8_t* const ss = lds_s[u & 1];
+      auto scales = [&](int row, int byte, uint32_t (&q)[4]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(ss + 16 * row);
+        uint32_t x[5] = {v.x, v.y, v.z, v.w, 0u};
+        if (!AL) x[4] = *reinterpret_cast<const uint32_t*>(ss + 16 * SR + 4 * row);
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
+        for (int d = 0; d < 4; ++d) q[d] = (!AL && byte >= 4 ? x[d + 1] : x[d]) >> (8 * (byte & 3));
+      };
 #pragma unroll
-      for (int i = 0; i < MB; ++i) qa[h][i] = scale(16 * MB * wm + 16 * i + r16, ma[i], 4 * h + g);
+      for (int i = 0; i < MB; ++i) {
+        uint32_t q[4];
+        scales(16 * MB * wm + 16 * i + r16, ma[i], q);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) qb[h][j] = scale(SM + 16 * NB * wn + 16 * j + r16, mb, 4 * h + g);
-    }
-    if (part && ks == nk - 1) {
-      const int left = p.K / 32 - ks * (kStep / 32);
+        for (int d = 0; d < 4; ++d) qa[d][i] = q[d];
+      }
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const bool past = 4 * h + g >= left;
+      for (int j = 0; j < NB; ++j) {
+        uint32_t q[4];
+        scales(SM + 16 * NB * wn + 16 * j + r16, mb, q);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) qa[h][i] = past ? 127 : qa[h][i];
+        for (int d = 0; d < 4; ++d) qb[d][j] = q[d];
+      }
+      const int left = p.K / 32 - (KG * u + kg) * 16;  // blocks from the unit on
+      if (left < 16) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) qb[h][j] = past ? 127 : qb[h][j];
+        for (int d = 0; d < 4; ++d) {
+          const bool past = 4 * d + g >= left;
+#pragma unroll
+          for (int i = 0; i < MB; ++i) qa[d][i] = past ? 127u : qa[d][i];
+#pragma unroll
+          for (int j = 0; j < NB; ++j) qb[d][j] = past ? 127u : qb[d][j];
+        }
       }
     }
     auto chunk = [&](const uint8_t* tile, int row, int c) {  // of a 128-byte row
@@ -414,23 +443,51 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) k_mx4_tile(Mx4Args p) {
       for (int j = 0; j < NB; ++j) {
         const v8i fb = bfrag(h, j);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) acc[j][i] = mfma4<FA>(fb, fa[i], acc[j][i], qb[h][j], qa[h][i]);
+        for (int i = 0; i < MB; ++i)
+          acc[j][i] = mfma4<FA>(fb, fa[i], acc[j][i], int(qb[kHalves * at + h][j]), int(qa[kHalves * at + h][i]));
       }
     }
     st = st == S - 1 ? 0 : st + 1;
+  };
+  for (int u = 0; u < (units + KG - 1) / KG; ++u) {
+#pragma unroll
+    for (int at = 0; at < kUnit; ++at) step(u, at);
+  }
+
+  if constexpr (KG > 1) {
+    v4f* const join = reinterpret_cast<v4f*>(lds_ab) + 64 * MB * NB * w + lane;
+    __syncthreads();
+    if (kg > 0) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) join[64 * MB * NB * NW * (kg - 1) + 64 * (MB * j + i)] = acc[j][i];
+    }
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int o = 0; o < KG - 1; ++o)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int i = 0; i < MB; ++i) acc[j][i] += join[64 * MB * NB * NW * o + 64 * (MB * j + i)];
+    }
   }
 
   // ---- out: 16 rows of the wave at a time through LDS, so that a store
   // instruction writes whole rows of the wave's columns
-  uint8_t* const stg = lds + w * 16 * kRowB;
+  uint8_t* const stg = lds_ab + w * 16 * kRowB;
   constexpr int LPR = 4 * NB, RPI = 64 / LPR;
   static_assert(64 % LPR == 0, "whole rows per instruction");
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     __syncthreads();
+    if (kg == 0) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) *reinterpret_cast<v4f*>(stg + r16 * kRowB + (16 * j + 4 * g) * 4) = acc[j][i];
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<v4f*>(stg + r16 * kRowB + (16 * j + 4 * g) * 4) = acc[j][i];
+    }
     __syncthreads();
+    if (kg > 0) continue;
 #pragma unroll
     for (int q = 0; q < 16 / RPI; ++q) {
       const int rr = RPI * q + lane / LPR, cc = 4 * (lane % LPR);
@@ -951,15 +1008,15 @@ bsq_status launch_few(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   });
 }
 
-template <int WM, int WN, int MB, int NB, int S>
+template <int WM, int WN, int MB, int NB, int S, int KG>
 bsq_status launch_tile(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   return in_parts(tile_rows(L, 16 * MB * WM) * up_to(L.N, 16 * NB * WN), kLaunchGroups, [&](int64_t first, int64_t n) {
     a.first = int(first);
     return with_code(L.a, [&](auto fa) {
       constexpr int FA = decltype(fa)::value;
-      const dim3 g = dim3(unsigned(n)), b = dim3(64 * WM * WN);
-      if (L.K % 128 == 0) hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, 1>), g, b, 0, st, a);
-      else hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, 0>), g, b, 0, st, a);
+      const dim3 g = dim3(unsigned(n)), b = dim3(64 * WM * WN * KG);
+      if (L.K % 128 == 0) hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, 1>), g, b, 0, st, a);
+      else hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, 0>), g, b, 0, st, a);
       return launch_status("mx4 product");
     });
   });
@@ -988,7 +1045,7 @@ bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
   const int64_t pitch_a = L.a == Code4::e2m1 ? L.K / 2 : L.K;
   const int64_t tiles = (L.offsets ? n / 256 + half : up_to(L.T, 256) * L.E) * up_to(L.N, 256);
   if (rows >= 160 && tiles >= 160 && (L.rows == nullptr || L.T * pitch_a < (int64_t(1) << 32))) return launch_big(L, a, st);
-  return launch_tile<2, 2, 2, 4, 2>(L, a, st);
+  return launch_tile<2, 2, 2, 4, 2, 1>(L, a, st);
 }
 
 }  // namespace bsq
