@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libbsq.so")
 SOURCES = ["api.hip", "api_moe.hip", "quant.hip", "gemm.hip", "route.hip", "rows.hip", "gate.hip", "moe_gemm.hip",
            "api_mx4.hip", "quant4.hip", "gemm4.hip", "norm.hip"]
 HEADERS = ["common.h", "fp4.h", "fp8.h", "lds.h", "quant.h", "quant4.h", "gemm.h", "gemm4.h", "moe.h",
-           "moe_index.h", "norm.h", "tiles.h"]
+           "moe_index.h", "mx4_index.h", "norm.h", "tiles.h"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -1,5 +1,4 @@
-// Launchers of the products with 4-bit weights (arguments already validated),
-// and which kernel a call takes.
+// Launcher of the products with 4-bit weights (arguments already validated).
 #pragma once
 
 #include "common.h"

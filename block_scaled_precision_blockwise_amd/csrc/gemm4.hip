@@ -20,6 +20,7 @@
 // gets in.
 #include "gemm4.h"
 #include "lds.h"
+#include "mx4_index.h"
 #include "tiles.h"
 
 #include <type_traits>
@@ -157,12 +158,13 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
   Place4 t;
   if (!find_place4<TM, TN>(p, p.offsets, deal4<TM>(p, p.offsets, lane), p.first + int(blockIdx.x), true, t)) return;
   const int g = lane >> 4, r16 = lane & 15;
-  const int nb = t.none ? 0 : p.K / 32;
+  bool any = false;
   const uint8_t *pa[MB], *psa[MB], *pb[NB], *psb[NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int s = source4(p, choice4(p, t, 16 * i + r16)), row = s < 0 ? 0 : s;
     if (w == 0 && g == 0) src[16 * i + r16] = s;
+    any |= s >= 0;
     pa[i] = view.a(t.e) + row * view.pitch_a();
     psa[i] = view.sa(t.e) + row * view.pitch_s();
   }
@@ -172,58 +174,79 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
     pb[j] = view.b(t.e) + row * view.pitch_b();
     psb[j] = view.sb(t.e) + row * view.pitch_s();
   }
+  const int nb = __ballot(any) ? p.K / 32 : 0;  // a tile without a choice is zeros
   v4f acc[NB][MB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   for (int c0 = w * U; 4 * c0 < nb; c0 += W * U) {
     uint4 b[U][NB], a[U][MB][FA == 4 ? 1 : 2];
     int sb[U][NB], sa[U][MB];
+    const bool whole = 4 * (c0 + U) <= nb;
+    if (whole) {
+      // a row's 16 scales at once: a load touches a line per row however little
+      // it takes of it
+      auto scales = [&](const uint8_t* row) {
+        uint4 v;
+        __builtin_memcpy(&v, row + 4 * c0, 16);
+        return v;
+      };
+      uint4 vb[NB], va[MB];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // block of the lane's scale, and of its chunks; past the end the last one
-      const int at = 4 * (c0 + u) + g, k0 = min(at, nb - 1);
+      for (int j = 0; j < NB; ++j) vb[j] = scales(psb[j]);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        b[u][j] = *reinterpret_cast<const uint4*>(pb[j] + 16 * k0);
-        sb[u][j] = psb[j][k0];
+      for (int i = 0; i < MB; ++i) va[i] = scales(psa[i]);
+      auto spread = [&](const uint4& v, int u) {
+        return int((u == 0 ? v.x : u == 1 ? v.y : u == 2 ? v.z : v.w) >> (8 * g));
+      };
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) b[u][j] = *reinterpret_cast<const uint4*>(pb[j] + 16 * (4 * (c0 + u) + g));
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          if constexpr (FA == 4) {
+            a[u][i][0] = *reinterpret_cast<const uint4*>(pa[i] + 16 * (4 * (c0 + u) + g));
+          } else {
+            // 8 bits: 16 elements of block g / 2 and 16 of block 2 + g / 2
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              a[u][i][h] = *reinterpret_cast<const uint4*>(pa[i] + 16 * (8 * (c0 + u) + 4 * h + g));
+          }
+        }
       }
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        sa[u][i] = psa[i][k0];
-        if constexpr (FA == 4) {
-          a[u][i][0] = *reinterpret_cast<const uint4*>(pa[i] + 16 * k0);
-        } else {
-          // 8 bits: 16 elements of block g / 2 and 16 of block 2 + g / 2
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 8 * (c0 + u) + 4 * h + g;  // chunk of 16 elements
-            a[u][i][h] = *reinterpret_cast<const uint4*>(pa[i] + 16 * min(c, 2 * nb - 1));
+        for (int j = 0; j < NB; ++j) sb[u][j] = spread(vb[j], u);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) sa[u][i] = spread(va[i], u);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // past the end the last block's and chunk's, as zeros under scales of 1
+        const int at = 4 * (c0 + u) + g, k0 = min(at, nb - 1);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          b[u][j] = *reinterpret_cast<const uint4*>(pb[j] + 16 * k0);
+          sb[u][j] = at < nb ? psb[j][k0] : 127;
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          sa[u][i] = at < nb ? psa[i][k0] : 127;
+#pragma unroll
+          for (int h = 0; h < (FA == 4 ? 1 : 2); ++h) {
+            const int n = FA == 4 ? nb : 2 * nb, c = FA == 4 ? at : 8 * (c0 + u) + 4 * h + g;
+            const uint4 v = *reinterpret_cast<const uint4*>(pa[i] + 16 * min(c, n - 1));
+            a[u][i][h] = c < n ? v : make_uint4(0u, 0u, 0u, 0u);
           }
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = 4 * (c0 + u) + g;
-      if (4 * (c0 + u) + 4 > nb) {  // an end inside the chunk, or before it
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          if (at >= nb) sa[u][i] = 127;
-          if constexpr (FA == 4) {
-            if (at >= nb) a[u][i][0] = zero;
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (8 * (c0 + u) + 4 * h + g >= 2 * nb) a[u][i][h] = zero;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-          if (at >= nb) sb[u][j] = 127;
-      }
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -231,7 +254,6 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
           if constexpr (FA == 4) acc[j][i] = mfma4<FA>(wide(b[u][j]), wide(a[u][i][0]), acc[j][i], sb[u][j], sa[u][i]);
           else acc[j][i] = mfma4<FA>(wide(b[u][j]), wide(a[u][i][0], a[u][i][1]), acc[j][i], sb[u][j], sa[u][i]);
         }
-    }
   }
 #pragma unroll
   for (int i = 0; i < MB; ++i)
@@ -294,9 +316,13 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   const View4<FA> view{p};
   Place4 t;
   if (!find_place4<TM, TN>(p, p.offsets, deal4<TM>(p, p.offsets, lane), p.first + int(blockIdx.x), false, t)) return;
-  for (int r = tid; r < TM; r += 64 * NW * KG) src[r] = source4(p, choice4(p, t, r));
-  __syncthreads();
-  const int all = t.none ? 0 : (p.K + kStep - 1) / kStep;
+  int any = 0;
+  for (int r = tid; r < TM; r += 64 * NW * KG) {
+    src[r] = source4(p, choice4(p, t, r));
+    any |= src[r] >= 0;
+  }
+  // a tile without a choice is zeros (a plan's alignment leaves such tiles)
+  const int all = __syncthreads_or(any) ? (p.K + kStep - 1) / kStep : 0;
   // units of the tile and of the group, steps of the group
   const int units = (all + kUnit - 1) / kUnit, mine = (units - kg + KG - 1) / KG;
   const int nk = mine * kUnit - ((units - 1) % KG == kg ? units * kUnit - all : 0);
@@ -1039,13 +1065,22 @@ bsq_status launch_big(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
 bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
   const Mx4Args a{L.A, L.B, L.SA, L.SB, L.out, L.offsets, L.rows, L.T, L.cap, int(L.E), int(L.N), int(L.K), L.k,
                   L.out_bf16 ? 1 : 0, 0};
-  const int64_t rows = L.offsets ? (L.rows && L.T < L.cap / L.k ? L.T * L.k : L.cap) / L.E : L.T;
-  if (rows <= 16 && L.cap <= (1 << 20)) return launch_few<1, 2, 8>(L, a, st);
-  const int64_t n = L.offsets ? rows * L.E : L.T * L.E, half = L.offsets ? L.E / 2 : 0;
   const int64_t pitch_a = L.a == Code4::e2m1 ? L.K / 2 : L.K;
-  const int64_t tiles = (L.offsets ? n / 256 + half : up_to(L.T, 256) * L.E) * up_to(L.N, 256);
-  if (rows >= 160 && tiles >= 160 && (L.rows == nullptr || L.T * pitch_a < (int64_t(1) << 32))) return launch_big(L, a, st);
-  return launch_tile<2, 2, 2, 4, 2, 1>(L, a, st);
+  switch (mx4_tile(Mx4Size{L.offsets != nullptr, L.rows != nullptr, L.T, L.cap, L.E, L.k, L.N, L.K})) {
+    case Mx4Tile::few16x16: return launch_few<1, 1, 4>(L, a, st);
+    case Mx4Tile::few16x32: return launch_few<1, 2, 4>(L, a, st);
+    case Mx4Tile::few32x32: return launch_few<2, 2, 4>(L, a, st);
+    case Mx4Tile::t32x64: return launch_tile<1, 4, 2, 1, 3, 1>(L, a, st);
+    case Mx4Tile::t32x64g2: return launch_tile<1, 4, 2, 1, 3, 2>(L, a, st);
+    case Mx4Tile::t64x64g2: return launch_tile<2, 2, 2, 2, 3, 2>(L, a, st);
+    case Mx4Tile::t64x128g2: return launch_tile<2, 2, 2, 4, 3, 2>(L, a, st);
+    case Mx4Tile::t64x128: return launch_tile<2, 2, 2, 4, 2, 1>(L, a, st);
+    case Mx4Tile::t128x128: return launch_tile<4, 2, 2, 4, 2, 1>(L, a, st);
+    default:
+      // gathered rows are addressed with 32 bits
+      if (L.rows != nullptr && L.T * pitch_a >= (int64_t(1) << 32)) return launch_tile<4, 2, 2, 4, 2, 1>(L, a, st);
+      return launch_big(L, a, st);
+  }
 }
 
 }  // namespace bsq
