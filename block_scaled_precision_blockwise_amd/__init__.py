@@ -826,31 +826,45 @@ def bsq_swiglu_mx_backward(kept, kept_scales, dh, dgu, code_dtype: Optional[int]
 # ----------------------------------------------------- 4-bit operands ----
 
 _codes_of = None
+_tensor = None
+_device = None
 
 
 def _here(*ts):
     """The tensors are on the current device, whose stream and memory the call uses."""
-    _dev(*ts)
-    now = _torch()._C._cuda_getDevice()
+    global _tensor, _device
+    if _tensor is None:
+        torch = _torch()
+        _tensor, _device = torch.Tensor, torch._C._cuda_getDevice
+    now = None
     for t in ts:
-        if t is not None and t.get_device() != now:
+        if t is None:
+            continue
+        if type(t) is not _tensor or not t.is_cuda or not t.is_contiguous():
+            _dev(t)
+        if now is None:
+            now = _device()
+        if t.get_device() != now:
             raise ValueError(f"tensors must be on the current device ({now}), got one on {t.get_device()}")
+
+
+def _formats():
+    global _codes_of
+    torch = _torch()
+    _codes_of = {torch.uint8: BSQ_E2M1, torch.float8_e4m3fn: BSQ_E4M3, torch.float8_e5m2: BSQ_E5M2}
+    if hasattr(torch, "float4_e2m1fn_x2"):
+        _codes_of[torch.float4_e2m1fn_x2] = BSQ_E2M1
+    return _codes_of
 
 
 def _code(t, code_dtype, name):
     """The format of codes: `code_dtype`, or what the dtype says (bytes: E2M1)."""
-    global _codes_of
-    if _codes_of is None:
-        torch = _torch()
-        _codes_of = {torch.uint8: BSQ_E2M1, torch.float8_e4m3fn: BSQ_E4M3, torch.float8_e5m2: BSQ_E5M2}
-        if hasattr(torch, "float4_e2m1fn_x2"):
-            _codes_of[torch.float4_e2m1fn_x2] = BSQ_E2M1
-    said = _codes_of.get(t.dtype)
+    said = (_codes_of or _formats()).get(t.dtype)
     if said is None:
         raise TypeError(f"{name} must be bytes of codes, got {t.dtype}")
-    if code_dtype is None:
+    if code_dtype is None or code_dtype == said:
         return said
-    if t.dtype != _torch().uint8 and said != code_dtype:
+    if t.dtype != _torch().uint8:
         raise TypeError(f"{name} of {t.dtype} cannot hold codes of format {code_dtype}")
     return code_dtype
 
@@ -861,13 +875,16 @@ def _packed(codes, scales, shape, block, name, optional=False):
         return
     if codes is None or scales is None:
         raise ValueError(f"{name} needs both codes and scales")
-    if shape[-1] % block:
-        raise ValueError(f"{name}: {shape[-1]} values are no multiple of the block ({block})")
-    if _code(codes, None, name) != BSQ_E2M1:
+    lead, n = shape[:-1], shape[-1]
+    if n % block:
+        raise ValueError(f"{name}: {n} values are no multiple of the block ({block})")
+    if (_codes_of or _formats()).get(codes.dtype) != BSQ_E2M1:
         raise TypeError(f"{name} must hold packed e2m1 codes, got {codes.dtype}")
-    _bytes1(scales, name + " scales")
-    _expect(codes, codes.dtype, (*shape[:-1], shape[-1] // 2), name)
-    _expect(scales, scales.dtype, (*shape[:-1], shape[-1] // block), name + " scales")
+    _bytes1(scales, "scales")
+    if codes.shape != (*lead, n // 2):
+        _expect(codes, codes.dtype, (*lead, n // 2), name)
+    if scales.shape != (*lead, n // block):
+        _expect(scales, scales.dtype, (*lead, n // block), name + " scales")
 
 
 def bsq_quant_fp4(src, codes=None, scales=None, codes_t=None, scales_t=None, format: int = BSQ_MXFP4, factor=None,
@@ -880,8 +897,7 @@ def bsq_quant_fp4(src, codes=None, scales=None, codes_t=None, scales_t=None, for
     _here(src, codes, scales, codes_t, scales_t, factor)
     if src.dim() not in (2, 3):
         raise ValueError(f"src must have 2 or 3 dimensions, got shape {tuple(src.shape)}")
-    lead = tuple(src.shape[:-2])
-    rows, cols = src.shape[-2:]
+    *lead, rows, cols = src.shape
     sd = _wide(src, "src")
     if format not in (BSQ_MXFP4, BSQ_NVFP4):
         raise ValueError("format must be BSQ_MXFP4 or BSQ_NVFP4")
@@ -896,13 +912,12 @@ def bsq_quant_fp4(src, codes=None, scales=None, codes_t=None, scales_t=None, for
 
 def _left(a, a_scales, rank, K, a_dtype, name):
     """Checks the left operand of a product with 4-bit weights; its format."""
-    code = _code(a, a_dtype, name)
-    shape = (*a.shape[:-1], K)
     _rank(a, rank, name)
+    code = _code(a, a_dtype, name)
     if code == BSQ_E2M1:
-        _packed(a, a_scales, shape, 32, name)
+        _packed(a, a_scales, (*a.shape[:-1], K), 32, name)
     else:
-        _blocks(a, a_scales, shape, name)
+        _blocks(a, a_scales, (*a.shape[:-1], K), name)
     return code
 
 
@@ -912,15 +927,15 @@ def bsq_scaled_matmul_mxfp4(lhs, rhs, lhs_scales, rhs_scales, out, lhs_dtype: Op
     codes; E8M0 scales [B, M, K/32] and [B, N, K/32]."""
     _here(lhs, rhs, lhs_scales, rhs_scales, out)
     _rank(rhs, 3, "rhs")
-    _rank(out, 3, "out")
-    B, N = rhs.shape[:2]
-    K = 2 * rhs.shape[2]
+    B, N, K = rhs.shape
+    K *= 2
     ld = _left(lhs, lhs_scales, 3, K, lhs_dtype, "lhs")
     _packed(rhs, rhs_scales, (B, N, K), 32, "rhs")
     M = lhs.shape[1]
     if lhs.shape[0] != B:
         raise ValueError("lhs and rhs must share B")
-    _expect(out, out.dtype, (B, M, N), "out")
+    if out.shape != (B, M, N):
+        _expect(out, out.dtype, (B, M, N), "out")
     _raise(lib().bsq_scaled_matmul_mxfp4(B, M, N, K, _ptr(lhs), ld, _ptr(rhs), _ptr(lhs_scales), _ptr(rhs_scales),
                                          _ptr(out), _wide(out, "out"), _stream(stream)), "bsq_scaled_matmul_mxfp4")
 
@@ -935,8 +950,8 @@ def bsq_moe_matmul_mxfp4(a, a_scales, b, b_scales, offsets, out, rows=None, k: i
     _here(a, a_scales, b, b_scales, offsets, out, rows)
     _rank(b, 3, "b")
     _rank(out, 2, "out")
-    E, N = b.shape[:2]
-    K = 2 * b.shape[2]
+    E, N, K = b.shape
+    K *= 2
     ad = _left(a, a_scales, 2, K, a_dtype, "a")
     _packed(b, b_scales, (E, N, K), 32, "b")
     T, cap = a.shape[0], out.shape[0]
@@ -950,9 +965,10 @@ def bsq_moe_matmul_mxfp4(a, a_scales, b, b_scales, offsets, out, rows=None, k: i
 
 
 def _vectors(C, **ts):
+    f32 = _torch().float32
     for name, t in ts.items():
-        if t is not None:
-            _expect(t, _torch().float32, (C,), name)
+        if t is not None and (t.dtype != f32 or t.shape != (C,)):
+            _expect(t, f32, (C,), name)
 
 
 def bsq_norm_mx(x, y=None, codes=None, scales=None, gamma=None, beta=None, mean=None, rstd=None, eps: float = 1e-5,
