@@ -25,13 +25,24 @@ namespace bsq {
 
 namespace {
 
+// Sum over a wave, left in each lane, by exchanges between registers (through
+// LDS, as shuffles, each of the six takes five times as long).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(dpp_mov<CTRL>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v = dpp_add<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v = dpp_add<0x141>(v);  // row_half_mirror
+  v = dpp_add<0x140>(v);  // row_mirror
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
 // Sum over NT threads (64: a wave of its own), left in each; `red` is one of
 // two or more places used in turn.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
-}
 template <int NT>
 __device__ __forceinline__ float sum_over(float v, float* red) {
   v = wave_sum(v);
@@ -50,9 +61,10 @@ __device__ __forceinline__ void sum_over(float& a, float& b, float* red) {
   b = wave_sum(b);
   if constexpr (NT > 64) {
     constexpr int W = NT / 64;
+    const int w = int(threadIdx.x >> 6) % W;
     if ((threadIdx.x & 63) == 0) {
-      red[threadIdx.x >> 6] = a;
-      red[W + (threadIdx.x >> 6)] = b;
+      red[w] = a;
+      red[W + w] = b;
     }
     __syncthreads();
     a = b = 0.f;
@@ -91,6 +103,46 @@ __device__ __forceinline__ void load_row(const void* base, int64_t row0, int t, 
     for (int i = 0; i < 8; ++i) v[i] = col<NT, 0>(t, p, i) < C ? load1<BF16>(base, row0 + col<NT, 0>(t, p, i)) : 0.f;
   }
 }
+// Eight values as they lie in memory, so that a row under way takes as few
+// registers as it can.
+template <int BF16, int NT, int VEC>
+struct Raw {
+  uint4 v[BF16 && VEC ? 1 : 2];
+  __device__ __forceinline__ void load(const void* base, int64_t row0, int t, int p, int C) {
+    if constexpr (VEC) {
+      v[0] = make_uint4(0u, 0u, 0u, 0u);
+      if (!BF16) v[1] = v[0];
+      const int64_t at = row0 + 8 * (t + NT * p);
+      if (8 * (t + NT * p) < C) {
+        if constexpr (BF16) {
+          v[0] = ldnt(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+        } else {
+          v[0] = ldnt(reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at));
+          v[1] = ldnt(reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at) + 1);
+        }
+      }
+    } else {
+      float x[8];
+      load_row<BF16, NT, 0>(base, row0, t, p, C, x);
+      v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (BF16 && VEC) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = decode_bf16(w[i] & 0xFFFFu);
+        x[2 * i + 1] = decode_bf16(w[i] >> 16);
+      }
+    } else {
+      const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 template <int BF16, int NT, int VEC>
 __device__ __forceinline__ void store_row(void* base, int64_t row0, int t, int p, int C, const float (&v)[8]) {
   if constexpr (VEC) {
@@ -140,50 +192,65 @@ __device__ __forceinline__ void put_codes(NormCode code, uint8_t* codes, uint8_t
 }
 
 // ---------------------------------------------------------------- forward --
+// Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
+// gamma and beta in registers, the next one's load under way.
 template <int BF16, int VEC, int NT, int P>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a, int64_t first) {
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;  // of a workgroup
-  __shared__ float red[2][NT > 64 ? NT / 64 : 1];
-  const int t = threadIdx.x % NT, C = int(a.C);
-  const int64_t r = (first + blockIdx.x) * kRows + threadIdx.x / NT;
-  const bool in = r < a.R;
-  const int64_t row0 = (in ? r : a.R - 1) * a.C;
+  __shared__ float red[2][2][NT > 64 ? NT / 64 : 1];
+  const int t = threadIdx.x % NT, sub = threadIdx.x / NT, C = int(a.C);
+  const int64_t step = int64_t(gridDim.x) * kRows;
   saturate_fp8();
-  float x[P][8];
+  Raw<BF16, NT, VEC> raw[P];
+  auto load = [&](int64_t r) {
 #pragma unroll
-  for (int p = 0; p < P; ++p) load_row<BF16, NT, VEC>(a.x, row0, t, p, C, x[p]);
-  float mean = 0.f, s = 0.f;
-  if (!a.rms) {
+    for (int p = 0; p < P; ++p) raw[p].load(a.x, (r < a.R ? r : a.R - 1) * a.C, t, p, C);
+  };
+  load(int64_t(blockIdx.x) * kRows + sub);
+  float g[P][8], b[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    load_weight<NT, VEC>(a.gamma, t, p, C, 1.f, g[p]);
+    load_weight<NT, VEC>(a.beta, t, p, C, 0.f, b[p]);
+  }
+  const bool words = VEC && C % 128 == 0 && aligned4(a.scales);
+  int buf = 0;
+  for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < a.R; r0 += step, buf ^= 1) {
+    const int64_t r = r0 + sub, row0 = r * a.C;
+    const bool in = r < a.R;
+    float x[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) raw[p].get(x[p]);
+    if (r0 + step < a.R) load(r + step);
+    float mean = 0.f, s = 0.f;
+    if (!a.rms) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[p][i];
+      mean = sum_over<NT>(s, red[buf][0]) / float(C);
+      s = 0.f;
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += x[p][i];
-    mean = sum_over<NT>(s, red[0]) / float(C);
-    s = 0.f;
-  }
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[p][i] = col<NT, VEC>(t, p, i) < C ? x[p][i] - mean : 0.f;
-      s += x[p][i] * x[p][i];
+      for (int i = 0; i < 8; ++i) {
+        x[p][i] = col<NT, VEC>(t, p, i) < C ? x[p][i] - mean : 0.f;
+        s += x[p][i] * x[p][i];
+      }
+    const float rstd = 1.0f / sqrtf(sum_over<NT>(s, red[buf][1]) / float(C) + a.eps);
+    if (t == 0 && in) {
+      if (a.mean != nullptr) a.mean[r] = mean;
+      if (a.rstd != nullptr) a.rstd[r] = rstd;
     }
-  const float rstd = 1.0f / sqrtf(sum_over<NT>(s, red[1]) / float(C) + a.eps);
-  if (t == 0 && in) {
-    if (a.mean != nullptr) a.mean[r] = mean;
-    if (a.rstd != nullptr) a.rstd[r] = rstd;
-  }
-  const bool words = VEC && C % 128 == 0 && aligned4(a.scales);
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    float g[8], b[8];
-    load_weight<NT, VEC>(a.gamma, t, p, C, 1.f, g);
-    load_weight<NT, VEC>(a.beta, t, p, C, 0.f, b);
+    for (int p = 0; p < P; ++p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[p][i] = x[p][i] * rstd * g[i] + b[i];
-    if (in && a.y != nullptr) store_row<BF16, NT, VEC>(a.y, row0, t, p, C, x[p]);
-    if (VEC && a.codes != nullptr)
-      put_codes(a.code, a.codes, a.scales, row0 + 8 * (t + NT * p), in && 8 * (t + NT * p) < C, words, x[p]);
+      for (int i = 0; i < 8; ++i) x[p][i] = x[p][i] * rstd * g[p][i] + b[p][i];
+      if (in && a.y != nullptr) store_row<BF16, NT, VEC>(a.y, row0, t, p, C, x[p]);
+      if (VEC && a.codes != nullptr)
+        put_codes(a.code, a.codes, a.scales, row0 + 8 * (t + NT * p), in && 8 * (t + NT * p) < C, words, x[p]);
+    }
   }
 }
 
@@ -231,14 +298,34 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
 }
 
 // --------------------------------------------------------------- backward --
-// Workgroups go through the rows blockIdx.x + gridDim.x i.
+// Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
+// the next one's loads under way while a row is summed and written.  Two rows
+// of 256 threads to a workgroup halve the groups' sums: 16384 x 4096 71 + 5 us
+// against 73 + 7.
+template <int NT>
+constexpr int rows_of = NT < 256 ? 256 / NT : NT == 256 ? 2 : 1;
 template <int BF16, int VEC, int NT, int P>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm_dx(NormBackwardLaunch a) {
-  constexpr int kRows = NT < 256 ? 256 / NT : 1;
-  __shared__ float red[2][2 * (NT > 64 ? NT / 64 : 1)];
+__global__ void __launch_bounds__(NT * rows_of<NT>) k_norm_dx(NormBackwardLaunch a) {
+  constexpr int kRows = rows_of<NT>;
+  __shared__ float reds[kRows][2][2 * (NT > 64 ? NT / 64 : 1)];
   __shared__ float join[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? 2 * 8 * P * NT : 1];
   const int t = threadIdx.x % NT, sub = threadIdx.x / NT, C = int(a.C);
+  float(*const red)[2 * (NT > 64 ? NT / 64 : 1)] = reds[sub];
   const float inv = 1.0f / float(C);
+  const int64_t step = int64_t(gridDim.x) * kRows;
+  Raw<BF16, NT, VEC> xr[P], dr[P];
+  float mean_r = 0.f, rstd_r = 0.f;
+  auto load = [&](int64_t r) {
+    const int64_t rr = r < a.R ? r : a.R - 1;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      xr[p].load(a.x, rr * a.C, t, p, C);
+      dr[p].load(a.dy, rr * a.C, t, p, C);
+    }
+    mean_r = a.rms ? 0.f : a.mean[rr];
+    rstd_r = a.rstd[rr];
+  };
+  load(int64_t(blockIdx.x) * kRows + sub);
   float g[P][8], sg[P][8], sb[P][8];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -246,23 +333,18 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm_dx(NormBackwardLau
 #pragma unroll
     for (int i = 0; i < 8; ++i) sg[p][i] = sb[p][i] = 0.f;
   }
-  const int64_t step = int64_t(gridDim.x) * kRows;
-  float x[P][8], dy[P][8], mean = 0.f, rstd = 0.f;
-  auto load = [&](int64_t r) {
-    const int64_t rr = r < a.R ? r : a.R - 1;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      load_row<BF16, NT, VEC>(a.x, rr * a.C, t, p, C, x[p]);
-      load_row<BF16, NT, VEC>(a.dy, rr * a.C, t, p, C, dy[p]);
-    }
-    mean = a.rms ? 0.f : a.mean[rr];
-    rstd = a.rstd[rr];
-  };
   int buf = 0;
   for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < a.R; r0 += step, buf ^= 1) {
     const int64_t r = r0 + sub;
-    load(r);
     const bool in = r < a.R;
+    float x[P][8], dy[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      xr[p].get(x[p]);
+      dr[p].get(dy[p]);
+    }
+    const float mean = mean_r, rstd = rstd_r;
+    if (r0 + step < a.R) load(r + step);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p)
@@ -356,28 +438,29 @@ __global__ void __launch_bounds__(256) k_norm_dw_long(NormBackwardLaunch a, int 
   a.space[(groups + gr) * a.C + c] = sb;
 }
 
-// Sums over the groups in their order: 32 columns x 8 shares of the groups,
-// the shares added through LDS.
-__global__ void __launch_bounds__(256) k_norm_sum(const float* __restrict__ space, int groups, int64_t C, float* dgamma,
-                                                  float* dbeta) {
-  __shared__ float part[8][32];
-  const int64_t chunks = up_to(C, 32);
+// Sums over the groups: 16 columns x 16 shares of the groups, each in their
+// order, the shares added through LDS.
+constexpr int kSumCols = 16, kShares = 16;
+__global__ void __launch_bounds__(kSumCols* kShares) k_norm_sum(const float* __restrict__ space, int groups, int64_t C,
+                                                                float* dgamma, float* dbeta) {
+  __shared__ float part[kShares][kSumCols];
+  const int64_t chunks = up_to(C, kSumCols);
   const int which = int(blockIdx.x / chunks);  // 0: dgamma, 1: dbeta
   float* const out = which ? dbeta : dgamma;
   if (out == nullptr) return;
-  const int x = threadIdx.x & 31, share = threadIdx.x >> 5;
-  const int64_t c = blockIdx.x % chunks * 32 + x;
-  const int per = (groups + 7) / 8, end = min(groups, (share + 1) * per);
+  const int x = threadIdx.x % kSumCols, share = threadIdx.x / kSumCols;
+  const int64_t c = blockIdx.x % chunks * kSumCols + x;
+  const int per = (groups + kShares - 1) / kShares, end = min(groups, (share + 1) * per);
   float s = 0.f;
   if (c < C) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = share * per; i < end; ++i) s += space[(int64_t(which) * groups + i) * C + c];
   }
   part[share][x] = s;
   __syncthreads();
   if (share > 0 || c >= C) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += part[i][x];
+  for (int i = 1; i < kShares; ++i) s += part[i][x];
   out[c] = s;
 }
 
@@ -406,16 +489,16 @@ bsq_status launch_norm(const NormLaunch& L, hipStream_t st) {
     });
   return with_shape(L.C, [&](auto nt, auto p) {
     constexpr int NT = decltype(nt)::value, P = decltype(p)::value, kRows = NT < 256 ? 256 / NT : 1;
-    return in_parts(up_to(L.R, kRows), kLaunchGroups / 2, [&](int64_t first, int64_t n) {
-      const dim3 g = dim3(unsigned(n)), b = dim3(NT < 256 ? 256 : NT);
-      switch ((L.bf16 ? 1 : 0) | (L.C % 8 == 0 ? 2 : 0)) {
-        case 0: hipLaunchKernelGGL((k_norm<0, 0, NT, P>), g, b, 0, st, L, first); break;
-        case 1: hipLaunchKernelGGL((k_norm<1, 0, NT, P>), g, b, 0, st, L, first); break;
-        case 2: hipLaunchKernelGGL((k_norm<0, 1, NT, P>), g, b, 0, st, L, first); break;
-        default: hipLaunchKernelGGL((k_norm<1, 1, NT, P>), g, b, 0, st, L, first);
-      }
-      return launch_status("norm");
-    });
+    // eight workgroups of 256 threads to a CU
+    const int64_t most = 8 * kCUs * 256 / (NT < 256 ? 256 : NT), all = up_to(L.R, kRows);
+    const dim3 g = dim3(unsigned(all < most ? all : most)), b = dim3(NT < 256 ? 256 : NT);
+    switch ((L.bf16 ? 1 : 0) | (L.C % 8 == 0 ? 2 : 0)) {
+      case 0: hipLaunchKernelGGL((k_norm<0, 0, NT, P>), g, b, 0, st, L); break;
+      case 1: hipLaunchKernelGGL((k_norm<1, 0, NT, P>), g, b, 0, st, L); break;
+      case 2: hipLaunchKernelGGL((k_norm<0, 1, NT, P>), g, b, 0, st, L); break;
+      default: hipLaunchKernelGGL((k_norm<1, 1, NT, P>), g, b, 0, st, L);
+    }
+    return launch_status("norm");
   });
 }
 
@@ -437,10 +520,10 @@ bsq_status launch_norm_backward(const NormBackwardLaunch& L, hipStream_t st) {
     s = launch_status("norm_backward");
   } else if (L.R > 0) {
     s = with_shape(L.C, [&](auto nt, auto p) {
-      constexpr int NT = decltype(nt)::value, P = decltype(p)::value, kRows = NT < 256 ? 256 / NT : 1;
-      const int64_t most = 512, all = up_to(L.R, kRows);
+      constexpr int NT = decltype(nt)::value, P = decltype(p)::value, kRows = rows_of<NT>;
+      const int64_t most = NT == 256 ? 256 : 512, all = up_to(L.R, kRows);
       groups = int(all < most ? all : most);
-      const dim3 g = dim3(unsigned(groups)), b = dim3(NT < 256 ? 256 : NT);
+      const dim3 g = dim3(unsigned(groups)), b = dim3(NT * kRows);
       switch ((L.bf16 ? 1 : 0) | (L.C % 8 == 0 ? 2 : 0)) {
         case 0: hipLaunchKernelGGL((k_norm_dx<0, 0, NT, P>), g, b, 0, st, L); break;
         case 1: hipLaunchKernelGGL((k_norm_dx<1, 0, NT, P>), g, b, 0, st, L); break;
@@ -451,7 +534,7 @@ bsq_status launch_norm_backward(const NormBackwardLaunch& L, hipStream_t st) {
     });
   }
   if (s != BSQ_OK || !weights) return s;
-  hipLaunchKernelGGL(k_norm_sum, dim3(unsigned(2 * up_to(L.C, 32))), 256, 0, st, L.space, groups, L.C, L.dgamma, L.dbeta);
+  hipLaunchKernelGGL(k_norm_sum, dim3(unsigned(2 * up_to(L.C, kSumCols))), kSumCols * kShares, 0, st, L.space, groups, L.C, L.dgamma, L.dbeta);
   return launch_status("norm_backward (weights)");
 }
 
