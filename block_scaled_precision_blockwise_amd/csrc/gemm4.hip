@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   static_assert(TN % 64 == 0, "scale rows by the 64");
   constexpr int kUnit = 512 / kStep;  // steps of 16 blocks
   static_assert(SR / 64 <= NW, "a wave has 64 rows of scales or none");
-  static_assert(S <= 3 && S - 1 <= kUnit, "two units of scales, waits by one step ahead");
+  constexpr int SU = (S - 1 + kUnit - 1) / kUnit + 1;  // units of scales that the steps under way are of
   constexpr int kStage = TM * BA + TN * BB;
   constexpr int kRowB = NB * 64 + 16;  // bytes of a staged output row of a wave, padded
   constexpr int kOut = NW * 16 * kRowB;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   constexpr int kMost = kOut > kJoin ? kOut : kJoin;
   constexpr int kAB = KG * S * kStage > kMost ? KG * S * kStage : kMost;
   __shared__ __attribute__((aligned(16))) uint8_t lds_ab[kAB];
-  __shared__ __attribute__((aligned(16))) uint8_t lds_sc[KG][2][SR * (AL ? 16 : 20)];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_sc[KG][SU][SR * (AL ? 16 : 20)];
   __shared__ int src[TM];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
     const int ks = global(i);
     const uint32_t at = uint32_t(st * kStage);
     if (has && i % kUnit == 0) {
-      const uint32_t from = so + 16u * uint32_t(ks / kUnit), to = uint32_t((i / kUnit & 1) * SR * (AL ? 16 : 20));
+      const uint32_t from = so + 16u * uint32_t(ks / kUnit), to = uint32_t(i / kUnit % SU * SR * (AL ? 16 : 20));
       dma16(rs, from, ls + to);
       if (!AL) dma4(rs, from + 16u, ls4 + to);
     }
@@ -404,8 +404,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
     const int i = u * kUnit + at;
     // S - 2 steps (and what scales come with them) stay under way; near the end,
     // where fewer are, all are waited for
+    // (units that start among the S - 2 steps: `starts`)
+    const int starts = (at + S - 2) / kUnit;
+    static_assert((kUnit - 1 + S - 2) / kUnit <= 2, "at most two");
     if (i + S - 2 >= nk) __builtin_amdgcn_s_waitcnt(vmcnt(0));
-    else if (S > 2 && has && at == kUnit - 1) __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads + kScales));
+    else if (has && starts == 2) __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads + 2 * kScales));
+    else if (has && starts == 1) __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads + kScales));
     else __builtin_amdgcn_s_waitcnt(vmcnt((S - 2) * kLoads));
     barrier();
     if (i >= nk) return;  // other groups' steps
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
     const uint8_t* ta = lds + st * kStage;
     const uint8_t* tb = ta + TM * BA;
     if (at == 0) {
-      const uint8_t* const ss = lds_s[u & 1];
+      const uint8_t* const ss = lds_s[u % SU];
       auto scales = [&](int row, int byte, uint32_t (&q)[4]) {
         const uint4 v = *reinterpret_cast<const uint4*>(ss + 16 * row);
         uint32_t x[5] = {v.x, v.y, v.z, v.w, 0u};
