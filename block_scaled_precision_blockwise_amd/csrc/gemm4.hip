@@ -145,7 +145,10 @@ __device__ __forceinline__ void store4(const Mx4Args& p, int64_t at, v4f v) {
 // Tiles of 16 MB rows x 16 NB columns, where the weights' bytes are most of the
 // work.  W waves share a tile's contraction, each with U chunks of 128 at a
 // time, straight from memory to the operand registers, and their sums are
-// joined through LDS in the waves' order.
+// joined through LDS in the waves' order.  Bound by the latency of a launch and
+// of memory: one row of 8192 x 4096 5.6 us (17.8 MB, 3.2 TB/s), of 4096 x 4096
+// 4.0 us.  Tiles of 64 x 64 this way are slower than through LDS (1024 x 1024 x
+// 16384 40 us / 22): a load's 16 rows of 64 bytes are half lines.
 template <int FA, int MB, int NB, int W>
 __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
   constexpr int TM = 16 * MB, TN = 16 * NB, U = 4;
@@ -285,12 +288,19 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
 //
 // Where there are fewer tiles than CUs, KG groups of WM x WN waves share a
 // tile's units (group i has i, i + KG, ..), each with a ring of its own, and
-// their sums are joined through LDS in the groups' order.
-template <int FA, int WM, int WN, int MB, int NB, int S, int KG, int AL>
+// their sums are joined through LDS in the groups' order.  A step has U parts.
+//
+// Measured: 1021 x 1792 x 2880, 8-bit A, 13.6 us (64 x 128, two groups); 1024 x
+// 1024 x 16384 in 4 bits 21 us (64 x 64, two groups; one group 29), 600 ns for
+// 512 of the contraction: more stages (3 to 5) or parts (1, 2) are within 0.5
+// us of that, waves of 64 x 32 23.  64 rows x 4096 x 4096 6.6 us (32 x 64, two
+// groups, two parts; one part 7.2).  8 tokens over 32 experts, N 4096, K 2048:
+// 17 us, 5.3 TB/s (32 x 64).
+template <int FA, int WM, int WN, int MB, int NB, int S, int KG, int U, int AL>
 __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   constexpr int NW = WM * WN, TM = 16 * MB * WM, TN = 16 * NB * WN;
-  constexpr int kStep = FA == 4 ? 256 : 128, kHalves = kStep / 128;
-  constexpr int BA = 128, BB = kStep / 2;  // bytes of a row of a step
+  constexpr int kPart = FA == 4 ? 256 : 128, kStep = U * kPart, kHalves = kPart / 128;
+  constexpr int BA = 128, BB = kPart / 2;  // bytes of a row of a part of a step
   constexpr int RB = 1024 / BB;            // rows of B of a load
   constexpr int LA = TM / 8 / NW, LB = TN / RB / NW;
   static_assert(TM % (8 * NW) == 0 && TN % (RB * NW) == 0 && NW % 2 == 0, "whole loads of every wave");
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   constexpr int kUnit = 512 / kStep;  // steps of 16 blocks
   static_assert(SR / 64 <= NW, "a wave has 64 rows of scales or none");
   constexpr int SU = (S - 1 + kUnit - 1) / kUnit + 1;  // units of scales that the steps under way are of
-  constexpr int kStage = TM * BA + TN * BB;
+  constexpr int kPartBytes = TM * BA + TN * BB, kStage = U * kPartBytes;
   constexpr int kRowB = NB * 64 + 16;  // bytes of a staged output row of a wave, padded
   constexpr int kOut = NW * 16 * kRowB;
   constexpr int kJoin = (KG - 1) * NW * MB * NB * 1024;  // the other groups' accumulators
@@ -342,9 +352,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
   for (int s = 0; s < LB; ++s)
     pb[s] = view.b(t.e) + int64_t(min(t.n0 + RB * (w + NW * s) + brow, p.N - 1)) * view.pitch_b() + cb;
   const uint32_t la = lds_of(lds + 1024 * w), lb = lds_of(lds + TM * BA + 1024 * w);
-  // whether the last step has not got the lane's chunk
-  const int64_t last = int64_t(all - 1) * BA, last_b = int64_t(all - 1) * BB;
-  const bool past_a = last + ca >= view.pitch_a(), past_b = last_b + cb >= view.pitch_b();
+  const int64_t last = int64_t(all - 1) * U * BA, last_b = int64_t(all - 1) * U * BB;
   const bool part = p.K % kStep != 0;
   // scales: wave w has rows 64 w .. of A's and then B's
   const int64_t sp = view.pitch_s();
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
                                : rsrc(view.sb(t.e), p.N * sp);
   const uint32_t so = (srow < SM ? uint32_t(bm + a_row(min(srow, TM - 1)) * sp) : uint32_t(b_row(srow - SM) * sp)) & ~3u;
   const uint32_t ls = lds_of(&lds_s[0][64 * w * 16]), ls4 = lds_of(&lds_s[0][SR * 16 + 64 * w * 4]);
-  constexpr int kLoads = LA + LB, kScales = AL ? 1 : 2;  // of a step, of a unit
+  constexpr int kLoads = U * (LA + LB), kScales = AL ? 1 : 2;  // of a step, of a unit
   const uint8_t* const zeros = kZeros;
   auto load = [&](int i, int st) {  // the group's i-th step
     const int ks = global(i);
@@ -368,16 +376,21 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
       dma16(rs, from, ls + to);
       if (!AL) dma4(rs, from + 16u, ls4 + to);
     }
-    if (part && ks == all - 1) {
 #pragma unroll
-      for (int s = 0; s < LA; ++s) dma16(past_a ? zeros : pa[s] + last, la + at + uint32_t(1024 * NW * s));
+    for (int u = 0; u < U; ++u) {
+      const uint32_t to = at + uint32_t(u * kPartBytes);
+      if (part && ks == all - 1) {  // zeros where the last step has not got the lane's chunk
+        const bool past_a = last + u * BA + ca >= view.pitch_a(), past_b = last_b + u * BB + cb >= view.pitch_b();
 #pragma unroll
-      for (int s = 0; s < LB; ++s) dma16(past_b ? zeros : pb[s] + last_b, lb + at + uint32_t(1024 * NW * s));
-    } else {
+        for (int s = 0; s < LA; ++s) dma16(past_a ? zeros : pa[s] + last + u * BA, la + to + uint32_t(1024 * NW * s));
 #pragma unroll
-      for (int s = 0; s < LA; ++s) dma16(pa[s] + int64_t(ks) * BA, la + at + uint32_t(1024 * NW * s));
+        for (int s = 0; s < LB; ++s) dma16(past_b ? zeros : pb[s] + last_b + u * BB, lb + to + uint32_t(1024 * NW * s));
+      } else {
 #pragma unroll
-      for (int s = 0; s < LB; ++s) dma16(pb[s] + int64_t(ks) * BB, lb + at + uint32_t(1024 * NW * s));
+        for (int s = 0; s < LA; ++s) dma16(pa[s] + (int64_t(ks) * U + u) * BA, la + to + uint32_t(1024 * NW * s));
+#pragma unroll
+        for (int s = 0; s < LB; ++s) dma16(pb[s] + (int64_t(ks) * U + u) * BB, lb + to + uint32_t(1024 * NW * s));
+      }
     }
   };
 
@@ -415,8 +428,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
     if (i >= nk) return;  // other groups' steps
     // past the barrier nobody reads the stage before this one
     if (i + S - 1 < nk) load(i + S - 1, st == 0 ? S - 1 : st - 1);
-    const uint8_t* ta = lds + st * kStage;
-    const uint8_t* tb = ta + TM * BA;
     if (at == 0) {
       const uint8_t* const ss = lds_s[u % SU];
       auto scales = [&](int row, int byte, uint32_t (&q)[4]) {
@@ -455,13 +466,16 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
     auto chunk = [&](const uint8_t* tile, int row, int c) {  // of a 128-byte row
       return *reinterpret_cast<const uint4*>(tile + row * 128 + 16 * (c ^ x8));
     };
-    auto bfrag = [&](int h, int j) {
+    auto bfrag = [&](const uint8_t* tb, int h, int j) {
       const int row = 16 * NB * wn + 16 * j + r16;
       if constexpr (BB == 128) return wide(chunk(tb, row, 4 * h + g));
       else return wide(*reinterpret_cast<const uint4*>(tb + (row >> 1) * 128 + 64 * (row & 1) + 16 * (g ^ ((row >> 2) & 3))));
     };
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
+    for (int c = 0; c < U * kHalves; ++c) {  // chunks of 128 of the contraction
+      const int h = c % kHalves, n = U * kHalves * at + c;
+      const uint8_t* ta = lds + st * kStage + c / kHalves * kPartBytes;
+      const uint8_t* tb = ta + TM * BA;
       v8i fa[MB];
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
@@ -471,10 +485,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
       }
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const v8i fb = bfrag(h, j);
+        const v8i fb = bfrag(tb, h, j);
 #pragma unroll
         for (int i = 0; i < MB; ++i)
-          acc[j][i] = mfma4<FA>(fb, fa[i], acc[j][i], int(qb[kHalves * at + h][j]), int(qa[kHalves * at + h][i]));
+          acc[j][i] = mfma4<FA>(fb, fa[i], acc[j][i], int(qb[n][j]), int(qa[n][i]));
       }
     }
     st = st == S - 1 ? 0 : st + 1;
@@ -531,7 +545,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
 
 // -------------------------------------------------------------- big tiles --
 // 256 x 256 by four waves of 128 x 128, one wave per SIMD: a step's LDS reads
-// are 128 KiB for 1024 4-bit MFMAs of 16 cycles on four SIMDs, and the
+// are 128 KiB for 512 4-bit MFMAs of 16 cycles on four SIMDs, and the
 // accumulators of a wave fill the 256 accumulation registers.  With nothing
 // else to run on its SIMD a wave may never wait, so it goes through a step in
 // four phases, one for each pairing of the halves of its A and B fragments (A0
@@ -547,10 +561,19 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
 // one word holds its block of each of four MFMAs.
 //
 // A workgroup goes through the tiles blockIdx.x + gridDim.x i.  Between two of
-// them the output of the last one goes from the accumulators to memory without
-// LDS (lanes exchange halves until each holds 16 neighbouring bytes of a row),
-// the loads of the next one's first two steps beside it; the search for the
-// one after follows while they land.
+// them come the loads of the next one's first two steps, then the output of the
+// last one, from the accumulators to memory without LDS (lanes exchange halves
+// until each holds 16 neighbouring bytes of a row).  Where the tile is whole the
+// number of its stores is known, and they are left under way: the waits for the
+// next tile's first steps count them out (360 us where waiting for them took
+// 391, the experts of 65536 rows below).  The search for a tile is made of a copy
+// of the offsets in LDS, so that it waits for no load.
+//
+// Measured: 16384 x 8192 x 4096 in 4 bits 263 us, 4.2 PFLOP/s; 65536 rows over
+// 32 experts, N 4096, K 2048, 360 us, 3.1.  Pure MFMAs on random codes reach 6.9
+// PFLOP/s (9.0 on zeros: the clock gives way).  Of the 263 us the loads are 32,
+// the stores 30, the LDS reads 10; two wait states in front of every MFMA and of
+// every load's m0 were 25 more.
 
 // 16 bytes from any address before `end`, which has 16 in front of it: the last
 // 16 where fewer are left.
@@ -1038,15 +1061,15 @@ bsq_status launch_few(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   });
 }
 
-template <int WM, int WN, int MB, int NB, int S, int KG>
+template <int WM, int WN, int MB, int NB, int S, int KG, int U>
 bsq_status launch_tile(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   return in_parts(tile_rows(L, 16 * MB * WM) * up_to(L.N, 16 * NB * WN), kLaunchGroups, [&](int64_t first, int64_t n) {
     a.first = int(first);
     return with_code(L.a, [&](auto fa) {
       constexpr int FA = decltype(fa)::value;
       const dim3 g = dim3(unsigned(n)), b = dim3(64 * WM * WN * KG);
-      if (L.K % 128 == 0) hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, 1>), g, b, 0, st, a);
-      else hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, 0>), g, b, 0, st, a);
+      if (L.K % 128 == 0) hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, U, 1>), g, b, 0, st, a);
+      else hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, U, 0>), g, b, 0, st, a);
       return launch_status("mx4 product");
     });
   });
@@ -1074,15 +1097,15 @@ bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
     case Mx4Tile::few16x16: return launch_few<1, 1, 4>(L, a, st);
     case Mx4Tile::few16x32: return launch_few<1, 2, 4>(L, a, st);
     case Mx4Tile::few32x32: return launch_few<2, 2, 4>(L, a, st);
-    case Mx4Tile::t32x64: return launch_tile<1, 4, 2, 1, 3, 1>(L, a, st);
-    case Mx4Tile::t32x64g2: return launch_tile<1, 4, 2, 1, 3, 2>(L, a, st);
-    case Mx4Tile::t64x64g2: return launch_tile<2, 2, 2, 2, 3, 2>(L, a, st);
-    case Mx4Tile::t64x128g2: return launch_tile<2, 2, 2, 4, 3, 2>(L, a, st);
-    case Mx4Tile::t64x128: return launch_tile<2, 2, 2, 4, 2, 1>(L, a, st);
-    case Mx4Tile::t128x128: return launch_tile<4, 2, 2, 4, 2, 1>(L, a, st);
+    case Mx4Tile::t32x64: return launch_tile<1, 4, 2, 1, 3, 1, 1>(L, a, st);
+    case Mx4Tile::t32x64g2: return launch_tile<1, 4, 2, 1, 2, 2, 2>(L, a, st);
+    case Mx4Tile::t64x64g2: return launch_tile<2, 2, 2, 2, 3, 2, 1>(L, a, st);
+    case Mx4Tile::t64x128g2: return launch_tile<2, 2, 2, 4, 3, 2, 1>(L, a, st);
+    case Mx4Tile::t64x128: return launch_tile<2, 2, 2, 4, 2, 1, 1>(L, a, st);
+    case Mx4Tile::t128x128: return launch_tile<4, 2, 2, 4, 2, 1, 1>(L, a, st);
     default:
       // gathered rows are addressed with 32 bits
-      if (L.rows != nullptr && L.T * pitch_a >= (int64_t(1) << 32)) return launch_tile<4, 2, 2, 4, 2, 1>(L, a, st);
+      if (L.rows != nullptr && L.T * pitch_a >= (int64_t(1) << 32)) return launch_tile<4, 2, 2, 4, 2, 1, 1>(L, a, st);
       return launch_big(L, a, st);
   }
 }
