@@ -929,8 +929,8 @@ def bsq_scaled_matmul_mxfp4(lhs, rhs, lhs_scales, rhs_scales, out, lhs_dtype: Op
     _rank(rhs, 3, "rhs")
     B, N, K = rhs.shape
     K *= 2
-    ld = _left(lhs, lhs_scales, 3, K, lhs_dtype, "lhs")
     _packed(rhs, rhs_scales, (B, N, K), 32, "rhs")
+    ld = _left(lhs, lhs_scales, 3, K, lhs_dtype, "lhs")
     M = lhs.shape[1]
     if lhs.shape[0] != B:
         raise ValueError("lhs and rhs must share B")
@@ -952,8 +952,8 @@ def bsq_moe_matmul_mxfp4(a, a_scales, b, b_scales, offsets, out, rows=None, k: i
     _rank(out, 2, "out")
     E, N, K = b.shape
     K *= 2
-    ad = _left(a, a_scales, 2, K, a_dtype, "a")
     _packed(b, b_scales, (E, N, K), 32, "b")
+    ad = _left(a, a_scales, 2, K, a_dtype, "a")
     T, cap = a.shape[0], out.shape[0]
     _expect(offsets, torch.int32, (E + 1,), "offsets")
     _expect(out, out.dtype, (cap, N), "out")

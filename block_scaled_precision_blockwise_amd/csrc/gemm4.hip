@@ -23,6 +23,7 @@
 #include "mx4_index.h"
 #include "tiles.h"
 
+#include <hip/hip_ext.h>
 #include <type_traits>
 
 namespace bsq {
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(256, 1) k_mx4_big(Mx4Args p) {
   };
   // Addresses of tile t, whose rows of A are in src[buf], and its first scales.
   auto begin = [&](const Place4& t, int buf) {
-    if (t.none || all == 0) return;
+    if (t.none) return;
     // rows of their own are near the tile's first; gathered ones anywhere
     const int near = p.rows != nullptr ? 0 : min(t.m0, int(p.T) - 1);
     auto a_row = [&](int r) { return max(src[buf][r], near) - near; };
@@ -1047,6 +1048,14 @@ bsq_status with_code(Code4 a, F&& f) {
   }
 }
 
+// Launches a product, with the events that the caller asked for, if any.
+template <typename Kernel>
+void launch_timed(Kernel k, dim3 grid, dim3 block, hipStream_t st, const Mx4Args& a) {
+  const GemmEvents ev = take_gemm_events();
+  if (ev.start != nullptr || ev.stop != nullptr) hipExtLaunchKernelGGL(k, grid, block, 0, st, ev.start, ev.stop, 0, a);
+  else hipLaunchKernelGGL(k, grid, block, 0, st, a);
+}
+
 // Tile rows of all segments at most, or of the batch.
 int64_t tile_rows(const Mx4Launch& L, int tm) { return L.offsets ? L.cap / tm + L.E + 1 : up_to(L.T, tm) * L.E; }
 
@@ -1055,7 +1064,7 @@ bsq_status launch_few(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   return in_parts(tile_rows(L, 16 * MB) * up_to(L.N, 16 * NB), kLaunchGroups, [&](int64_t first, int64_t n) {
     a.first = int(first);
     return with_code(L.a, [&](auto fa) {
-      hipLaunchKernelGGL((k_mx4_few<decltype(fa)::value, MB, NB, W>), dim3(unsigned(n)), dim3(64 * W), 0, st, a);
+      launch_timed(k_mx4_few<decltype(fa)::value, MB, NB, W>, dim3(unsigned(n)), dim3(64 * W), st, a);
       return launch_status("mx4 product (few rows)");
     });
   });
@@ -1068,8 +1077,8 @@ bsq_status launch_tile(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
     return with_code(L.a, [&](auto fa) {
       constexpr int FA = decltype(fa)::value;
       const dim3 g = dim3(unsigned(n)), b = dim3(64 * WM * WN * KG);
-      if (L.K % 128 == 0) hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, U, 1>), g, b, 0, st, a);
-      else hipLaunchKernelGGL((k_mx4_tile<FA, WM, WN, MB, NB, S, KG, U, 0>), g, b, 0, st, a);
+      if (L.K % 128 == 0) launch_timed(k_mx4_tile<FA, WM, WN, MB, NB, S, KG, U, 1>, g, b, st, a);
+      else launch_timed(k_mx4_tile<FA, WM, WN, MB, NB, S, KG, U, 0>, g, b, st, a);
       return launch_status("mx4 product");
     });
   });
@@ -1081,8 +1090,8 @@ bsq_status launch_big(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   const dim3 g = dim3(unsigned(grid < kCUs ? grid : kCUs)), b = dim3(256);
   return with_code(L.a, [&](auto fa) {
     constexpr int FA = decltype(fa)::value;
-    if (L.out_bf16) hipLaunchKernelGGL((k_mx4_big<FA, 1>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_mx4_big<FA, 0>), g, b, 0, st, a);
+    if (L.out_bf16) launch_timed(k_mx4_big<FA, 1>, g, b, st, a);
+    else launch_timed(k_mx4_big<FA, 0>, g, b, st, a);
     return launch_status("mx4 product (big tiles)");
   });
 }
@@ -1104,8 +1113,10 @@ bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
     case Mx4Tile::t64x128: return launch_tile<2, 2, 2, 4, 2, 1, 1>(L, a, st);
     case Mx4Tile::t128x128: return launch_tile<4, 2, 2, 4, 2, 1, 1>(L, a, st);
     default:
-      // gathered rows are addressed with 32 bits
-      if (L.rows != nullptr && L.T * pitch_a >= (int64_t(1) << 32)) return launch_tile<4, 2, 2, 4, 2, 1, 1>(L, a, st);
+      // gathered rows are addressed with 32 bits, and scales read 16 at a time
+      // (experts' rows may be many more than the tokens; no contraction has none)
+      if ((L.rows != nullptr && L.T * pitch_a >= (int64_t(1) << 32)) || L.T * (L.K / 32) < 16)
+        return launch_tile<4, 2, 2, 4, 2, 1, 1>(L, a, st);
       return launch_big(L, a, st);
   }
 }

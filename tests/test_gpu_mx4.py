@@ -10,6 +10,7 @@ import torch
 
 import block_scaled_precision_blockwise_amd as bsq
 from gpu_helpers import assert_bytes_equal, host, say, to_dev
+from mx4_sizes import DENSE, RAGGED, cap_of
 from oracle import fp4
 
 pytestmark = pytest.mark.gpu
@@ -141,67 +142,48 @@ def hold(out, y, T, G, K, eight, what):
 
 
 KINDS = ["e2m1", "e4m3", "e5m2"]
-# one row to several tiles, contractions of one block, of parts of a step and of several steps
-DENSE = [(1, 1, 16, 32), (1, 1, 48, 4096), (1, 3, 272, 96), (2, 16, 64, 160), (1, 16, 4112, 1056), (1, 17, 80, 128), (3, 5, 32, 64),
-         (1, 33, 144, 256), (1, 64, 128, 288), (2, 100, 208, 416), (1, 129, 272, 512), (1, 257, 528, 1312),
-         (1, 300, 16, 2880), (3, 70, 96, 1056)]
+
+
+def dense(a, sa, b, sb, dtype):
+    out = empty(a.shape[0], a.shape[1], b.shape[1], dtype=dtype)
+    bsq.bsq_scaled_matmul_mxfp4(a, b, sa, sb, out)
+    return out
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B, M, N, K", DENSE)
-def test_dense_exact(B, M, N, K, kind):
+@pytest.mark.parametrize("tile", DENSE)
+def test_dense_exact_by_each_tile(tile, kind):
+    B, M, N, Ks = DENSE[tile]
+    for K in Ks:
+        say("mxfp4 dense", tile, B, M, N, K, kind)
+        a, sa = exact_operand((B, M, K), kind, 1)
+        b, sb = exact_operand((B, N, K), "e2m1", 2)
+        out, bf = dense(a, sa, b, sb, torch.float32), dense(a, sa, b, sb, torch.bfloat16)
+        for i in range(B):
+            y = decode(a[i], sa[i]) @ decode(b[i], sb[i]).t()
+            assert torch.equal(out[i].double(), y), (K, i, int((out[i].double() != y).sum()))
+            assert torch.equal(bf[i], y.float().bfloat16()), (K, i)
+
+
+# odd rows, columns and batches, one value's block, empty contractions
+SMALL = [(1, 1, 16, 32), (1, 3, 272, 96), (2, 16, 64, 160), (3, 5, 32, 64), (1, 33, 144, 256), (2, 100, 208, 416),
+         (1, 129, 272, 512), (1, 300, 16, 2880), (3, 70, 96, 1056), (5, 7, 48, 0), (1, 4100, 3600, 0)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B, M, N, K", SMALL)
+def test_dense_exact_small(B, M, N, K, kind):
     say("mxfp4 dense", B, M, N, K, kind)
     a, sa = exact_operand((B, M, K), kind, 1)
     b, sb = exact_operand((B, N, K), "e2m1", 2)
-    out, bf = empty(B, M, N, dtype=torch.float32), empty(B, M, N, dtype=torch.bfloat16)
-    bsq.bsq_scaled_matmul_mxfp4(a, b, sa, sb, out)
-    bsq.bsq_scaled_matmul_mxfp4(a, b, sa, sb, bf)
-    for i in range(B):
-        y = decode(a[i], sa[i]) @ decode(b[i], sb[i]).t()
-        assert torch.equal(out[i].double(), y), (i, int((out[i].double() != y).sum()))
-        assert torch.equal(bf[i], y.float().bfloat16())
-
-
-# tiles of 256 x 256: one step of the contraction or less, two, more than a
-# group of scales, ends inside a step; rows and columns past the last tile
-BIG = [(1, 2817, 3600, K) for K in (32, 96, 128, 256, 288, 384, 512, 544, 800, 1024, 1056, 1408)] + [(3, 1030, 2576, 672)]
+    y = torch.bmm(decode(a, sa), decode(b, sb).transpose(1, 2).contiguous())
+    assert torch.equal(dense(a, sa, b, sb, torch.float32).double(), y)
+    assert torch.equal(dense(a, sa, b, sb, torch.bfloat16), y.float().bfloat16())
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B, M, N, K", BIG)
-def test_dense_exact_big(B, M, N, K, kind):
-    test_dense_exact(B, M, N, K, kind)
-
-
-@pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("own", [True, False])
-@pytest.mark.parametrize("K", [128, 288, 1056])
-def test_ragged_exact_big(K, own, kind):
-    """Many rows to an expert: segments that start anywhere, an empty one, holes, rows behind the last."""
-    counts, T, N, k = [600, 0, 1033, 257, 900, 1, 640], 1100, 2576, 3
-    say("mxfp4 ragged, big tiles", K, own, kind)
-    b, sb = exact_operand((len(counts), N, K), "e2m1", 6)
-    offsets, rows = ragged(counts, T, k, 8, 7)
-    cap = rows.numel()
-    T = cap - 30 if own else T  # own rows past A's are zeros
-    a, sa = exact_operand((T, K), kind, 5)
-    out, bf = empty(cap, N, dtype=torch.float32), empty(cap, N, dtype=torch.bfloat16)
-    for o in (out, bf):
-        bsq.bsq_moe_matmul_mxfp4(a, sa, b, sb, offsets, o, rows=None if own else rows, k=k)
-    want = torch.zeros(cap, N, dtype=torch.float64, device="cuda")
-    ends, x = offsets.tolist(), decode(a, sa)
-    at = torch.arange(cap, device="cuda") if own else torch.where(rows >= 0, rows // k, -1).long()
-    at = torch.where(at < T, at, -1)
-    for e in range(len(counts)):
-        r = at[ends[e]:ends[e + 1]]
-        want[ends[e]:ends[e + 1]] = torch.where((r >= 0)[:, None], x[r.clamp_min(0)], 0.0) @ decode(b[e], sb[e]).t()
-    assert torch.equal(out.double(), want), int((out.double() != want).sum())
-    assert torch.equal(bf, want.float().bfloat16())
-
-
-@pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B, M, N, K", [(1, 1, 272, 4096), (2, 33, 144, 288), (1, 200, 272, 1056), (1, 257, 528, 1312),
-                                        (1, 2817, 3600, 1056)])
+@pytest.mark.parametrize("B, M, N, K", [(1, 1, 272, 4096), (2, 33, 144, 288), (1, 257, 528, 1312), (1, 400, 1200, 1312),
+                                        (1, 1000, 1504, 1056), (1, 1700, 2000, 1056), (1, 4100, 3600, 1056)])
 def test_dense_any_codes(B, M, N, K, kind):
     say("mxfp4 dense, any codes", B, M, N, K, kind)
     a, sa = full_operand((B, M, K), kind, 3)
@@ -227,26 +209,63 @@ def ragged(counts, T, k, align, seed):
     return i32(offsets), i32(rows)
 
 
+def experts(a, sa, b, sb, offsets, rows, cap, k, dtype):
+    out = empty(cap, b.shape[1], dtype=dtype)
+    bsq.bsq_moe_matmul_mxfp4(a, sa, b, sb, offsets, out, rows=rows, k=k)
+    return out
+
+
+def experts_reference(a, sa, b, sb, offsets, rows, cap, k):
+    """Rows of segments that may lie anywhere in [0, cap), the rest zeros."""
+    T = a.shape[0]
+    at = torch.arange(cap, device="cuda") if rows is None else torch.where(rows >= 0, rows // k, -1).long()
+    at = torch.where(at < T, at, -1)
+    want = torch.zeros(cap, b.shape[1], dtype=torch.float64, device="cuda")
+    x, ends = decode(a, sa), offsets.tolist()
+    for e in range(b.shape[0]):
+        r = at[ends[e]:ends[e + 1]]
+        if r.numel() and T:
+            want[ends[e]:ends[e + 1]] = torch.where((r >= 0)[:, None], x[r.clamp_min(0)], 0.0) @ decode(b[e], sb[e]).t()
+    return want
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("tile", RAGGED)
+def test_ragged_exact_by_each_tile(tile, own, kind):
+    counts, align, N, Ks = RAGGED[tile]
+    cap, k = cap_of(counts, align), 2
+    T = cap - 3 if own else cap  # own rows past A's are zeros
+    offsets, rows = ragged(counts, T, k, align, 7)
+    assert rows.numel() == cap
+    for K in Ks:
+        say("mxfp4 ragged", tile, own, K, kind)
+        a, sa = exact_operand((T, K), kind, 5)
+        b, sb = exact_operand((len(counts), N, K), "e2m1", 6)
+        args = (a, sa, b, sb, offsets, None if own else rows, cap, k)
+        want = experts_reference(*args)
+        assert torch.equal(experts(*args, torch.float32).double(), want), K
+        assert torch.equal(experts(*args, torch.bfloat16), want.float().bfloat16()), K
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("counts, T, N, K, k, align", [
     ([1], 1, 16, 32, 1, 1), ([0, 1, 0, 2, 1], 3, 80, 96, 2, 1), ([3, 16, 17, 0, 1, 40], 9, 272, 160, 4, 1),
-    ([5, 0, 130], 31, 144, 512, 2, 32), ([200, 7, 0, 64], 40, 208, 1056, 3, 128), ([0, 0], 4, 32, 64, 1, 1)])
+    ([5, 0, 130], 31, 144, 512, 2, 32), ([200, 7, 0, 64], 40, 208, 1056, 3, 128), ([0, 0], 4, 32, 64, 1, 1),
+    ([1, 0, 2], 1, 64, 96, 4, 128), ([3, 1], 2, 48, 0, 2, 1), ([2, 2], 0, 48, 64, 1, 1), ([1] * 1024, 700, 32, 64, 3, 1),
+    ([7000, 5000, 6000], 5, 1552, 32, 4000, 1), ([7000, 5000, 6000], 2, 1552, 512, 9000, 1),
+    ([7000, 5000, 6000], 0, 1552, 288, 2, 1), ([7000, 5000, 6000], 9000, 1552, 0, 2, 1)])
 def test_ragged_exact(counts, T, N, K, k, align, kind):
-    say("mxfp4 ragged", counts, T, N, K, k, align, kind)
+    """Few tokens chosen often, holes, a plan's alignment, no contraction, no tokens, the most experts, big tiles of
+    fewer scales than they read at once."""
+    say("mxfp4 ragged", len(counts), T, N, K, k, align, kind)
     a, sa = exact_operand((T, K), kind, 5)
     b, sb = exact_operand((len(counts), N, K), "e2m1", 6)
-    offsets, rows = ragged(counts, T, k, align, 7)
-    cap = rows.numel()
-    out, bf = empty(cap, N, dtype=torch.float32), empty(cap, N, dtype=torch.bfloat16)
-    bsq.bsq_moe_matmul_mxfp4(a, sa, b, sb, offsets, out, rows=rows, k=k)
-    bsq.bsq_moe_matmul_mxfp4(a, sa, b, sb, offsets, bf, rows=rows, k=k)
-    want = torch.zeros(cap, N, dtype=torch.float64, device="cuda")
-    ends, at, x = offsets.tolist(), rows.long(), decode(a, sa)
-    for e in range(len(counts)):
-        r = at[ends[e]:ends[e + 1]]
-        want[ends[e]:ends[e + 1]] = torch.where((r >= 0)[:, None], x[r.clamp_min(0) // k], 0.0) @ decode(b[e], sb[e]).t()
-    assert torch.equal(out.double(), want), int((out.double() != want).sum())
-    assert torch.equal(bf, want.float().bfloat16())
+    offsets, rows = ragged(counts, max(T, 1), k, align, 7)
+    args = (a, sa, b, sb, offsets, rows, rows.numel(), k)
+    want = experts_reference(*args)
+    assert torch.equal(experts(*args, torch.float32).double(), want)
+    assert torch.equal(experts(*args, torch.bfloat16), want.float().bfloat16())
 
 
 def test_ragged_own_rows():
@@ -259,4 +278,21 @@ def test_ragged_own_rows():
     want = torch.zeros(60, 48, dtype=torch.float64, device="cuda")
     want[:20] = x[:20] @ decode(b[0], sb[0]).t()
     want[20:41] = x[20:41] @ decode(b[2], sb[2]).t()
+    assert torch.equal(out.double(), want)
+
+
+@pytest.mark.parametrize("T, K", [(5, 32), (0, 32), (15, 32), (16, 32), (3, 256), (1, 512)])
+def test_ragged_own_rows_past_few_tokens(T, K):
+    """Segments of thousands of rows, of which A has the first few."""
+    say("mxfp4 ragged", T, K)
+    cap, N, ends = 18000, 1552, [2, 7000, 18000]
+    a, sa = exact_operand((T, K), "e2m1", 8)
+    b, sb = exact_operand((3, N, K), "e2m1", 9)
+    out = empty(cap, N, dtype=torch.float32)
+    bsq.bsq_moe_matmul_mxfp4(a, sa, b, sb, torch.tensor([0] + ends, dtype=torch.int32, device="cuda"), out)
+    want = torch.zeros(cap, N, dtype=torch.float64, device="cuda")
+    if T:
+        x = decode(a, sa)
+        want[:min(T, 2)] = x[:2] @ decode(b[0], sb[0]).t()
+        want[2:max(T, 2)] = x[2:] @ decode(b[1], sb[1]).t()
     assert torch.equal(out.double(), want)
