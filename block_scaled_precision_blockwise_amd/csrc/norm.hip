@@ -193,7 +193,9 @@ __device__ __forceinline__ void put_codes(NormCode code, uint8_t* codes, uint8_t
 
 // ---------------------------------------------------------------- forward --
 // Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
-// gamma and beta in registers, the next one's load under way.
+// gamma and beta in registers, the next one's load under way.  16384 x 4096
+// bfloat16 to bfloat16 and e4m3 61-69 us, 5.0-5.5 TB/s (a copy reaches 5.1);
+// one row 2.7 us.
 template <int BF16, int VEC, int NT, int P>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;  // of a workgroup
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
 // Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
 // the next one's loads under way while a row is summed and written.  Two rows
 // of 256 threads to a workgroup halve the groups' sums: 16384 x 4096 71 + 5 us
-// against 73 + 7.
+// against 73 + 7, 5.9 TB/s.
 template <int NT>
 constexpr int rows_of = NT < 256 ? 256 / NT : NT == 256 ? 2 : 1;
 template <int BF16, int VEC, int NT, int P>
