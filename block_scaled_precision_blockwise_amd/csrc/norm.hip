@@ -509,17 +509,19 @@ bsq_status launch_norm_backward(const NormBackwardLaunch& L, hipStream_t st) {
   int groups = 0;
   bsq_status s = BSQ_OK;
   if (L.R > 0 && L.C > kInRegisters) {
+    if (weights) {  // first: dx may take the place of x or dy
+      groups = int(L.R < 32 ? L.R : 32);
+      const dim3 g = dim3(unsigned(up_to(L.C, 256) * groups));
+      if (L.bf16) hipLaunchKernelGGL((k_norm_dw_long<1>), g, 256, 0, st, L, groups);
+      else hipLaunchKernelGGL((k_norm_dw_long<0>), g, 256, 0, st, L, groups);
+      s = launch_status("norm_backward (weights)");
+      if (s != BSQ_OK) return s;
+    }
     s = in_parts(L.R, kLaunchGroups / 2, [&](int64_t first, int64_t n) {
       if (L.bf16) hipLaunchKernelGGL((k_norm_dx_long<1>), dim3(unsigned(n)), kLong, 0, st, L, first);
       else hipLaunchKernelGGL((k_norm_dx_long<0>), dim3(unsigned(n)), kLong, 0, st, L, first);
       return launch_status("norm_backward");
     });
-    if (s != BSQ_OK || !weights) return s;
-    groups = int(L.R < 32 ? L.R : 32);
-    const dim3 g = dim3(unsigned(up_to(L.C, 256) * groups));
-    if (L.bf16) hipLaunchKernelGGL((k_norm_dw_long<1>), g, 256, 0, st, L, groups);
-    else hipLaunchKernelGGL((k_norm_dw_long<0>), g, 256, 0, st, L, groups);
-    s = launch_status("norm_backward");
   } else if (L.R > 0) {
     s = with_shape(L.C, [&](auto nt, auto p) {
       constexpr int NT = decltype(nt)::value, P = decltype(p)::value, kRows = rows_of<NT>;

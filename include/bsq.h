@@ -550,7 +550,7 @@ typedef enum bsq_norm {
  * eps), y = (x - mean) rstd gamma + beta, in float32.
  *   x      [R, C] of x_dtype (BSQ_F32 or BSQ_BF16)
  *   gamma, beta  float32 [C], or NULL (1 and 0)
- *   y      [R, C] of x_dtype (out), or NULL
+ *   y      [R, C] of x_dtype (out; may be x itself), or NULL
  *   codes, scales  y (before its rounding to x_dtype) quantized along rows, or
  *          both NULL: code_dtype BSQ_E4M3 or BSQ_E5M2, codes [R, C], as
  *          bsq_quant_mx; or BSQ_E2M1, codes [R, C / 2], as bsq_quant_fp4
@@ -568,7 +568,8 @@ bsq_status bsq_norm_mx(int64_t R, int64_t C, const void* x, int x_dtype, int kin
 /* Gradients of bsq_norm_mx: with xn = (x - mean) rstd and d = dy gamma,
  * dx = rstd (d - xn sum(d xn) / C - sum(d) / C), without the last term for
  * BSQ_RMS_NORM; dgamma = sum over rows of dy xn, dbeta = sum over rows of dy.
- *   x, dy, dx  [R, C] of x_dtype;  gamma float32 [C] or NULL (1)
+ *   x, dy, dx  [R, C] of x_dtype, dx may be x or dy itself;  gamma float32 [C]
+ *              or NULL (1)
  *   mean (NULL with BSQ_RMS_NORM), rstd  float32 [R], as bsq_norm_mx gave them
  *   dgamma, dbeta  float32 [C] (out), or NULL; zeros where R is 0
  *   workspace  at least bsq_norm_backward_workspace_bytes(R, C) bytes, for

@@ -183,3 +183,33 @@ def test_infinities_and_nan_show_in_their_row_alone(C):
         assert torch.isnan(y[r]).all()
         if coded:
             assert bool((scales.view(u8)[r] == 255).all())
+
+
+@pytest.mark.parametrize("dt", [f32, bf16])
+@pytest.mark.parametrize("R, C", [(5, 96), (2100, 64), (7, 1001), (700, 4096), (3, 16384), (40, 16416), (3, 20001)])
+def test_in_place(R, C, dt):
+    """y in x's place, dx in x's or dy's: the same bytes as elsewhere."""
+    say("norm in place", R, C, dt)
+    x, dy, gamma, beta = inputs(R, C, dt, R + C)
+    x, dy = (torch.from_numpy(v).to("cuda", dt) for v in (x, dy))
+    gd, bd = (torch.from_numpy(v).to("cuda", f32) for v in (gamma, beta))
+    coded = C % 32 == 0
+    new = lambda: (empty(R, C, dtype=E4M3), empty(R, C // 32, dtype=E8M0)) if coded else (None, None)  # noqa: E731
+    (q, s), (qi, si) = new(), new()
+    y, yi, mean, rstd = empty(R, C, dtype=dt), x.clone(), empty(R, dtype=f32), empty(R, dtype=f32)
+    bsq.bsq_norm_mx(x, y=y, codes=q, scales=s, gamma=gd, beta=bd, mean=mean, rstd=rstd)
+    bsq.bsq_norm_mx(yi, y=yi, codes=qi, scales=si, gamma=gd, beta=bd)
+    assert torch.equal(y, yi)
+    if coded:
+        assert torch.equal(q.view(u8), qi.view(u8)) and torch.equal(s.view(u8), si.view(u8))
+    space = empty(bsq.bsq_norm_backward_workspace_bytes(R, C))
+    outs = []
+    for place in ("own", "x", "dy"):
+        xi, di = x.clone(), dy.clone()
+        dx = {"own": empty(R, C, dtype=dt), "x": xi, "dy": di}[place]
+        dg, db = empty(C, dtype=f32), empty(C, dtype=f32)
+        bsq.bsq_norm_backward(xi, di, rstd, dx, mean=mean, gamma=gd, dgamma=dg, dbeta=db, workspace=space)
+        outs.append((dx, dg, db))
+    for got in outs[1:]:
+        for a, b in zip(got, outs[0]):
+            assert torch.equal(a, b)
