@@ -146,13 +146,15 @@ __device__ __forceinline__ void store4(const Mx4Args& p, int64_t at, v4f v) {
 // Tiles of 16 MB rows x 16 NB columns, where the weights' bytes are most of the
 // work.  W waves share a tile's contraction, each with U chunks of 128 at a
 // time, straight from memory to the operand registers, and their sums are
-// joined through LDS in the waves' order.  Bound by the latency of a launch and
+// joined through LDS in the waves' order.  U is 8 where every wave has as many
+// (1 x 4096 x 14336 9.2 us / 10.8 with 4, x 4096 4.9 / 5.1), else 4 (8 x 2048 x
+// 416 3.0 / 3.2, 1 x 8192 x 2880 5.8 / 6.0).  Bound by the latency of a launch and
 // of memory: one row of 8192 x 4096 5.6 us (17.8 MB, 3.2 TB/s), of 4096 x 4096
 // 4.0 us.  Tiles of 64 x 64 this way are slower than through LDS (1024 x 1024 x
 // 16384 40 us / 22): a load's 16 rows of 64 bytes are half lines.
-template <int FA, int MB, int NB, int W>
+template <int FA, int MB, int NB, int W, int U>
 __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
-  constexpr int TM = 16 * MB, TN = 16 * NB, U = 4;
+  constexpr int TM = 16 * MB, TN = 16 * NB;
   constexpr int kPitch = TN + 4;  // of a row of sums, padded
   __shared__ __attribute__((aligned(16))) float red[W][TM][kPitch];
   __shared__ int src[TM];
@@ -189,21 +191,22 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
     int sb[U][NB], sa[U][MB];
     const bool whole = 4 * (c0 + U) <= nb;
     if (whole) {
-      // a row's 16 scales at once: a load touches a line per row however little
+      // a row's scales 16 at a time: a load touches a line per row however little
       // it takes of it
-      auto scales = [&](const uint8_t* row) {
-        uint4 v;
-        __builtin_memcpy(&v, row + 4 * c0, 16);
-        return v;
+      struct Scales {
+        uint32_t v[U];
       };
-      uint4 vb[NB], va[MB];
+      auto scales = [&](const uint8_t* row) {
+        Scales s;
+        __builtin_memcpy(&s, row + 4 * c0, 4 * U);
+        return s;
+      };
+      Scales vb[NB], va[MB];
 #pragma unroll
       for (int j = 0; j < NB; ++j) vb[j] = scales(psb[j]);
 #pragma unroll
       for (int i = 0; i < MB; ++i) va[i] = scales(psa[i]);
-      auto spread = [&](const uint4& v, int u) {
-        return int((u == 0 ? v.x : u == 1 ? v.y : u == 2 ? v.z : v.w) >> (8 * g));
-      };
+      auto spread = [&](const Scales& s, int u) { return int(s.v[u] >> (8 * g)); };
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -1059,12 +1062,12 @@ void launch_timed(Kernel k, dim3 grid, dim3 block, hipStream_t st, const Mx4Args
 // Tile rows of all segments at most, or of the batch.
 int64_t tile_rows(const Mx4Launch& L, int tm) { return L.offsets ? L.cap / tm + L.E + 1 : up_to(L.T, tm) * L.E; }
 
-template <int MB, int NB, int W>
+template <int MB, int NB, int W, int U>
 bsq_status launch_few(const Mx4Launch& L, Mx4Args a, hipStream_t st) {
   return in_parts(tile_rows(L, 16 * MB) * up_to(L.N, 16 * NB), kLaunchGroups, [&](int64_t first, int64_t n) {
     a.first = int(first);
     return with_code(L.a, [&](auto fa) {
-      launch_timed(k_mx4_few<decltype(fa)::value, MB, NB, W>, dim3(unsigned(n)), dim3(64 * W), st, a);
+      launch_timed(k_mx4_few<decltype(fa)::value, MB, NB, W, U>, dim3(unsigned(n)), dim3(64 * W), st, a);
       return launch_status("mx4 product (few rows)");
     });
   });
@@ -1103,9 +1106,9 @@ bsq_status launch_mx4_product(const Mx4Launch& L, hipStream_t st) {
                   L.out_bf16 ? 1 : 0, 0};
   const int64_t pitch_a = L.a == Code4::e2m1 ? L.K / 2 : L.K;
   switch (mx4_tile(Mx4Size{L.offsets != nullptr, L.rows != nullptr, L.T, L.cap, L.E, L.k, L.N, L.K})) {
-    case Mx4Tile::few16x16: return launch_few<1, 1, 4>(L, a, st);
-    case Mx4Tile::few16x32: return launch_few<1, 2, 4>(L, a, st);
-    case Mx4Tile::few32x32: return launch_few<2, 2, 4>(L, a, st);
+    case Mx4Tile::few16x16: return L.K >= 128 * 8 * 4 ? launch_few<1, 1, 4, 8>(L, a, st) : launch_few<1, 1, 4, 4>(L, a, st);
+    case Mx4Tile::few16x32: return L.K >= 128 * 8 * 4 ? launch_few<1, 2, 4, 8>(L, a, st) : launch_few<1, 2, 4, 4>(L, a, st);
+    case Mx4Tile::few32x32: return launch_few<2, 2, 4, 4>(L, a, st);
     case Mx4Tile::t32x64: return launch_tile<1, 4, 2, 1, 3, 1, 1>(L, a, st);
     case Mx4Tile::t32x64g2: return launch_tile<1, 4, 2, 1, 2, 2, 2>(L, a, st);
     case Mx4Tile::t64x64g2: return launch_tile<2, 2, 2, 2, 3, 2, 1>(L, a, st);

@@ -182,7 +182,7 @@ def test_dense_exact_small(B, M, N, K, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B, M, N, K", [(1, 1, 272, 4096), (2, 33, 144, 288), (1, 257, 528, 1312), (1, 400, 1200, 1312),
+@pytest.mark.parametrize("B, M, N, K", [(1, 1, 272, 4096), (1, 3, 272, 9312), (1, 16, 4112, 8192), (2, 33, 144, 288), (1, 257, 528, 1312), (1, 400, 1200, 1312),
                                         (1, 1000, 1504, 1056), (1, 1700, 2000, 1056), (1, 4100, 3600, 1056)])
 def test_dense_any_codes(B, M, N, K, kind):
     say("mxfp4 dense, any codes", B, M, N, K, kind)
