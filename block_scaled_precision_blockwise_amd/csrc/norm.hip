@@ -76,6 +76,12 @@ __device__ __forceinline__ void sum_over(float& a, float& b, float* red) {
   }
 }
 
+// 1 / sqrt(var + eps); NaN where the variance is infinite: an infinity in the row, which makes the whole row NaN (of
+// rms norm the other values would become zeros).
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  return var < __builtin_inff() ? 1.0f / sqrtf(var + eps) : __builtin_nanf("");
+}
+
 template <int BF16>
 __device__ __forceinline__ float load1(const void* p, int64_t at) {
   return BF16 ? decode_bf16(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
         x[p][i] = col<NT, VEC>(t, p, i) < C ? x[p][i] - mean : 0.f;
         s += x[p][i] * x[p][i];
       }
-    const float rstd = 1.0f / sqrtf(sum_over<NT>(s, red[buf][1]) / float(C) + a.eps);
+    const float rstd = rstd_of(sum_over<NT>(s, red[buf][1]) / float(C), a.eps);
     if (t == 0 && in) {
       if (a.mean != nullptr) a.mean[r] = mean;
       if (a.rstd != nullptr) a.rstd[r] = rstd;
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
     const float d = load1<BF16>(a.x, row0 + c) - mean;
     s += d * d;
   }
-  const float rstd = 1.0f / sqrtf(sum_over<kLong>(s, red[1]) / float(a.C) + a.eps);
+  const float rstd = rstd_of(sum_over<kLong>(s, red[1]) / float(a.C), a.eps);
   if (threadIdx.x == 0) {
     if (a.mean != nullptr) a.mean[r] = mean;
     if (a.rstd != nullptr) a.rstd[r] = rstd;

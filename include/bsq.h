@@ -556,8 +556,8 @@ typedef enum bsq_norm {
  *          bsq_quant_mx; or BSQ_E2M1, codes [R, C / 2], as bsq_quant_fp4
  *          (BSQ_MXFP4); scales E8M0 [R, C / 32]
  *   mean, rstd   float32 [R] (out), or NULL; the gradient reads them
- * Infinities and NaN in a row make it NaN: in y, in e4m3 and e5m2 codes, and as
- * the NaN scale of e2m1 codes.
+ * Infinities and NaN in a row make all of it NaN, of either kind of norm: in y
+ * and rstd, in e4m3 and e5m2 codes, and as the NaN scales of e2m1 codes.
  * Rules: with codes C % 32 == 0 (else SHAPE); C <= 2^24, eps >= 0 (else
  * UNSUPPORTED).  Rows of up to 16384 are held in registers, longer ones are
  * read three times. */
