@@ -7,7 +7,9 @@
 //   term for layer norm only; dgamma = sum over rows of dy xn, dbeta of dy
 //
 // in float32.  The variance is summed from x - mean in a second pass over the
-// registers, so that rows far from zero lose nothing.  Codes are of the
+// registers, so that rows far from zero do not cancel.  Where a sum or a square
+// passes float32, or squares are too small for it, the row is taken again times
+// the power of two that brings its largest value below 1.  Codes are of the
 // float32 y, before y's own rounding.
 //
 // Bound by memory.  A row stays in the registers of NT threads, P times eight
@@ -76,10 +78,40 @@ __device__ __forceinline__ void sum_over(float& a, float& b, float* red) {
   }
 }
 
-// 1 / sqrt(var + eps); NaN where the variance is infinite: an infinity in the row, which makes the whole row NaN (of
-// rms norm the other values would become zeros).
-__device__ __forceinline__ float rstd_of(float var, float eps) {
-  return var < __builtin_inff() ? 1.0f / sqrtf(var + eps) : __builtin_nanf("");
+// Whether float32 held the sums of a row: the variance is finite, and the
+// squares (each off by 2^-150 at most) are not lost beside it and eps.
+__device__ __forceinline__ bool held(float var, float eps) {
+  return var < __builtin_inff() && var + eps >= 0x1p-100f;
+}
+// The power of two k for a row that it did not hold: the largest magnitude (its
+// bits are `top`) times 2^-k is below 1, and so is eps times 2^-2k.
+__device__ __forceinline__ int exponent_of(uint32_t top, float eps) {
+  const float m = fmaxf(__uint_as_float(top), eps < __builtin_inff() ? sqrtf(eps) : 0.f);
+  return m > 0.f ? __builtin_amdgcn_frexp_expf(m) : 0;
+}
+// 1 / sqrt of such a row's variance and eps, both times 2^-2k.  A row of one
+// value has zeros to normalise, beside which eps counts however small it is: it
+// goes on as it was.
+__device__ __forceinline__ float rstd_again(float var, float eps, float& mean, int& k) {
+  if (var == 0.f) {
+    mean = ldexpf(mean, k);
+    k = 0;
+  }
+  return 1.0f / sqrtf(var + ldexpf(eps, -2 * k));
+}
+constexpr uint32_t kInfinity = 0x7F800000u;
+// Largest of magnitudes' bits over NT threads, left in each.
+template <int NT>
+__device__ __forceinline__ uint32_t max_over(uint32_t v, float* red) {
+  v = group_max_bits<64>(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = __uint_as_float(v);
+    __syncthreads();
+    v = 0u;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) v = max(v, __float_as_uint(red[i]));
+  }
+  return v;
 }
 
 template <int BF16>
@@ -205,7 +237,7 @@ __device__ __forceinline__ void put_codes(NormCode code, uint8_t* codes, uint8_t
 template <int BF16, int VEC, int NT, int P>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;  // of a workgroup
-  __shared__ float red[2][2][NT > 64 ? NT / 64 : 1];
+  __shared__ float red[2][2][NT > 64 ? NT / 64 : 1], again[3][NT > 64 ? NT / 64 : 1];
   const int t = threadIdx.x % NT, sub = threadIdx.x / NT, C = int(a.C);
   const int64_t step = int64_t(gridDim.x) * kRows;
   saturate_fp8();
@@ -246,10 +278,43 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
         x[p][i] = col<NT, VEC>(t, p, i) < C ? x[p][i] - mean : 0.f;
         s += x[p][i] * x[p][i];
       }
-    const float rstd = rstd_of(sum_over<NT>(s, red[buf][1]) / float(C), a.eps);
+    const float var = sum_over<NT>(s, red[buf][1]) / float(C);
+    float rstd = 1.0f / sqrtf(var + a.eps);
+    int k = 0;
+    if (!held(var, a.eps)) {  // of all threads of the row; x is read again, and y not yet written
+      uint32_t top = 0u;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        load_row<BF16, NT, VEC>(a.x, (in ? r : a.R - 1) * a.C, t, p, C, x[p]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, abs_bits(x[p][i]));
+      }
+      top = max_over<NT>(top, again[0]);
+      rstd = __builtin_nanf("");  // an infinity or NaN makes the whole row NaN
+      if (top < kInfinity) {
+        k = exponent_of(top, a.eps);
+        mean = s = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s += x[p][i] = ldexpf(x[p][i], -k);
+        // no further out than the row's values, so that 2^k times it is finite
+        const float most = ldexpf(__uint_as_float(top), -k);
+        if (!a.rms) mean = __builtin_amdgcn_fmed3f(sum_over<NT>(s, again[1]) / float(C), -most, most);
+        s = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[p][i] = col<NT, VEC>(t, p, i) < C ? x[p][i] - mean : 0.f;
+            s += x[p][i] * x[p][i];
+          }
+        rstd = rstd_again(sum_over<NT>(s, again[2]) / float(C), a.eps, mean, k);
+      }
+    }
     if (t == 0 && in) {
-      if (a.mean != nullptr) a.mean[r] = mean;
-      if (a.rstd != nullptr) a.rstd[r] = rstd;
+      if (a.mean != nullptr) a.mean[r] = ldexpf(mean, k);
+      if (a.rstd != nullptr) a.rstd[r] = ldexpf(rstd, -k);
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -266,26 +331,45 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
 constexpr int kLong = 1024;
 template <int BF16>
 __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first) {
-  __shared__ float red[2][kLong / 64];
+  __shared__ float red[5][kLong / 64];
   const int64_t r = first + blockIdx.x, row0 = r * a.C;
   saturate_fp8();
-  float mean = 0.f, s = 0.f;
-  if (!a.rms) {
-    for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += load1<BF16>(a.x, row0 + c);
-    mean = sum_over<kLong>(s, red[0]) / float(a.C);
-    s = 0.f;
+  int k = 0;  // the row is taken times 2^-k
+  auto at = [&](int64_t c) { return ldexpf(load1<BF16>(a.x, row0 + c), -k); };
+  float mean = 0.f;
+  auto variance = [&](float* red_mean, float* red_var) {
+    float s = 0.f;
+    if (!a.rms) {
+      for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += at(c);
+      mean = sum_over<kLong>(s, red_mean) / float(a.C);
+      s = 0.f;
+    }
+    for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
+      const float d = at(c) - mean;
+      s += d * d;
+    }
+    return sum_over<kLong>(s, red_var) / float(a.C);
+  };
+  const float var = variance(red[0], red[1]);
+  float rstd = 1.0f / sqrtf(var + a.eps);
+  if (!held(var, a.eps)) {
+    uint32_t top = 0u;
+    for (int64_t c = threadIdx.x; c < a.C; c += kLong) top = max(top, abs_bits(at(c)));
+    top = max_over<kLong>(top, red[2]);
+    rstd = __builtin_nanf("");  // an infinity or NaN makes the whole row NaN
+    if (top < kInfinity) {
+      k = exponent_of(top, a.eps);
+      const float scaled = variance(red[3], red[4]), most = ldexpf(__uint_as_float(top), -k);
+      mean = __builtin_amdgcn_fmed3f(mean, -most, most);  // so that 2^k times it is finite
+      rstd = rstd_again(scaled, a.eps, mean, k);
+    }
   }
-  for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
-    const float d = load1<BF16>(a.x, row0 + c) - mean;
-    s += d * d;
-  }
-  const float rstd = rstd_of(sum_over<kLong>(s, red[1]) / float(a.C), a.eps);
   if (threadIdx.x == 0) {
-    if (a.mean != nullptr) a.mean[r] = mean;
-    if (a.rstd != nullptr) a.rstd[r] = rstd;
+    if (a.mean != nullptr) a.mean[r] = ldexpf(mean, k);
+    if (a.rstd != nullptr) a.rstd[r] = ldexpf(rstd, -k);
   }
   auto value = [&](int64_t c) {
-    const float xn = (load1<BF16>(a.x, row0 + c) - mean) * rstd;
+    const float xn = (at(c) - mean) * rstd;
     return xn * (a.gamma != nullptr ? a.gamma[c] : 1.f) + (a.beta != nullptr ? a.beta[c] : 0.f);
   };
   if (a.codes == nullptr) {

@@ -556,6 +556,8 @@ typedef enum bsq_norm {
  *          bsq_quant_mx; or BSQ_E2M1, codes [R, C / 2], as bsq_quant_fp4
  *          (BSQ_MXFP4); scales E8M0 [R, C / 32]
  *   mean, rstd   float32 [R] (out), or NULL; the gradient reads them
+ * A row may hold any finite values, also where their sum or squares pass float32
+ * (rstd may then be subnormal, or infinite for rows below 2^-128 without eps).
  * Infinities and NaN in a row make all of it NaN, of either kind of norm: in y
  * and rstd, in e4m3 and e5m2 codes, and as the NaN scales of e2m1 codes.
  * Rules: with codes C % 32 == 0 (else SHAPE); C <= 2^24, eps >= 0 (else

@@ -1,11 +1,13 @@
-"""The norm on rows that hold infinities or NaN: every kernel, both kinds, every operand."""
+"""The norm on rows that hold infinities or NaN, and on rows whose sums or squares do not fit float32: every kernel,
+both kinds."""
+import numpy as np
 import pytest
 import torch
 
 import block_scaled_precision_blockwise_amd as bsq
 from gpu_helpers import say
 from test_gpu_mx4 import E4M3, E5M2, E8M0, empty, gen, u8
-from test_gpu_norm import KIND
+from test_gpu_norm import KIND, U, bounds, roundings
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,64 @@ def test_infinities_and_nan_make_their_whole_row_nan(C, code, dt, rms):
             assert bool((s.view(u8) == 255).all()), r
         elif code != "none":
             assert bool(torch.isnan(q.float()).all()), r
+
+
+# ------------------------------------------- rows that pass float32 on the way --
+
+ROWS = ("largest", "one against the rest", 100, 64, 0, -62, -90, -118)  # of which powers of two
+
+
+def rows(C, dt, seed):
+    """Rows of every magnitude."""
+    g = np.random.default_rng(seed)
+    x = g.standard_normal((len(ROWS), C))
+    for r, e in enumerate(ROWS):
+        if e == "largest":
+            x[r] = g.uniform(-3.3e38, 3.3e38, C)
+        elif e == "one against the rest":
+            x[r], x[r, C // 2] = -3.3e38, 3.3e38
+        else:
+            x[r] = (x[r] + 0.25) * 2.0 ** e
+    return torch.from_numpy(x).to(dt).double().numpy()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-5, 1e-30])
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("dt", [f32, bf16])
+@pytest.mark.parametrize("C", [5, 64, 512, 1000, 2048, 4096, 8192, 9999, 16384, 16416, 20001])
+def test_rows_whose_sums_or_squares_pass_float32(C, dt, rms, eps):
+    """Squares above 2^128 and below 2^-149, sums and differences above the largest: the bounds of other rows hold."""
+    say("norm of large and small rows", C, dt, rms, eps)
+    eps = float(np.float32(eps))
+    x = rows(C, dt, C)
+    R = x.shape[0]
+    g = np.random.default_rng(1)
+    w = lambda v: v.astype(np.float32).astype(np.float64)  # noqa: E731
+    gamma, beta = w(1 + 0.3 * g.standard_normal(C)), w(0.3 * g.standard_normal(C))
+    dev = lambda v, t=f32: torch.from_numpy(v).to("cuda", t)  # noqa: E731
+    xd, gd = dev(x, dt), dev(gamma)
+    y, mean, rstd = empty(R, C, dtype=dt), empty(R, dtype=f32), empty(R, dtype=f32)
+    bsq.bsq_norm_mx(xd, y=y, gamma=gd, beta=dev(beta), mean=mean, rstd=rstd, eps=eps, kind=KIND[rms])
+    want, tol = bounds(x, gamma, beta, rms, eps)
+    for got, v, t, kind, what in ((y, want[0], tol[1], dt, "y"), (mean, want[1], tol[2], f32, "mean"),
+                                  # rstd of the largest rows is subnormal
+                                  (rstd, want[2], tol[3] + 2.0 ** -149, f32, "rstd")):
+        for r in range(R):  # what `held` adds for all is too much for some
+            err, t_r = np.abs(got[r].double().cpu().numpy() - v[r]), t[r] * 1.01
+            t_r = t_r + (2.0 ** -8 * (np.abs(v[r]) + t_r) if kind == bf16 else 0.0)
+            assert np.all(err <= t_r), (what, ROWS[r], float(np.max(err - t_r)))
+    # in place: the row is read again
+    xi = xd.clone()
+    bsq.bsq_norm_mx(xi, y=xi, gamma=gd, beta=dev(beta), eps=eps, kind=KIND[rms])
+    assert same(xi, y)
+    # every value the largest, and zeros
+    big = float(torch.finfo(dt).max)
+    x = torch.full((2, C), big, device="cuda", dtype=dt)
+    x[1] = 0
+    bsq.bsq_norm_mx(x, y=y[:2], mean=mean[:2], rstd=rstd[:2], eps=1e-5, kind=KIND[rms])
+    n = roundings(C)
+    if rms:
+        assert bool(((y[0].double() - 1).abs() <= (n + 8) * U + (2.0 ** -8 if dt == bf16 else 0)).all())
+    else:
+        assert abs(float(mean[0]) / big - 1) <= (n + 1) * U and bool(torch.isfinite(y[0]).all())
+    assert not y[1].any() and abs(float(rstd[1]) * 1e-5 ** 0.5 - 1) < 1e-6
