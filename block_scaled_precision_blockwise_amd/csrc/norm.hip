@@ -390,6 +390,15 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
 }
 
 // --------------------------------------------------------------- backward --
+// (x - mean) rstd, of halves where the row is so large that the difference may
+// pass float32.
+struct Centre {
+  float h, mean, rstd;
+  __device__ __forceinline__ Centre(float m, float r)
+      : h(r < 0x1p-64f ? 0.5f : 1.0f), mean(m * h), rstd(r < 0x1p-64f ? r + r : r) {}
+  __device__ __forceinline__ float operator()(float x) const { return fmaf(x, h, -mean) * rstd; }
+};
+
 // Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
 // the next one's loads under way while a row is summed and written.  Two rows
 // of 256 threads to a workgroup halve the groups' sums: 16384 x 4096 71 + 5 us
@@ -435,7 +444,8 @@ __global__ void __launch_bounds__(NT * rows_of<NT>) k_norm_dx(NormBackwardLaunch
       xr[p].get(x[p]);
       dr[p].get(dy[p]);
     }
-    const float mean = mean_r, rstd = rstd_r;
+    const Centre norm(mean_r, rstd_r);
+    const float rstd = rstd_r;
     if (r0 + step < a.R) load(r + step);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(NT * rows_of<NT>) k_norm_dx(NormBackwardLaunch
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // columns and rows that are not there have dy 0
-        const float d = in ? dy[p][i] : 0.f, xn = in ? (x[p][i] - mean) * rstd : 0.f;
+        const float d = in ? dy[p][i] : 0.f, xn = in ? norm(x[p][i]) : 0.f;
         x[p][i] = xn;
         sg[p][i] += d * xn;
         sb[p][i] += d;
@@ -498,11 +508,12 @@ template <int BF16>
 __global__ void __launch_bounds__(kLong) k_norm_dx_long(NormBackwardLaunch a, int64_t first) {
   __shared__ float red[2 * kLong / 64];
   const int64_t r = first + blockIdx.x, row0 = r * a.C;
-  const float mean = a.rms ? 0.f : a.mean[r], rstd = a.rstd[r];
+  const float rstd = a.rstd[r];
+  const Centre norm(a.rms ? 0.f : a.mean[r], rstd);
   float s1 = 0.f, s2 = 0.f;
   for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
     const float d = load1<BF16>(a.dy, row0 + c) * (a.gamma != nullptr ? a.gamma[c] : 1.f);
-    s1 += d * ((load1<BF16>(a.x, row0 + c) - mean) * rstd);
+    s1 += d * norm(load1<BF16>(a.x, row0 + c));
     s2 += d;
   }
   sum_over<kLong>(s1, s2, red);
@@ -510,7 +521,7 @@ __global__ void __launch_bounds__(kLong) k_norm_dx_long(NormBackwardLaunch a, in
   s2 = a.rms ? 0.f : s2 / float(a.C);
   for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
     const float d = load1<BF16>(a.dy, row0 + c) * (a.gamma != nullptr ? a.gamma[c] : 1.f);
-    const float xn = (load1<BF16>(a.x, row0 + c) - mean) * rstd;
+    const float xn = norm(load1<BF16>(a.x, row0 + c));
     store1<BF16>(a.dx, row0 + c, rstd * (d - xn * s1 - s2));
   }
 }
@@ -523,7 +534,7 @@ __global__ void __launch_bounds__(256) k_norm_dw_long(NormBackwardLaunch a, int 
   float sg = 0.f, sb = 0.f;
   for (int64_t r = gr; r < a.R; r += groups) {
     const float d = load1<BF16>(a.dy, r * a.C + c);
-    sg += d * ((load1<BF16>(a.x, r * a.C + c) - (a.rms ? 0.f : a.mean[r])) * a.rstd[r]);
+    sg += d * Centre(a.rms ? 0.f : a.mean[r], a.rstd[r])(load1<BF16>(a.x, r * a.C + c));
     sb += d;
   }
   a.space[gr * a.C + c] = sg;

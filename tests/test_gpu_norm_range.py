@@ -6,8 +6,9 @@ import torch
 
 import block_scaled_precision_blockwise_amd as bsq
 from gpu_helpers import say
+from oracle import norm
 from test_gpu_mx4 import E4M3, E5M2, E8M0, empty, gen, u8
-from test_gpu_norm import KIND, U, bounds, roundings
+from test_gpu_norm import KIND, U, bounds, held, roundings
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,46 @@ def test_rows_whose_sums_or_squares_pass_float32(C, dt, rms, eps):
     else:
         assert abs(float(mean[0]) / big - 1) <= (n + 1) * U and bool(torch.isfinite(y[0]).all())
     assert not y[1].any() and abs(float(rstd[1]) * 1e-5 ** 0.5 - 1) < 1e-6
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("dt", [f32, bf16])
+@pytest.mark.parametrize("C", [5, 64, 512, 1000, 2048, 4096, 8192, 9999, 16384, 16416, 20001])
+def test_gradients_of_rows_whose_differences_pass_float32(C, dt, rms):
+    """x - mean above the largest, rstd next to the smallest: from the norm's own mean and rstd, dx to the bounds of other
+    rows, and the weights' gradients."""
+    say("gradients of large and small rows", C, dt, rms)
+    eps = 1e-30
+    x = rows(C, dt, C)
+    R = x.shape[0]
+    g = np.random.default_rng(2)
+    # of a size that brings dx, as large as dy / x, well inside float32
+    dy = g.standard_normal((R, C)) * 2.0 ** np.array([[62 if isinstance(e, str) else e // 2] for e in ROWS])
+    dy = torch.from_numpy(dy).to(dt).double().numpy()
+    gamma = (1 + 0.3 * g.standard_normal(C)).astype(np.float32).astype(np.float64)
+    dev = lambda v, t=f32: torch.from_numpy(v).to("cuda", t)  # noqa: E731
+    xd, gd = dev(x, dt), dev(gamma)
+    mean, rstd = empty(R, dtype=f32), empty(R, dtype=f32)
+    bsq.bsq_norm_mx(xd, mean=mean, rstd=rstd, eps=eps, kind=KIND[rms])
+    dx, dg, db = empty(R, C, dtype=dt), empty(C, dtype=f32), empty(C, dtype=f32)
+    bsq.bsq_norm_backward(xd, dev(dy, dt), rstd, dx, mean=None if rms else mean, gamma=gd, dgamma=dg, dbeta=db,
+                          workspace=empty(bsq.bsq_norm_backward_workspace_bytes(R, C)), kind=KIND[rms])
+    eps = float(np.float32(eps))
+    want, tol = bounds(x, gamma, 0 * gamma, rms, eps)
+    wx, wg, wb = norm.backward(x, dy, gamma, eps, rms)
+    n, r = roundings(C), want[2][:, None]
+    xn, d = (x - want[1][:, None]) * r, dy * gamma
+    t_r = tol[3][:, None] / r + 2.0 ** -149 / r  # rstd may be subnormal
+    t_xn = tol[0] * 1.01 + np.abs(xn) * 2.0 ** -149 / r
+    s1, s2 = (d * xn).mean(1, keepdims=True), (0 if rms else 1) * d.mean(1, keepdims=True)
+    t1 = (np.abs(d) * t_xn).mean(1, keepdims=True) + (n + 4) * U * np.abs(d * xn).mean(1, keepdims=True)
+    t2 = (n + 3) * U * np.abs(d).mean(1, keepdims=True)
+    inner = U * 4 * (np.abs(d) + np.abs(xn * s1) + np.abs(s2)) + t_xn * np.abs(s1) + (np.abs(xn) + t_xn) * t1 + t2
+    t_x = (r * inner * 1.01 + np.abs(wx) * (t_r + 2 * U)) * 1.02
+    t_x += 2.0 ** -8 * (np.abs(wx) + t_x) if dt == bf16 else 0.0
+    err = np.abs(dx.double().cpu().numpy() - wx)
+    for i in range(R):
+        assert np.all(err[i] <= t_x[i]), ("dx", ROWS[i], float((err[i] - t_x[i]).max()))
+    # sums over the rows: up to R of a group, 16 shares and their joining
+    held(dg, wg, (np.abs(dy) * t_xn).sum(0) + (R + 35) * U * np.abs(dy * xn).sum(0), f32, "dgamma")
+    held(db, wb, (R + 34) * U * np.abs(dy).sum(0), f32, "dbeta")
