@@ -78,16 +78,20 @@ __device__ __forceinline__ void sum_over(float& a, float& b, float* red) {
   }
 }
 
-// Whether float32 held the sums of a row: the variance is finite, and the
-// squares (each off by 2^-150 at most) are not lost beside it and eps.
-__device__ __forceinline__ bool held(float var, float eps) {
-  return var < __builtin_inff() && var + eps >= 0x1p-100f;
+constexpr uint32_t kInfinity = 0x7F800000u;
+// Whether float32 held the sums of a row, by its variance and eps (the same in
+// every lane): they are finite, and the squares (each off by 2^-150 at most) are
+// not lost beside them.
+__device__ __forceinline__ bool held(float v) {
+  constexpr uint32_t kLeast = 0x0D800000u;  // 2^-100
+  return __builtin_expect(uint32_t(__builtin_amdgcn_readfirstlane(int(__float_as_uint(v)))) - kLeast < kInfinity - kLeast, 1);
 }
 // The power of two k for a row that it did not hold: the largest magnitude (its
-// bits are `top`) times 2^-k is below 1, and so is eps times 2^-2k.
+// bits are `top`) times 2^-k is below 1, and so is eps times 2^-2k; 2^-k is a
+// float32.
 __device__ __forceinline__ int exponent_of(uint32_t top, float eps) {
   const float m = fmaxf(__uint_as_float(top), eps < __builtin_inff() ? sqrtf(eps) : 0.f);
-  return m > 0.f ? __builtin_amdgcn_frexp_expf(m) : 0;
+  return max(m > 0.f ? __builtin_amdgcn_frexp_expf(m) : 0, -126);
 }
 // 1 / sqrt of such a row's variance and eps, both times 2^-2k.  A row of one
 // value has zeros to normalise, beside which eps counts however small it is: it
@@ -99,7 +103,6 @@ __device__ __forceinline__ float rstd_again(float var, float eps, float& mean, i
   }
   return 1.0f / sqrtf(var + ldexpf(eps, -2 * k));
 }
-constexpr uint32_t kInfinity = 0x7F800000u;
 // Largest of magnitudes' bits over NT threads, left in each.
 template <int NT>
 __device__ __forceinline__ uint32_t max_over(uint32_t v, float* red) {
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
     const float var = sum_over<NT>(s, red[buf][1]) / float(C);
     float rstd = 1.0f / sqrtf(var + a.eps);
     int k = 0;
-    if (!held(var, a.eps)) {  // of all threads of the row; x is read again, and y not yet written
+    if (!held(var + a.eps)) {  // all threads of the row; x is read again, and y not yet written
       uint32_t top = 0u;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -334,32 +337,40 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
   __shared__ float red[5][kLong / 64];
   const int64_t r = first + blockIdx.x, row0 = r * a.C;
   saturate_fp8();
-  int k = 0;  // the row is taken times 2^-k
-  auto at = [&](int64_t c) { return ldexpf(load1<BF16>(a.x, row0 + c), -k); };
+  // `again`: the row is taken times 2^-k
+  constexpr std::false_type no{};
+  constexpr std::true_type yes{};
+  int k = 0;
+  float down = 1.f;
+  auto at = [&](int64_t c, auto again) {
+    const float x = load1<BF16>(a.x, row0 + c);
+    return decltype(again)::value ? x * down : x;
+  };
   float mean = 0.f;
-  auto variance = [&](float* red_mean, float* red_var) {
+  auto variance = [&](float* red_mean, float* red_var, auto again) {
     float s = 0.f;
     if (!a.rms) {
-      for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += at(c);
+      for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += at(c, again);
       mean = sum_over<kLong>(s, red_mean) / float(a.C);
       s = 0.f;
     }
     for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
-      const float d = at(c) - mean;
+      const float d = at(c, again) - mean;
       s += d * d;
     }
     return sum_over<kLong>(s, red_var) / float(a.C);
   };
-  const float var = variance(red[0], red[1]);
+  const float var = variance(red[0], red[3], no);
   float rstd = 1.0f / sqrtf(var + a.eps);
-  if (!held(var, a.eps)) {
+  if (!held(var + a.eps)) {
     uint32_t top = 0u;
-    for (int64_t c = threadIdx.x; c < a.C; c += kLong) top = max(top, abs_bits(at(c)));
-    top = max_over<kLong>(top, red[2]);
+    for (int64_t c = threadIdx.x; c < a.C; c += kLong) top = max(top, abs_bits(at(c, no)));
+    top = max_over<kLong>(top, red[1]);
     rstd = __builtin_nanf("");  // an infinity or NaN makes the whole row NaN
     if (top < kInfinity) {
       k = exponent_of(top, a.eps);
-      const float scaled = variance(red[3], red[4]), most = ldexpf(__uint_as_float(top), -k);
+      down = ldexpf(1.f, -k);
+      const float scaled = variance(red[2], red[4], yes), most = __uint_as_float(top) * down;
       mean = __builtin_amdgcn_fmed3f(mean, -most, most);  // so that 2^k times it is finite
       rstd = rstd_again(scaled, a.eps, mean, k);
     }
@@ -368,25 +379,29 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
     if (a.mean != nullptr) a.mean[r] = ldexpf(mean, k);
     if (a.rstd != nullptr) a.rstd[r] = ldexpf(rstd, -k);
   }
-  auto value = [&](int64_t c) {
-    const float xn = (at(c) - mean) * rstd;
-    return xn * (a.gamma != nullptr ? a.gamma[c] : 1.f) + (a.beta != nullptr ? a.beta[c] : 0.f);
-  };
-  if (a.codes == nullptr) {
-    if (a.y == nullptr) return;
-    for (int64_t c = threadIdx.x; c < a.C; c += kLong) store1<BF16>(a.y, row0 + c, value(c));
-    return;
-  }
-  // blocks of 32, four lanes of eight neighbours each; a wave's lanes go on
-  // together, since the maximum of a block is taken across them
-  for (int64_t c0 = 0; c0 < a.C; c0 += 8 * kLong) {
-    const int64_t c = c0 + 8 * threadIdx.x;
-    float v[8];
+  auto write = [&](auto again) {
+    auto value = [&](int64_t c) {
+      const float xn = (at(c, again) - mean) * rstd;
+      return xn * (a.gamma != nullptr ? a.gamma[c] : 1.f) + (a.beta != nullptr ? a.beta[c] : 0.f);
+    };
+    if (a.codes == nullptr) {
+      if (a.y == nullptr) return;
+      for (int64_t c = threadIdx.x; c < a.C; c += kLong) store1<BF16>(a.y, row0 + c, value(c));
+      return;
+    }
+    // blocks of 32, four lanes of eight neighbours each; a wave's lanes go on
+    // together, since the maximum of a block is taken across them
+    for (int64_t c0 = 0; c0 < a.C; c0 += 8 * kLong) {
+      const int64_t c = c0 + 8 * threadIdx.x;
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c < a.C ? value(c + i) : 0.f;
-    if (c < a.C && a.y != nullptr) store8<BF16>(a.y, row0 + c, v);
-    put_codes(a.code, a.codes, a.scales, row0 + c, c < a.C, false, v);
-  }
+      for (int i = 0; i < 8; ++i) v[i] = c < a.C ? value(c + i) : 0.f;
+      if (c < a.C && a.y != nullptr) store8<BF16>(a.y, row0 + c, v);
+      put_codes(a.code, a.codes, a.scales, row0 + c, c < a.C, false, v);
+    }
+  };
+  if (k == 0) write(no);
+  else write(yes);
 }
 
 // --------------------------------------------------------------- backward --
