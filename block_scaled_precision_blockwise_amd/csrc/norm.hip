@@ -330,11 +330,14 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
   }
 }
 
-// Any length: a workgroup reads its row three times.
+// Any length: a workgroup reads its row three times.  A thread's share of a sum
+// is long, so the mean is summed from the row's first value on, and mended by
+// that of x - mean, which the second pass brings: rows far from zero are as good
+// as others at any length, and a row of one value is zeros.
 constexpr int kLong = 1024;
 template <int BF16>
 __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first) {
-  __shared__ float red[5][kLong / 64];
+  __shared__ float red[3][kLong / 64], pairs[2][2 * kLong / 64];
   const int64_t r = first + blockIdx.x, row0 = r * a.C;
   saturate_fp8();
   // `again`: the row is taken times 2^-k
@@ -348,19 +351,27 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
   };
   float mean = 0.f;
   auto variance = [&](float* red_mean, float* red_var, auto again) {
-    float s = 0.f;
-    if (!a.rms) {
-      for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += at(c, again);
-      mean = sum_over<kLong>(s, red_mean) / float(a.C);
-      s = 0.f;
+    float s = 0.f, left = 0.f;
+    if (a.rms) {
+      for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += at(c, again) * at(c, again);
+      return sum_over<kLong>(s, red_var) / float(a.C);
     }
+    const float x0 = at(0, again);
+    for (int64_t c = threadIdx.x; c < a.C; c += kLong) s += at(c, again) - x0;
+    mean = x0 + sum_over<kLong>(s, red_mean) / float(a.C);
+    s = 0.f;
     for (int64_t c = threadIdx.x; c < a.C; c += kLong) {
       const float d = at(c, again) - mean;
+      left += d;
       s += d * d;
     }
-    return sum_over<kLong>(s, red_var) / float(a.C);
+    sum_over<kLong>(s, left, red_var);
+    left /= float(a.C);
+    mean += left;
+    const float v = s / float(a.C) - left * left;
+    return v < 0.f ? 0.f : v;
   };
-  const float var = variance(red[0], red[3], no);
+  const float var = variance(red[0], pairs[0], no);
   float rstd = 1.0f / sqrtf(var + a.eps);
   if (!held(var + a.eps)) {
     uint32_t top = 0u;
@@ -370,7 +381,7 @@ __global__ void __launch_bounds__(kLong) k_norm_long(NormLaunch a, int64_t first
     if (top < kInfinity) {
       k = exponent_of(top, a.eps);
       down = ldexpf(1.f, -k);
-      const float scaled = variance(red[2], red[4], yes), most = __uint_as_float(top) * down;
+      const float scaled = variance(red[2], pairs[1], yes), most = __uint_as_float(top) * down;
       mean = __builtin_amdgcn_fmed3f(mean, -most, most);  // so that 2^k times it is finite
       rstd = rstd_again(scaled, a.eps, mean, k);
     }

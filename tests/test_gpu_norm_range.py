@@ -157,3 +157,33 @@ def test_gradients_of_rows_whose_differences_pass_float32(C, dt, rms):
     # sums over the rows: up to R of a group, 16 shares and their joining
     held(dg, wg, (np.abs(dy) * t_xn).sum(0) + (R + 35) * U * np.abs(dy * xn).sum(0), f32, "dgamma")
     held(db, wb, (R + 34) * U * np.abs(dy).sum(0), f32, "dbeta")
+
+
+# --------------------------------------------------------------- long rows --
+
+@pytest.mark.parametrize("dt", [f32, bf16])
+@pytest.mark.parametrize("C", [16385, 300001, (1 << 22) + 32])
+def test_long_rows_far_from_zero(C, dt):
+    """The mean is that of the row to its own rounding and to those of sums of x - mean, however many values there are:
+    a row of one value is zeros."""
+    say("norm of long rows far from zero", C, dt)
+    g = np.random.default_rng(C)
+    x = np.stack([np.full(C, 1000.1), np.full(C, -0.3), 1000.0 + g.standard_normal(C), 20.0 + 1e-3 * g.standard_normal(C)])
+    x = torch.from_numpy(x).to(dt).double().numpy()
+    y, mean, rstd = empty(4, C, dtype=f32), empty(4, dtype=f32), empty(4, dtype=f32)
+    bsq.bsq_norm_mx(torch.from_numpy(x).to("cuda", f32), y=y, mean=mean, rstd=rstd)
+    want, m, r = norm.forward(x, eps=float(np.float32(1e-5)))
+    n = roundings(C)
+    d = np.abs(x - m[:, None])
+    t_first = (n + 1) * U * np.abs(x).mean(1)  # of the first mean, from which the second's differences are taken
+    t_mean = U * np.abs(m) + (n + 4) * U * (d.mean(1) + t_first)
+    assert np.all(np.abs(mean.double().cpu().numpy() - m) <= t_mean), np.abs(mean.double().cpu().numpy() - m) / t_mean
+    # the variance: sums of (x - first mean)^2, less the square of what that is off
+    var = (d * d).mean(1) + 1e-5
+    t_d = U * (d + t_first[:, None])
+    t_var = ((2 * d * t_d + t_d * t_d).mean(1) + 2 * (n + 6) * U * ((d * d).mean(1) + t_first ** 2) +
+             2 * t_first * (n + 4) * U * (d.mean(1) + t_first) + 4 * U * var)
+    rel = 0.5 * t_var / var * (1 + 2 * t_var / var) + 3 * U
+    assert np.all(np.abs(rstd.double().cpu().numpy() - r) <= r * rel)
+    t_y = (r * t_mean)[:, None] * (1 + rel[:, None]) + np.abs(want) * (rel[:, None] + 4 * U)
+    assert np.all(np.abs(y.double().cpu().numpy() - want) <= t_y * 1.01)
