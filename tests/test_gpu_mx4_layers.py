@@ -1,11 +1,13 @@
-"""Steps of layers in 4 bits that tests/test_gpu_mx4_use.py does not take: streams that are named."""
+"""Steps of layers in 4 bits that tests/test_gpu_mx4_use.py does not take: streams that are named, scales at both ends
+of their range, the experts' backward pass, nvfp4 operands value by value."""
 import pytest
 import torch
 
 import block_scaled_precision_blockwise_amd as bsq
 from gpu_helpers import say
-from test_gpu_mx4 import E8M0, empty, exact_operand, u8
-from test_gpu_mx4_use import randn
+from mx4_sizes import DENSE
+from test_gpu_mx4 import E4M3, E8M0, TABLE, decode, dense, empty, exact_operand, experts_reference, ragged, u8
+from test_gpu_mx4_use import quant, randn
 
 pytestmark = pytest.mark.gpu
 f32, bf16 = torch.float32, torch.bfloat16
@@ -60,3 +62,94 @@ def test_a_named_stream_is_the_one_that_is_used():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(g.view(u8), w.view(u8)), name
+
+
+# --------------------------------------------------------- scales far apart --
+
+@pytest.mark.parametrize("kind", ["e2m1", "e4m3", "e5m2"])
+@pytest.mark.parametrize("tile", [t for t in DENSE if t != "t256x256 batch"])
+def test_scales_at_the_ends_of_their_range_cancel(tile, kind):
+    """A's scales of 2^-119 under B's of 2^119, and the other way, give the product under scales of 1."""
+    B, M, N, _ = DENSE[tile]
+    K = 288
+    a, sa = exact_operand((B, M, K), kind, 1)
+    b, sb = exact_operand((B, N, K), "e2m1", 2)
+    want = dense(a, sa, b, sb, f32)
+    for by in (-119, 119):
+        say("scales far apart", tile, kind, by)
+        up, down = (sa.view(u8).int() + by).to(u8).view(E8M0), (sb.view(u8).int() - by).to(u8).view(E8M0)
+        assert torch.equal(dense(a, up, b, down, f32), want)
+
+
+# ------------------------------------------------------------------ experts --
+
+@pytest.mark.parametrize("align", [1, 32])
+@pytest.mark.parametrize("gathers", [False, True])
+@pytest.mark.parametrize("code", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("counts, F, H", [([30, 0, 70, 1, 44], 160, 96), ([300, 0, 433, 157, 250, 1, 240], 544, 1056)])
+def test_the_experts_input_gradient(counts, F, H, code, gathers, align):
+    """dX of each row is its dY times its expert's weights: the product of the transposed operand that the quantizer
+    writes, contracting the weights' rows; from rows in their order, or from each token's dY."""
+    E, k = len(counts), 2
+    say("experts' input gradient", counts, F, H, code, gathers, align)
+    cap = sum(n + -n % align for n in counts) + 5
+    T = cap if not gathers else 61
+    offsets, rows = ragged(counts, T, k, align, 3)
+    w, dy = randn(E, F, H, seed=1, dtype=bf16) * H ** -0.5, randn(T, F, seed=2)
+    (_, _), (wt, wts) = quant(w)  # codes_t [E, H, F / 2]
+    if code == "e2m1":
+        g, gs = quant(dy, both=False)
+    else:
+        g, gs = empty(T, F, dtype=E4M3), empty(T, F // 32, dtype=E8M0)
+        bsq.bsq_quant_mx(dy, g, gs, 1, bsq.BSQ_E4M3)
+    dx = empty(cap, H, dtype=f32)
+    bsq.bsq_moe_matmul_mxfp4(g, gs, wt, wts, offsets, dx, rows=rows if gathers else None, k=k if gathers else 1)
+    if not gathers:
+        rows = None
+    args = (offsets, rows, cap, k if gathers else 1)
+    want = experts_reference(g, gs, wt, wts, *args)
+    # sums of F products and, of 8-bit codes, the 13 bits that they are cut to: by the sums of magnitudes
+    size = experts_reference(g.float().abs().to(E4M3) if code != "e2m1" else g & 0x77, gs, wt & 0x77, wts, *args)
+    tol = ((F / 8 + F / 32 + 4) * 2.0 ** -23 + (7 * 2.0 ** -13 if code != "e2m1" else 0.0)) * size
+    assert bool(((dx.double() - want).abs() <= tol).all())
+    # what the codes stand for is the transposed weights, each to half a step (see the linear layer's test)
+    v = w.transpose(1, 2).double()
+    scale = torch.exp2(wts.view(u8).double() - 127).repeat_interleave(32, -1)
+    assert bool(((decode(wt, wts) - v).abs() <= torch.maximum(v.abs() / 4, scale / 4)).all())
+    # and the rows' gradient is that of sum(out c) by differences of the forward's sum, which is linear in x
+    if not gathers:
+        at = offsets[1] - 1  # a row of the first expert
+        step = torch.randn(H, device="cuda", dtype=torch.float64)
+        fwd = lambda x: float((decode(g, gs)[at] * (decode(wt[0], wts[0]).t() @ x)).sum())  # noqa: E731
+        diff = fwd(step) - fwd(-step)
+        got = 2 * float((dx[at].double() * step).sum())
+        assert abs(diff - got) <= 2 * float((tol[at] * step.abs()).sum()) + 1e-9 * abs(diff)
+
+
+# ------------------------------------------------------------------- nvfp4 --
+
+@pytest.mark.parametrize("M, N, K", [(1, 64, 256), (48, 64, 256), (130, 272, 640)])
+def test_nvfp4_operands_and_their_product_value_by_value(M, N, K):
+    """Each code stands for its value to half a step, and the product is that of what the codes stand for."""
+    say("nvfp4 value by value", M, N, K)
+    ops = []
+    for shape, seed in (((1, M, K), 1), ((1, N, K), 2)):
+        t = randn(*shape, seed=seed) * 0.01
+        f = 6 * 448 / t.abs().max().reshape(1)
+        q, s = empty(1, shape[1], K // 2), empty(1, shape[1], K // 16, dtype=E4M3)
+        bsq.bsq_quant_fp4(t, q, s, format=bsq.BSQ_NVFP4, factor=f)
+        c = torch.stack([q & 15, q >> 4], -1).flatten(-2).long()
+        v = TABLE.cuda().double()[c & 7]
+        scale = s.double().repeat_interleave(16, -1)
+        v = torch.where(c > 7, -v, v) * scale
+        y = (t * f).double()
+        # half a step is a fifth of the value at most (1 at 5, 0.25 at 1.25), or a quarter of the scale; the scale, a
+        # sixth of the largest, is rounded by 2^-4, by which the largest may pass 6
+        assert bool(((v - y).abs() <= torch.maximum(y.abs() / 5, scale / 4) * (1 + 2.0 ** -20)).all())
+        ops.append((q, s, v[0]))
+    (qa, sa, a), (qb, sb, b) = ops
+    out = empty(1, M, N, dtype=f32)
+    bsq.bsq_scaled_matmul_nvfp4(qa, qb, sa, sb, out, empty(bsq.bsq_nvfp4_workspace_bytes(1, M, N, K)))
+    # a code times its scale has 6 bits: exact in the product's operands; K roundings of its float32 sums
+    err = (out[0].double() - a @ b.t()).abs()
+    assert bool((err <= K * 2.0 ** -23 * (a.abs() @ b.abs().t())).all())
