@@ -33,9 +33,12 @@ auto in_parts(int64_t n, int64_t most, F&& f) -> decltype(f(n, n)) {
   return s;
 }
 
-// Rows that the products' arrays may have: 64 lanes with `limit` tiles each
-// stay below 2^32.
-constexpr int64_t kMaxRows = 0x7FFFFFFF - 0xFFFF;
+// Rows that tiles of tm may be cut from, of up to 1024 segments: 64 lanes with
+// `limit` tiles each stay below 2^32.
+constexpr int64_t rows_counted(int64_t tm) { return (tm << 26) - 2048 * tm; }
+// Rows that the products' arrays may have.  Tiles of 16 rows are for fewer, which
+// the choice of tile sees to (mx4_tile).
+constexpr int64_t kMaxRows = rows_counted(32);
 
 // Whether row r of a tile whose first row is row0 is before `end`.
 BSQ_INDEX bool row_in(int row0, int r, int end) { return r < end - row0; }
@@ -52,8 +55,9 @@ struct Segment {
 };
 
 // The segments [offsets[i], offsets[i + 1]) of i = 0 .. E - 1, and as segment E
-// the rows past the last, each cut into tiles of TM (32 or more) rows from its
-// first row.  A wave's lane l has c segments from l c on.
+// the rows past the last, each cut into tiles of TM rows from its first row, of
+// at most rows_counted(TM) rows in all.  A wave's lane l has c segments from l c
+// on.
 template <int TM>
 struct Segments {
   const int32_t* offsets;

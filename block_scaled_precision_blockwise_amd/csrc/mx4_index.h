@@ -27,14 +27,19 @@ struct Mx4Size {
   }
 };
 
+// Tiles of 16 x 16 up to which the kernels for few rows are taken.  No more rows
+// than rows_counted(16) have as few.
+constexpr int64_t kFewLaunched = 16 * kCUs;
+static_assert(16 * kFewLaunched <= rows_counted(16), "a wave counts tiles in 32 bits");
+
 inline Mx4Tile mx4_tile(const Mx4Size& s) {
   // Few tiles: the smallest of which no CU gets two.  Straight from memory to
   // registers, us against 32 x 64 tiles of two groups at (rows, N, K): 16 x 16
   // (1, 4096, 4096) 4.0 / 6.6, (128, 256, 4096) 4.8 / 6.6; 16 x 32 (1, 8192,
   // 4096) 5.8 / 6.7, (64, 2048, 4096) 5.9 / 6.8; 32 x 32 (64, 4096, 2048) 5.5 /
   // 6.2, (64, 4096, 4096) 7.2 / 7.0.  Not where many workgroups start for
-  // nothing.
-  if (s.launched(16, 16) <= 16 * kCUs) {
+  // nothing, which also bounds the rows that their tiles of 16 are counted from.
+  if (s.launched(16, 16) <= kFewLaunched) {
     if (s.tiles(16, 16) <= kCUs) return Mx4Tile::few16x16;
     if (s.tiles(16, 32) <= kCUs) return Mx4Tile::few16x32;
     if (s.tiles(32, 32) <= kCUs && s.K <= 2048) return Mx4Tile::few32x32;
