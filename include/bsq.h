@@ -512,8 +512,9 @@ bsq_status bsq_quant_fp4(int64_t B, int64_t rows, int64_t cols, const void* src,
  * the matrix core.
  *   lhs [B, M, K / 2] (lhs_dtype BSQ_E2M1) or [B, M, K] (BSQ_E4M3, BSQ_E5M2)
  *   rhs [B, N, K / 2], BSQ_E2M1
- *   lhs_scales [B, M, K / 32], rhs_scales [B, N, K / 32], E8M0; read in whole
- *       aligned words, so that up to 3 bytes behind the last are looked at
+ *   lhs_scales [B, M, K / 32], rhs_scales [B, N, K / 32], E8M0, 4-byte aligned;
+ *       read in whole aligned words, so that up to 3 bytes behind the last are
+ *       looked at (and have no effect)
  *   out [B, M, N] of out_dtype (BSQ_F32 or BSQ_BF16)
  * The gradients are the same call with the transposed operands that
  * bsq_quant_fp4 writes: dX = dY W with rhs = W's codes_t, dW = dY^T X with lhs
@@ -530,6 +531,7 @@ bsq_status bsq_scaled_matmul_mxfp4(int64_t B, int64_t M, int64_t N, int64_t K, c
  *   a [T, K / 2] (a_dtype BSQ_E2M1) or [T, K] (BSQ_E4M3, BSQ_E5M2), a_scales
  *       [T, K / 32]
  *   b [E, N, K / 2], BSQ_E2M1, b_scales [E, N, K / 32]
+ *   a_scales and b_scales are 4-byte aligned and read in whole aligned words
  *   offsets int32 [E + 1] (any row numbers, also unaligned), rows int32 [cap]
  *   out [cap, N] of out_dtype (BSQ_F32 or BSQ_BF16)
  * Rules: K % 32 == 0 (else SHAPE); N % 16 == 0, T <= 2^30, T K / 32 and N K /

@@ -81,6 +81,31 @@ def test_scales_at_the_ends_of_their_range_cancel(tile, kind):
         assert torch.equal(dense(a, up, b, down, f32), want)
 
 
+@pytest.mark.parametrize("tile", [t for t in DENSE if t != "t256x256 batch"])
+def test_what_lies_behind_the_scales_has_no_effect(tile):
+    """Scales that end inside a word, between NaN scales: of the dense call and of the experts'."""
+    B, M, N, _ = DENSE[tile]
+    M += 1 - M % 2  # odd, for 3 scales to a row
+    K = 96
+    a, sa = exact_operand((B, M, K), "e4m3", 1)
+    b, sb = exact_operand((B, N, K), "e2m1", 2)
+    around = []
+    for s in (sa, sb):
+        whole = empty(s.numel() + 128, fill=0xFF)
+        whole[64:64 + s.numel()] = s.view(u8).reshape(-1)
+        around.append(whole[64:64 + s.numel()].view(s.shape).view(E8M0))
+    say("scales between others", tile)
+    assert torch.equal(dense(a, around[0], b, around[1], f32), dense(a, sa, b, sb, f32))
+    T = B * M  # the same rows as segments of the batch's weights
+    offsets = torch.arange(0, T + 1, M, dtype=torch.int32, device="cuda")
+    outs = []
+    for x, y in ((sa, sb), around):
+        out = empty(T, N, dtype=f32)
+        bsq.bsq_moe_matmul_mxfp4(a.view(T, K), x.reshape(T, K // 32), b, y, offsets, out)
+        outs.append(out)
+    assert torch.equal(*outs) and torch.equal(outs[0].view(B, M, N), dense(a, sa, b, sb, f32))
+
+
 # ------------------------------------------------------------------ experts --
 
 @pytest.mark.parametrize("align", [1, 32])
