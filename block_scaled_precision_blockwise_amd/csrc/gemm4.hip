@@ -45,7 +45,7 @@ struct Mx4Args {
 };
 
 // What a workgroup computes: output rows [m0, m_end) and columns from n0 of
-// expert (or product) e.  `last`: no such expert, rows past the last segment.
+// expert (or product) e.  `none`: no such expert, rows past the last segment.
 struct Place4 {
   int e, m0, m_end, n0;
   bool none;
@@ -146,12 +146,14 @@ __device__ __forceinline__ void store4(const Mx4Args& p, int64_t at, v4f v) {
 // Tiles of 16 MB rows x 16 NB columns, where the weights' bytes are most of the
 // work.  W waves share a tile's contraction, each with U chunks of 128 at a
 // time, straight from memory to the operand registers, and their sums are
-// joined through LDS in the waves' order.  U is 8 where every wave has as many
-// (1 x 4096 x 14336 9.2 us / 10.8 with 4, x 4096 4.9 / 5.1), else 4 (8 x 2048 x
-// 416 3.0 / 3.2, 1 x 8192 x 2880 5.8 / 6.0).  Bound by the latency of a launch and
-// of memory: one row of 8192 x 4096 5.6 us (17.8 MB, 3.2 TB/s), of 4096 x 4096
-// 4.0 us.  Tiles of 64 x 64 this way are slower than through LDS (1024 x 1024 x
-// 16384 40 us / 22): a load's 16 rows of 64 bytes are half lines.
+// joined through LDS in the waves' order.  U is 8 where every wave has as many,
+// else 4.  Kernels in a replayed graph, weights from memory: 1 x 4096 x 14336 9.0
+// us with 8, 10.5 with 4, x 4096 4.7 / 5.0; with less of the contraction to a
+// wave (timed with 8 first) 8 x 2048 x 416 3.2 / 3.0, 1 x 8192 x 2880 6.0 / 5.8.
+// Bound by the latency of a launch and of memory: one row of 8192 x 4096 6.1 us
+// (17.8 MB, 2.9 TB/s), of 4096 x 4096 4.7 us, with weights that the caches hold
+// 5.3 and 4.0.  Tiles of 64 x 64 this way are slower than through LDS (1024 x
+// 1024 x 16384 40 us / 22): a load's 16 rows of 64 bytes are half lines.
 template <int FA, int MB, int NB, int W, int U>
 __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
   constexpr int TM = 16 * MB, TN = 16 * NB;
@@ -297,8 +299,8 @@ __global__ void __launch_bounds__(64 * W) k_mx4_few(Mx4Args p) {
 // Measured: 1021 x 1792 x 2880, 8-bit A, 13.6 us (64 x 128, two groups); 1024 x
 // 1024 x 16384 in 4 bits 21 us (64 x 64, two groups; one group 29), 600 ns for
 // 512 of the contraction: more stages (3 to 5) or parts (1, 2) are within 0.5
-// us of that, waves of 64 x 32 23.  64 rows x 4096 x 4096 6.6 us (32 x 64, two
-// groups, two parts; one part 7.2).  8 tokens over 32 experts, N 4096, K 2048:
+// us of that, waves of 64 x 32 23.  64 rows x 4096 x 4096, held by the caches, 6.6
+// us (32 x 64, two groups, two parts; one part 7.2), from memory 9.4.  8 tokens over 32 experts, N 4096, K 2048:
 // 17 us, 5.3 TB/s (32 x 64).
 template <int FA, int WM, int WN, int MB, int NB, int S, int KG, int U, int AL>
 __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
@@ -574,8 +576,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 1) k_mx4_tile(Mx4Args p) {
 // of the offsets in LDS, so that it waits for no load.
 //
 // Measured: 16384 x 8192 x 4096 in 4 bits 263 us, 4.2 PFLOP/s; 65536 rows over
-// 32 experts, N 4096, K 2048, 360 us, 3.1.  Pure MFMAs on random codes reach 6.9
-// PFLOP/s (9.0 on zeros: the clock gives way).  Of the 263 us the loads are 32,
+// 32 experts, N 4096, K 2048, 360 us, 3.1; 8192 x 4096 x 4096 with e4m3 106 us,
+// 2.6.  Pure MFMAs on random codes reach 6.6-6.9 PFLOP/s (9.0 on zeros: the clock
+// gives way), e2m1 times e4m3 4.3 (4.9).  Of the 263 us the loads are 32,
 // the stores 30, the LDS reads 10; two wait states in front of every MFMA and of
 // every load's m0 were 25 more.
 

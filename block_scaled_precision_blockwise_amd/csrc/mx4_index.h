@@ -34,17 +34,19 @@ static_assert(16 * kFewLaunched <= rows_counted(16), "a wave counts tiles in 32 
 
 inline Mx4Tile mx4_tile(const Mx4Size& s) {
   // Few tiles: the smallest of which no CU gets two.  Straight from memory to
-  // registers, us against 32 x 64 tiles of two groups at (rows, N, K): 16 x 16
-  // (1, 4096, 4096) 4.0 / 6.6, (128, 256, 4096) 4.8 / 6.6; 16 x 32 (1, 8192,
-  // 4096) 5.8 / 6.7, (64, 2048, 4096) 5.9 / 6.8; 32 x 32 (64, 4096, 2048) 5.5 /
-  // 6.2, (64, 4096, 4096) 7.2 / 7.0.  Not where many workgroups start for
+  // registers, us of kernels in a replayed graph, weights from memory, against 32
+  // x 64 tiles of two groups at (rows, N, K): 16 x 16 (1, 4096, 4096) 4.7 / 8.4,
+  // (128, 256, 4096) 4.9 / 6.9; 16 x 32 (1, 8192, 4096) 6.1 / 8.8, (64, 2048,
+  // 4096) 6.3 / 8.8; 32 x 32 (64, 4096, 2048) 5.2 / 5.9, and with weights that the
+  // caches hold (64, 4096, 4096) 7.2 / 7.0.  Not where many workgroups start for
   // nothing, which also bounds the rows that their tiles of 16 are counted from.
   if (s.launched(16, 16) <= kFewLaunched) {
     if (s.tiles(16, 16) <= kCUs) return Mx4Tile::few16x16;
     if (s.tiles(16, 32) <= kCUs) return Mx4Tile::few16x32;
     if (s.tiles(32, 32) <= kCUs && s.K <= 2048) return Mx4Tile::few32x32;
   }
-  // two groups of waves share a tile's contraction: 32 x 64 against one group
+  // two groups of waves share a tile's contraction, inputs held by the caches: 32
+  // x 64 against one group
   // (128, 4096, 4096) 7.2 / 8.6, 64 x 64 (1024, 1024, 16384) 22 / 29, 64 x 128
   // (1021, 1792, 2880) 13.8 / 17.8
   if (s.tiles(32, 64) <= kCUs) return Mx4Tile::t32x64g2;

@@ -12,8 +12,9 @@
 // the power of two that brings its largest value below 1.  Codes are of the
 // float32 y, before y's own rounding.
 //
-// Bound by memory.  A row stays in the registers of NT threads, P times eight
-// values each; rows too long for that are read again instead.  The weights'
+// Bound by memory where a row has enough values to fill its threads.  A row stays
+// in the registers of NT threads, P times eight values each; rows too long for
+// that are read again instead.  The weights'
 // gradients are summed by groups of rows in registers, a group's sums go to the
 // workspace, and a second kernel adds the groups in their order, so that every
 // run gives the same bytes.
@@ -235,8 +236,10 @@ __device__ __forceinline__ void put_codes(NormCode code, uint8_t* codes, uint8_t
 // ---------------------------------------------------------------- forward --
 // Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
 // gamma and beta in registers, the next one's load under way.  16384 x 4096
-// bfloat16 to bfloat16 and e4m3 61-69 us, 5.0-5.5 TB/s (a copy reaches 5.1);
-// one row 2.7 us.
+// bfloat16 to bfloat16 and e4m3 58-69 us, 5.0-5.8 TB/s (a copy reaches 5.1), to
+// bfloat16 and e2m1 50, to e2m1 alone 45; one row 2.7 us.  Rows that leave lanes
+// idle are bound by their instructions: 524288 x 128 155 us, 1.7 TB/s, 262144 x 64
+// 70 us, 1.0.
 template <int BF16, int VEC, int NT, int P>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormLaunch a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;  // of a workgroup
@@ -428,7 +431,10 @@ struct Centre {
 // Workgroups go through the rows blockIdx.x + gridDim.x i (of kRows rows each),
 // the next one's loads under way while a row is summed and written.  Two rows
 // of 256 threads to a workgroup halve the groups' sums: 16384 x 4096 71 + 5 us
-// against 73 + 7, 5.9 TB/s.
+// against 73 + 7, 5.9 TB/s.  Rows of 8193 and more have 1024 threads, whose 128
+// registers do not hold two rows under way, gamma and both sums: some are spilled
+// in the loop (11 of bfloat16, 82 of float32, 97 of single values), 4096 x 16384
+// bfloat16 116 us, 3.5 TB/s, float32 331 us, 2.4.
 template <int NT>
 constexpr int rows_of = NT < 256 ? 256 / NT : NT == 256 ? 2 : 1;
 template <int BF16, int VEC, int NT, int P>
