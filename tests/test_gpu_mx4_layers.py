@@ -38,30 +38,31 @@ def calls():
 
 
 def test_a_named_stream_is_the_one_that_is_used():
-    """The outputs are there when the named stream is done, while the current stream has yet to come through the work
-    that was put on it before the call."""
-    busy, named = torch.cuda.Stream(), torch.cuda.Stream()
-    big = torch.zeros(1 << 28, device="cuda")
+    """A named stream that is being captured takes the call into its graph, whatever the current stream: nothing is written
+    until the graph is replayed.  (Streams may share a hardware queue, so that one held up may hold up the other.)"""
+    named, current = torch.cuda.Stream(), torch.cuda.Stream()
     for name, call, outs in calls():
         say("named stream", name)
         call(None)
+        torch.cuda.synchronize()
         want = [t.clone() for t in outs]
+        untouched = lambda: all(bool((t.view(u8) == 0xFF).all()) for t in outs)  # noqa: E731
         for t in outs:
             t.view(u8).fill_(0xFF)  # NaN in every type
         torch.cuda.synchronize()
-        with torch.cuda.stream(busy):
-            for _ in range(500):  # 2 GiB of traffic each, 200 ms in all
-                big.add_(1.0)
-            held_up = torch.cuda.Event()
-            held_up.record()
-            call(named)
-        with torch.cuda.stream(named):
-            got = [t.clone() for t in outs]
-        named.synchronize()
-        assert not held_up.query(), "the current stream was done first: nothing is shown"
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=named):
+            with torch.cuda.stream(current):
+                call(named)
         torch.cuda.synchronize()
-        for g, w in zip(got, want):
-            assert torch.equal(g.view(u8), w.view(u8)), name
+        assert untouched(), name
+        for _ in range(2):
+            g.replay()
+            torch.cuda.synchronize()
+            for got, w in zip(outs, want):
+                assert torch.equal(got.view(u8), w.view(u8)), name
+            for t in outs:
+                t.view(u8).fill_(0xFF)
 
 
 # --------------------------------------------------------- scales far apart --
