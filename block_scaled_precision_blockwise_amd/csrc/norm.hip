@@ -82,7 +82,8 @@ __device__ __forceinline__ void sum_over(float& a, float& b, float* red) {
 constexpr uint32_t kInfinity = 0x7F800000u;
 // Whether float32 held the sums of a row, by its variance and eps (the same in
 // every lane): they are finite, and the squares (each off by 2^-150 at most) are
-// not lost beside them.
+// not lost beside them.  500000 x 128 bfloat16 rms 118 us, 114 without the check;
+// from 512 columns on the same.
 __device__ __forceinline__ bool held(float v) {
   constexpr uint32_t kLeast = 0x0D800000u;  // 2^-100
   return __builtin_expect(uint32_t(__builtin_amdgcn_readfirstlane(int(__float_as_uint(v)))) - kLeast < kInfinity - kLeast, 1);
